@@ -4,7 +4,9 @@ N logical ranks are N buffers in one GPU's HBM.  The collectives and schedules
 (Ring / Recursive Halving-Doubling / Double Binary Tree AllReduce, Ring
 ReduceScatter and AllGather, binomial Broadcast and Scatter, Pairwise and
 Bruck AllToAll, and a fused one-pass form of each) run in hand-written sm_103a
-CUDA kernels behind the C ABI of ``include/vc.h``; this package is the thin
+CUDA kernels behind the C ABI of ``include/vc.h``, and so do the layer
+operators next to them (a norm fused with its ReduceScatter, routing to
+experts, the exchange of tokens between ranks); this package is the thin
 Python binding over it.
 """
 from .binding import (  # noqa: F401
@@ -12,6 +14,7 @@ from .binding import (  # noqa: F401
     COLLS,
     DTYPES,
     LIB_PATH,
+    SCORES,
     VCError,
     lib,
     vc_allgather,
@@ -27,6 +30,14 @@ from .binding import (  # noqa: F401
     vc_plan_exec_order,
     vc_plan_form,
     vc_reduce_scatter,
+    vc_reduce_scatter_norm,
+    vc_reduce_scatter_norm_backward,
+    vc_route,
+    vc_route_backward,
+    vc_dispatch_plan,
+    vc_dispatch,
+    vc_combine,
+    vc_combine_backward,
     vc_scatter,
     vc_select_algo,
     vc_set_cost_model,

@@ -22,7 +22,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libvcoll.so")
 
 VC_SUCCESS, VC_ERR_INVALID_ARG, VC_ERR_UNSUPPORTED, VC_ERR_CUDA, VC_ERR_NOMEM, VC_ERR_TIMEOUT = range(6)
-DTYPES = {"f32": 0, "bf16": 1, "i32": 2, "f16": 3}
+DTYPES = {"f32": 0, "bf16": 1, "i32": 2, "f16": 3, "i8": 4}
 OPS = {"sum": 0, "max": 1, "min": 2}
 ALGOS = {"fused": 0, "ring": 1, "rhd": 2, "dbt": 3, "binomial": 4, "scatter_allgather": 5,
          "pairwise": 6, "bruck": 7, "auto": 8, "pipe_chain": 9, "pipe_tree": 10, "mesh": 11, "ring_hop": 12}
@@ -30,6 +30,7 @@ ALGO_NAMES = {v: k for k, v in ALGOS.items()}
 COST_POLICIES = {"hbm": 0, "link": 1}
 COLLS = {"allreduce": 0, "reduce_scatter": 1, "allgather": 2, "broadcast": 3, "scatter": 4,
          "alltoall": 5, "gather": 6, "reduce": 7}
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 class VCError(RuntimeError):
@@ -48,7 +49,13 @@ KERNEL_MODES = {0: "copy", 1: "f32", 2: "i32", 3: "bf16", 4: "bf16_pure", 5: "f1
 KERNEL_OPS = {0: "sum", 1: "max", 2: "min"}
 
 
+LAYER_KERNELS = ("norm", "norm_backward", "norm_weight", "route", "route_backward", "dispatch_plan", "dispatch",
+                 "combine", "combine_backward")
+
+
 def kernel_name(code: int) -> str:
+    if code & 512:  # a layer operator
+        return LAYER_KERNELS[code & 15]
     mode = KERNEL_MODES[code & 7]
     name = mode if mode == "copy" else f"{KERNEL_OPS[(code >> 3) & 3]}_{mode}"
     if code & 256:  # one launch over the whole GPU, each thread carrying its group through every step
@@ -65,6 +72,12 @@ class PlanEntry(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("reduce", ctypes.c_int32), ("byte_off", ctypes.c_int64),
                 ("n", ctypes.c_int64), ("nb", ctypes.c_int64), ("stride_bytes", ctypes.c_int64),
                 ("elem0", ctypes.c_int64)]
+
+
+class RouteHow(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("topk", ctypes.c_int), ("ngroups", ctypes.c_int),
+                ("topk_groups", ctypes.c_int), ("group_top", ctypes.c_int), ("renormalize", ctypes.c_int),
+                ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -89,6 +102,14 @@ def lib() -> ctypes.CDLL:
             "vc_broadcast_pipelined": [P, PP, I, Z, I, I, I, I, V],
             "vc_gather": [PP, P, I, Z, I, I, I, V],
             "vc_reduce": [PP, P, I, Z, I, I, I, I, V],
+            "vc_reduce_scatter_norm": [PP, PP, PP, PP, PP, PP, PP, I, Z, Z, ctypes.c_double, I, I, V],
+            "vc_reduce_scatter_norm_backward": [PP, PP, PP, PP, PP, PP, PP, PP, I, Z, Z, I, V],
+            "vc_route": [PP, PP, PP, PP, I, Z, I, ctypes.POINTER(RouteHow), I, V],
+            "vc_route_backward": [PP, PP, PP, PP, I, Z, I, ctypes.POINTER(RouteHow), I, V],
+            "vc_dispatch_plan": [PP, PP, PP, I, Z, I, I, Z, V],
+            "vc_dispatch": [PP, PP, PP, PP, PP, I, Z, Z, I, Z, I, V],
+            "vc_combine": [PP, PP, PP, PP, I, Z, Z, I, Z, I, V],
+            "vc_combine_backward": [PP, PP, PP, PP, PP, PP, I, Z, Z, I, Z, I, V],
         }.items():
             f = getattr(L, name)
             f.argtypes = args
@@ -320,6 +341,242 @@ def vc_reduce(send, recv_root, root=0, algo="fused", op="sum", stream=None) -> N
     sp, (rp,) = _checked(send, n, send[0]), _checked([recv_root], n, send[0])
     check(lib().vc_reduce(_ptr_array(sp), ctypes.c_void_p(rp), N, n, _dtype_code(send[0]), _code(OPS, op),
                           int(root), _code(ALGOS, algo), _stream_handle(stream, send[0])))
+
+
+# ---------------------------------------------------------------------------
+# layer operators
+# ---------------------------------------------------------------------------
+# Each per-rank argument is a sequence of one tensor per virtual rank, or one
+# contiguous tensor whose first dimension is the ranks (rank r's buffer is its
+# slice r).  Sizes come from the tensors' shapes.
+
+def _invalid(msg: str):
+    return VCError(VC_ERR_INVALID_ARG, msg)
+
+
+def _any(a):
+    """A tensor of a per-rank argument to take the dtype and device from."""
+    return a[0] if isinstance(a, (list, tuple)) else a
+
+
+def _per_rank(a, N: int, what: str, shape: tuple, dtype, dev: int, shared: bool = False):
+    """The pointer array of a per-rank argument (None stays None): each rank's
+    tensor contiguous, of `shape` and `dtype`, on device `dev`.  `shared`: one
+    tensor of `shape` may stand for every rank."""
+    if a is None:
+        return None
+    if not isinstance(a, (list, tuple)):
+        whole = (N, *shape)
+        same = shared and tuple(a.shape) == shape
+        if CHECK_TENSORS and ((tuple(a.shape) != whole and not same) or a.dtype is not dtype or a.get_device() != dev
+                              or not a.is_contiguous()):
+            raise _invalid(f"{what}: want contiguous {whole} {dtype} on cuda:{dev}, not {tuple(a.shape)} {a.dtype} "
+                           f"on {a.device}" + ("" if a.is_contiguous() else " (not contiguous)"))
+        p = a.data_ptr()
+        if same:
+            return _ptr_array([p] * N)
+        n = a.element_size()
+        for s in shape:
+            n *= s
+        return _ptr_array([p + r * n for r in range(N)])
+    if len(a) != N:
+        raise _invalid(f"{what}: {len(a)} tensors for {N} ranks")
+    if CHECK_TENSORS:
+        for x in a:
+            if tuple(x.shape) != shape or x.dtype is not dtype or x.get_device() != dev or not x.is_contiguous():
+                raise _invalid(f"{what}: want contiguous {shape} {dtype} on cuda:{dev}, not {tuple(x.shape)} {x.dtype} "
+                               f"on {x.device}" + ("" if x.is_contiguous() else " (not contiguous)"))
+    return _ptr_array([x.data_ptr() for x in a])
+
+
+def _device(t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise _invalid(f"tensors must be on a CUDA device, not {t.device}")
+    return dev
+
+
+def _dims(a, n: int, what: str) -> tuple:
+    """The shape of each rank's tensor of a per-rank argument."""
+    shape = tuple(a[0].shape) if isinstance(a, (list, tuple)) else tuple(a.shape[1:])
+    if len(shape) != n:
+        raise _invalid(f"{what}: want {n} dimensions for each rank, not {shape}")
+    return shape
+
+
+def _torch():
+    import torch
+
+    return torch
+
+
+def vc_reduce_scatter_norm(send, weight, out, residual=None, residual_out=None, scale=None, rstd=None,
+                           eps: float = 1e-6, stream=None) -> None:
+    """ReduceScatter of the ranks' partial sums, residual and RMS norm in one pass.
+
+    ``send[q]`` is (N * rows, hidden), ``out[r]`` (rows, hidden) in the data
+    type, or int8 with ``scale[r]`` (rows,) fp32.  ``weight`` is (hidden,) for
+    each rank or one for all.  ``residual[r]`` is added, the sum goes to
+    ``residual_out[r]`` (which may be the residual), 1/rms to ``rstd[r]``
+    (rows,) fp32."""
+    torch = _torch()
+    N, x = len(send), _any(send)
+    dev = _device(x)
+    rows, hidden = _dims(out, 2, "out")
+    dt, i8 = x.dtype, _any(out).dtype is torch.int8
+    row = (rows, hidden)
+    if i8 and scale is None:
+        raise _invalid("an int8 output wants a scale")
+    check(lib().vc_reduce_scatter_norm(
+        _per_rank(send, N, "send", (N * rows, hidden), dt, dev),
+        _per_rank(residual, N, "residual", row, dt, dev),
+        _per_rank(weight, N, "weight", (hidden,), dt, dev, shared=True),
+        _per_rank(residual_out, N, "residual_out", row, dt, dev),
+        _per_rank(out, N, "out", row, torch.int8 if i8 else dt, dev),
+        _per_rank(scale, N, "scale", (rows,), torch.float32, dev) if i8 else None,
+        _per_rank(rstd, N, "rstd", (rows,), torch.float32, dev),
+        N, rows, hidden, float(eps), _dtype_code(x), DTYPES["i8"] if i8 else _dtype_code(x),
+        _stream_handle(stream, x)))
+
+
+def vc_reduce_scatter_norm_backward(dout, h, weight, rstd, dsend=None, dresidual=None, dweight=None,
+                                    dresidual_out=None, stream=None) -> None:
+    """Gradients of vc_reduce_scatter_norm; ``h`` is its residual_out.
+
+    ``dsend[q]`` (N * rows, hidden), ``dresidual[r]`` (rows, hidden) and
+    ``dweight[r]`` (hidden,) fp32, this rank's part, are written where given;
+    ``dresidual_out`` is the gradient that reaches the sum itself."""
+    torch = _torch()
+    N, x = len(dout), _any(dout)
+    dev = _device(x)
+    rows, hidden = _dims(dout, 2, "dout")
+    dt, row = x.dtype, (rows, hidden)
+    check(lib().vc_reduce_scatter_norm_backward(
+        _per_rank(dout, N, "dout", row, dt, dev),
+        _per_rank(dresidual_out, N, "dresidual_out", row, dt, dev),
+        _per_rank(h, N, "h", row, dt, dev),
+        _per_rank(weight, N, "weight", (hidden,), dt, dev, shared=True),
+        _per_rank(rstd, N, "rstd", (rows,), torch.float32, dev),
+        _per_rank(dsend, N, "dsend", (N * rows, hidden), dt, dev),
+        _per_rank(dresidual, N, "dresidual", row, dt, dev),
+        _per_rank(dweight, N, "dweight", (hidden,), torch.float32, dev),
+        N, rows, hidden, _dtype_code(x), _stream_handle(stream, x)))
+
+
+def vc_route(logits, ids, weights, bias=None, score="softmax", ngroups: int = 1, topk_groups: int = 1,
+             group_top: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None) -> None:
+    """Choice of experts: ``ids[r]`` (rows, topk) int32 and ``weights[r]``
+    (rows, topk) fp32 from ``logits[r]`` (rows, experts).
+
+    ``bias`` is (experts,) fp32 for each rank or one for all."""
+    torch = _torch()
+    N, x = len(logits), _any(logits)
+    dev = _device(x)
+    rows, experts = _dims(logits, 2, "logits")
+    topk = _dims(ids, 2, "ids")[1]
+    how = RouteHow(_code(SCORES, score), topk, int(ngroups), int(topk_groups), int(group_top), int(bool(renormalize)),
+                   float(scale))
+    check(lib().vc_route(
+        _per_rank(logits, N, "logits", (rows, experts), x.dtype, dev),
+        _per_rank(bias, N, "bias", (experts,), torch.float32, dev, shared=True),
+        _per_rank(ids, N, "ids", (rows, topk), torch.int32, dev),
+        _per_rank(weights, N, "weights", (rows, topk), torch.float32, dev),
+        N, rows, experts, ctypes.byref(how), _dtype_code(x), _stream_handle(stream, x)))
+
+
+def vc_route_backward(dweights, logits, ids, dlogits, score="softmax", renormalize: bool = True, scale: float = 1.0,
+                      stream=None) -> None:
+    """``dlogits[r]`` (rows, experts) from ``dweights[r]`` (rows, topk) fp32,
+    with vc_route's logits and ids."""
+    torch = _torch()
+    N, x = len(logits), _any(logits)
+    dev = _device(x)
+    rows, experts = _dims(logits, 2, "logits")
+    topk = _dims(ids, 2, "ids")[1]
+    how = RouteHow(_code(SCORES, score), topk, 1, 1, 1, int(bool(renormalize)), float(scale))
+    check(lib().vc_route_backward(
+        _per_rank(dweights, N, "dweights", (rows, topk), torch.float32, dev),
+        _per_rank(logits, N, "logits", (rows, experts), x.dtype, dev),
+        _per_rank(ids, N, "ids", (rows, topk), torch.int32, dev),
+        _per_rank(dlogits, N, "dlogits", (rows, experts), x.dtype, dev),
+        N, rows, experts, ctypes.byref(how), _dtype_code(x), _stream_handle(stream, x)))
+
+
+def vc_dispatch_plan(ids, slots, offsets, capacity: int, stream=None) -> None:
+    """Where every (token, choice) goes: ``slots[r]`` (rows, topk) int32, and
+    ``offsets[d]`` (experts of a rank + 1,) int32, where rank d's experts'
+    rows begin, from ``ids[r]`` (rows, topk) int32.  ``capacity`` rows a rank
+    at most."""
+    torch = _torch()
+    N, x = len(ids), _any(ids)
+    dev = _device(x)
+    rows, topk = _dims(ids, 2, "ids")
+    each = _dims(offsets, 1, "offsets")[0] - 1
+    if capacity < 1:
+        raise _invalid("capacity must be at least 1")
+    check(lib().vc_dispatch_plan(
+        _per_rank(ids, N, "ids", (rows, topk), torch.int32, dev),
+        _per_rank(slots, N, "slots", (rows, topk), torch.int32, dev),
+        _per_rank(offsets, N, "offsets", (each + 1,), torch.int32, dev),
+        N, rows, topk, each * N, int(capacity), _stream_handle(stream, x)))
+
+
+def vc_dispatch(send, slots, recv, scale=None, recv_scale=None, stream=None) -> None:
+    """``send[r]``'s rows (rows, hidden) to the slots' rows of ``recv[d]``
+    (capacity, hidden), and ``scale[r]`` (rows,) fp32 to ``recv_scale[d]``
+    (capacity,) where given.  fp32, bf16, fp16 or int8 rows."""
+    torch = _torch()
+    N, x = len(send), _any(send)
+    dev = _device(x)
+    rows, hidden = _dims(send, 2, "send")
+    topk, cap = _dims(slots, 2, "slots")[1], _dims(recv, 2, "recv")[0]
+    check(lib().vc_dispatch(
+        _per_rank(send, N, "send", (rows, hidden), x.dtype, dev),
+        _per_rank(scale, N, "scale", (rows,), torch.float32, dev),
+        _per_rank(slots, N, "slots", (rows, topk), torch.int32, dev),
+        _per_rank(recv, N, "recv", (cap, hidden), x.dtype, dev),
+        _per_rank(recv_scale, N, "recv_scale", (cap,), torch.float32, dev),
+        N, rows, hidden, topk, cap, DTYPES["i8"] if x.dtype is torch.int8 else _dtype_code(x),
+        _stream_handle(stream, x)))
+
+
+def vc_combine(recv, slots, out, weights=None, stream=None) -> None:
+    """``out[r]`` (rows, hidden): each token's rows of ``recv[d]`` (capacity,
+    hidden), weighted by ``weights[r]`` (rows, topk) fp32 (1 where None) and
+    summed.  With the gradient of recv and no weights: dispatch's gradient."""
+    torch = _torch()
+    N, x = len(out), _any(out)
+    dev = _device(x)
+    rows, hidden = _dims(out, 2, "out")
+    topk, cap = _dims(slots, 2, "slots")[1], _dims(recv, 2, "recv")[0]
+    check(lib().vc_combine(
+        _per_rank(recv, N, "recv", (cap, hidden), x.dtype, dev),
+        _per_rank(slots, N, "slots", (rows, topk), torch.int32, dev),
+        _per_rank(weights, N, "weights", (rows, topk), torch.float32, dev),
+        _per_rank(out, N, "out", (rows, hidden), x.dtype, dev),
+        N, rows, hidden, topk, cap, _dtype_code(x), _stream_handle(stream, x)))
+
+
+def vc_combine_backward(dout, recv, slots, weights=None, drecv=None, dweights=None, stream=None) -> None:
+    """Gradients of vc_combine: ``drecv[d]`` (capacity, hidden) and
+    ``dweights[r]`` (rows, topk) fp32, where given.  ``recv`` may be None
+    without dweights."""
+    torch = _torch()
+    N, x = len(dout), _any(dout)
+    dev = _device(x)
+    rows, hidden = _dims(dout, 2, "dout")
+    topk = _dims(slots, 2, "slots")[1]
+    if recv is None and drecv is None:
+        raise _invalid("no gradient is asked for")
+    cap = _dims(recv if recv is not None else drecv, 2, "recv")[0]
+    check(lib().vc_combine_backward(
+        _per_rank(dout, N, "dout", (rows, hidden), x.dtype, dev),
+        _per_rank(recv, N, "recv", (cap, hidden), x.dtype, dev),
+        _per_rank(slots, N, "slots", (rows, topk), torch.int32, dev),
+        _per_rank(weights, N, "weights", (rows, topk), torch.float32, dev),
+        _per_rank(drecv, N, "drecv", (cap, hidden), x.dtype, dev),
+        _per_rank(dweights, N, "dweights", (rows, topk), torch.float32, dev),
+        N, rows, hidden, topk, cap, _dtype_code(x), _stream_handle(stream, x)))
 
 
 def vc_busbw_factor(coll, nranks: int) -> float:

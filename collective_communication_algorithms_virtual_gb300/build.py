@@ -16,8 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libvcoll.so")
-SOURCES = ["plan.cpp", "vc.cu"]
-HEADERS = ["plan.h", "kernels.cuh", "slice.cuh"]
+SOURCES = ["plan.cpp", "vc.cu", "norm.cu", "route.cu", "exchange.cu"]
+HEADERS = ["plan.h", "host.h", "kernels.cuh", "slice.cuh", "layer.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

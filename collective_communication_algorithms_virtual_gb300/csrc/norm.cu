@@ -1,0 +1,562 @@
+// ReduceScatter + residual + RMS norm of the virtual ranks' partial sums, and
+// its gradient (see vc.h).
+//
+// Both stream: every input is read once and every output written once, and
+// the norm's mean is taken while the row is on chip.  A row of 16-byte
+// vectors is held in registers by one block, up to kMaxVec of them; any other
+// row (odd sizes, unaligned buffers, longer rows) in shared memory in fp32.
+#include "layer.cuh"
+
+namespace vc {
+namespace layer {
+namespace {
+
+constexpr int kThreads = 512;  // most threads of a block that holds a row in registers
+
+struct NormParams {
+  const void* send[VC_MAX_RANKS];
+  const void* residual[VC_MAX_RANKS];
+  const void* weight[VC_MAX_RANKS];
+  void* residual_out[VC_MAX_RANKS];
+  void* out[VC_MAX_RANKS];
+  float* scale[VC_MAX_RANKS];
+  float* rstd[VC_MAX_RANKS];
+  int nranks, has_residual, has_residual_out, has_rstd;
+  uint32_t rows;
+  int32_t hidden;
+  float eps;
+};
+
+// Quantiser of a row whose largest magnitude has the bits `top`: a factor in
+// two steps, since 127 / max overflows for the smallest rows.
+struct Quant {
+  float pre, inv, scale;
+  __device__ __forceinline__ explicit Quant(uint32_t top) {
+    const float most = __uint_as_float(top);
+    pre = most < 1e-30f ? 0x1p64f : 1.f;
+    inv = most > 0.f ? 127.f / (most * pre) : 0.f;
+    scale = most / 127.f;
+  }
+  __device__ __forceinline__ int operator()(float y) const {  // a NaN becomes 0 (its row's scale is NaN)
+    return max(-127, min(127, __float2int_rn(y * pre * inv)));
+  }
+};
+__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
+  return (a & 255) | (b & 255) << 8 | (c & 255) << 16 | static_cast<uint32_t>(d) << 24;
+}
+
+// One block per row; VPT vectors of the row in each thread.
+template <int DT, int VPT, bool I8>
+__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ NormParams p) {
+  using E = El<DT>;
+  constexpr int kVec = E::kVec;
+  constexpr int kBatch = VPT == 1 ? 8 : VPT == 2 ? 4 : 2;  // ranks whose loads are in flight together
+  __shared__ float part[32];
+  __shared__ uint32_t most[32];
+  stream_order();
+  const uint32_t row = blockIdx.x;
+  const uint32_t r = row / p.rows, t = row - r * p.rows;
+  const int nv = p.hidden / kVec;
+  const int64_t at = static_cast<int64_t>(row) * nv;  // the row's first vector in each send buffer
+  const int64_t own = static_cast<int64_t>(t) * nv;   // and in rank r's own buffers
+  float h[VPT][kVec];
+#pragma unroll
+  for (int u = 0; u < VPT; ++u)
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) h[u][i] = 0.f;
+  for (int q0 = 0; q0 < p.nranks; q0 += kBatch) {
+    uint4 v[kBatch][VPT];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+      for (int u = 0; u < VPT; ++u) {
+        const int c = threadIdx.x + u * blockDim.x;
+        if (q0 + b < p.nranks && c < nv) v[b][u] = dev::ld16(static_cast<const uint4*>(p.send[q0 + b]) + at + c);
+        else v[b][u] = make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+      for (int u = 0; u < VPT; ++u) {
+        float f[kVec];
+        E::widen(v[b][u], f);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) h[u][i] += f[i];
+      }
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int u = 0; u < VPT; ++u) {
+    const int c = threadIdx.x + u * blockDim.x;
+    if (c < nv) {
+      if (p.has_residual) {
+        float f[kVec];
+        E::widen(ld16_plain(static_cast<const uint4*>(p.residual[r]) + own + c), f);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) h[u][i] += f[i];
+      }
+      if (p.has_residual_out) dev::st16_wb(static_cast<uint4*>(p.residual_out[r]) + own + c, E::narrow(h[u]));
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) ss += h[u][i] * h[u][i];
+  }
+  const float rs = 1.f / sqrtf(block_sum(ss, part) / static_cast<float>(p.hidden) + p.eps);
+  if (p.has_rstd && threadIdx.x == 0) p.rstd[r][t] = rs;
+  uint32_t top = 0;
+#pragma unroll
+  for (int u = 0; u < VPT; ++u) {
+    const int c = threadIdx.x + u * blockDim.x;
+    if (c < nv) {
+      float w[kVec];
+      E::widen(ld16_plain(static_cast<const uint4*>(p.weight[r]) + c), w);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        h[u][i] = h[u][i] * rs * w[i];
+        top = max(top, __float_as_uint(fabsf(h[u][i])));
+      }
+      if (!I8) dev::st16_wb(static_cast<uint4*>(p.out[r]) + own + c, E::narrow(h[u]));
+    }
+  }
+  if (I8) {
+    const Quant quant(block_max_bits(top, most));
+    if (threadIdx.x == 0) p.scale[r][t] = quant.scale;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+      const int c = threadIdx.x + u * blockDim.x;
+      if (c < nv) {
+        uint32_t w[kVec / 4];
+#pragma unroll
+        for (int i = 0; i < kVec / 4; ++i)
+          w[i] = pack4(quant(h[u][4 * i]), quant(h[u][4 * i + 1]), quant(h[u][4 * i + 2]), quant(h[u][4 * i + 3]));
+        if constexpr (kVec == 8) static_cast<uint2*>(p.out[r])[own + c] = make_uint2(w[0], w[1]);
+        else static_cast<uint32_t*>(p.out[r])[own + c] = w[0];
+      }
+    }
+  }
+}
+
+// Any row, element by element, held in shared memory.
+template <int DT, bool I8>
+__global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ NormParams p) {
+  using E = El<DT>;
+  extern __shared__ float h[];
+  __shared__ float part[32];
+  __shared__ uint32_t most[32];
+  stream_order();
+  const uint32_t row = blockIdx.x;
+  const uint32_t r = row / p.rows, t = row - r * p.rows;
+  const int64_t at = static_cast<int64_t>(row) * p.hidden, own = static_cast<int64_t>(t) * p.hidden;
+  float ss = 0.f;
+  for (int c = threadIdx.x; c < p.hidden; c += blockDim.x) {
+    float x = 0.f;
+#pragma unroll 4
+    for (int q = 0; q < p.nranks; ++q) x += E::load(p.send[q], at + c);
+    if (p.has_residual) x += E::load(p.residual[r], own + c);
+    if (p.has_residual_out) E::store(p.residual_out[r], own + c, x);
+    h[c] = x;
+    ss += x * x;
+  }
+  const float rs = 1.f / sqrtf(block_sum(ss, part) / static_cast<float>(p.hidden) + p.eps);
+  if (p.has_rstd && threadIdx.x == 0) p.rstd[r][t] = rs;
+  uint32_t top = 0;
+  for (int c = threadIdx.x; c < p.hidden; c += blockDim.x) {  // each thread reads back what it wrote
+    const float y = h[c] * rs * E::load(p.weight[r], c);
+    if (I8) {
+      h[c] = y;
+      top = max(top, __float_as_uint(fabsf(y)));
+    } else {
+      E::store(p.out[r], own + c, y);
+    }
+  }
+  if (I8) {
+    const Quant quant(block_max_bits(top, most));
+    if (threadIdx.x == 0) p.scale[r][t] = quant.scale;
+    for (int c = threadIdx.x; c < p.hidden; c += blockDim.x)
+      static_cast<int8_t*>(p.out[r])[own + c] = static_cast<int8_t>(quant(h[c]));
+  }
+}
+
+struct GradParams {
+  const void* dout[VC_MAX_RANKS];
+  const void* dres_out[VC_MAX_RANKS];
+  const void* h[VC_MAX_RANKS];
+  const void* weight[VC_MAX_RANKS];
+  const float* rstd[VC_MAX_RANKS];
+  void* dsend[VC_MAX_RANKS];
+  void* dres[VC_MAX_RANKS];
+  float* part;  // [nranks * per][hidden] sums of the weight's gradient over each block's rows
+  int nranks, has_dres_out, has_dsend, has_dres, has_dweight;
+  uint32_t rows, per;  // tokens, blocks of each rank
+  int32_t hidden;
+};
+
+// Block b of rank r takes the rank's rows b, b + per, ...; each thread keeps
+// the weight's gradient of its columns over them.
+template <int DT, int VPT>
+__global__ void __launch_bounds__(kThreads) norm_grad_kernel(const __grid_constant__ GradParams p) {
+  using E = El<DT>;
+  constexpr int kVec = E::kVec;
+  __shared__ float part[2][32];
+  stream_order();
+  const uint32_t r = blockIdx.x / p.per, b = blockIdx.x - r * p.per;
+  const int nv = p.hidden / kVec;
+  float dw[VPT][kVec];
+#pragma unroll
+  for (int u = 0; u < VPT; ++u)
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) dw[u][i] = 0.f;
+  int flip = 0;
+  for (uint32_t t = b; t < p.rows; t += p.per, flip ^= 1) {
+    const int64_t own = static_cast<int64_t>(t) * nv;
+    const float rs = p.rstd[r][t];
+    float g[VPT][kVec], h[VPT][kVec], gh = 0.f;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+      const int c = threadIdx.x + u * blockDim.x;
+      if (c < nv) {
+        float w[kVec];
+        E::widen(dev::ld16(static_cast<const uint4*>(p.dout[r]) + own + c), g[u]);
+        E::widen(dev::ld16(static_cast<const uint4*>(p.h[r]) + own + c), h[u]);
+        E::widen(ld16_plain(static_cast<const uint4*>(p.weight[r]) + c), w);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          dw[u][i] += g[u][i] * h[u][i] * rs;
+          g[u][i] *= w[i];
+          gh += g[u][i] * h[u][i];
+        }
+      }
+    }
+    const float mean = block_sum(gh, part[flip]) / static_cast<float>(p.hidden) * rs * rs;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+      const int c = threadIdx.x + u * blockDim.x;
+      if (c < nv) {
+        float d[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) d[i] = rs * (g[u][i] - h[u][i] * mean);
+        if (p.has_dres_out) {
+          float f[kVec];
+          E::widen(ld16_plain(static_cast<const uint4*>(p.dres_out[r]) + own + c), f);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) d[i] += f[i];
+        }
+        const uint4 x = E::narrow(d);
+        if (p.has_dres) dev::st16_wb(static_cast<uint4*>(p.dres[r]) + own + c, x);
+        if (p.has_dsend) {
+          const int64_t at = (static_cast<int64_t>(r) * p.rows + t) * nv + c;
+          for (int q = 0; q < p.nranks; ++q) dev::st16(static_cast<uint4*>(p.dsend[q]) + at, x);
+        }
+      }
+    }
+  }
+  if (p.has_dweight) {
+    float* to = p.part + static_cast<int64_t>(blockIdx.x) * p.hidden;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+      const int c = threadIdx.x + u * blockDim.x;
+      if (c < nv) {
+#pragma unroll
+        for (int i = 0; i < kVec; i += 4)
+          *reinterpret_cast<float4*>(to + c * kVec + i) = make_float4(dw[u][i], dw[u][i + 1], dw[u][i + 2], dw[u][i + 3]);
+      }
+    }
+  }
+}
+
+// Any row, element by element; the weight's gradient in shared memory.
+template <int DT>
+__global__ void __launch_bounds__(1024) norm_grad_any_kernel(const __grid_constant__ GradParams p) {
+  using E = El<DT>;
+  extern __shared__ float dw[];
+  __shared__ float part[2][32];
+  stream_order();
+  const uint32_t r = blockIdx.x / p.per, b = blockIdx.x - r * p.per;
+  for (int c = threadIdx.x; c < p.hidden; c += blockDim.x) dw[c] = 0.f;  // only its own thread uses a column
+  int flip = 0;
+  for (uint32_t t = b; t < p.rows; t += p.per, flip ^= 1) {
+    const int64_t own = static_cast<int64_t>(t) * p.hidden;
+    const float rs = p.rstd[r][t];
+    float gh = 0.f;
+    for (int c = threadIdx.x; c < p.hidden; c += blockDim.x) {
+      const float dy = E::load(p.dout[r], own + c), h = E::load(p.h[r], own + c);
+      dw[c] += dy * h * rs;
+      gh += dy * E::load(p.weight[r], c) * h;
+    }
+    const float mean = block_sum(gh, part[flip]) / static_cast<float>(p.hidden) * rs * rs;
+    const int64_t at = (static_cast<int64_t>(r) * p.rows + t) * p.hidden;
+    for (int c = threadIdx.x; c < p.hidden; c += blockDim.x) {
+      const float g = E::load(p.dout[r], own + c) * E::load(p.weight[r], c);
+      float d = rs * (g - E::load(p.h[r], own + c) * mean);
+      if (p.has_dres_out) d += E::load(p.dres_out[r], own + c);
+      if (p.has_dres) E::store(p.dres[r], own + c, d);
+      if (p.has_dsend)
+        for (int q = 0; q < p.nranks; ++q) E::store(p.dsend[q], at + c, d);
+    }
+  }
+  if (p.has_dweight)
+    for (int c = threadIdx.x; c < p.hidden; c += blockDim.x) p.part[static_cast<int64_t>(blockIdx.x) * p.hidden + c] = dw[c];
+}
+
+struct WeightParams {
+  const float* part;
+  float* dweight[VC_MAX_RANKS];
+  uint32_t per, chunks;  // parts of each rank; blocks of each rank
+  int32_t hidden;
+};
+constexpr int kSumThreads = 256;
+
+// dweight[r] = the sum of rank r's parts: 32 columns a block, its warps take
+// the parts in turn, and the warps' sums are added in warp order.
+__global__ void __launch_bounds__(kSumThreads) norm_weight_kernel(const __grid_constant__ WeightParams p) {
+  __shared__ float sums[kSumThreads / 32][32];
+  stream_order();
+  const uint32_t r = blockIdx.x / p.chunks, chunk = blockIdx.x - r * p.chunks;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = static_cast<int>(chunk) * 32 + lane;
+  float x = 0.f;
+  if (c < p.hidden) {
+#pragma unroll 8
+    for (uint32_t b = warp; b < p.per; b += kSumThreads / 32)
+      x += p.part[(static_cast<int64_t>(r) * p.per + b) * p.hidden + c];
+  }
+  sums[warp][lane] = x;
+  __syncthreads();
+  if (warp == 0 && c < p.hidden) {
+    x = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSumThreads / 32; ++w) x += sums[w][lane];
+    p.dweight[r][c] = x;
+  }
+}
+
+// Vectors a thread holds for a row of nv vectors: the fewest that keep the
+// block within kThreads; 0 where that is more than `most`.
+int vectors_per_thread(int64_t nv, int most) {
+  for (int v = 1; v <= most; v *= 2)
+    if (nv <= static_cast<int64_t>(v) * kThreads) return v;
+  return 0;
+}
+unsigned threads_for(int64_t n, int per_thread, int most) {
+  const int64_t t = (n + per_thread - 1) / per_thread;
+  return static_cast<unsigned>(std::min<int64_t>(most, (t + 31) / 32 * 32));
+}
+// Threads of a block that takes a row element by element.
+unsigned any_threads(int64_t hidden) { return threads_for(hidden, 4, 1024); }
+
+template <int DT, int VPT>
+vc_status_t launch_norm(int dev, unsigned blocks, int64_t nv, bool i8, cudaStream_t s, const NormParams& p, int64_t bytes) {
+  const Shape shape{blocks, threads_for(nv, VPT, kThreads)};
+  return i8 ? launch<norm_kernel<DT, VPT, true>>(dev, shape, s, p, kNorm, 0, bytes)
+            : launch<norm_kernel<DT, VPT, false>>(dev, shape, s, p, kNorm, 0, bytes);
+}
+
+vc_status_t norm(const void* const* send, const void* const* residual, const void* const* weight,
+                 void* const* residual_out, void* const* out, float* const* scale, float* const* rstd, int nranks,
+                 size_t rows, size_t hidden, double eps, vc_dtype_t dtype, vc_dtype_t out_dtype, cudaStream_t stream) {
+  vc_status_t rc = check_ranks(nranks);
+  if (rc == VC_SUCCESS) rc = check_float(dtype);
+  if (rc != VC_SUCCESS) return rc;
+  const bool i8 = out_dtype == VC_INT8;
+  if (!i8 && out_dtype != dtype) return fail(VC_ERR_UNSUPPORTED, "out_dtype must be the data's or VC_INT8");
+  if (!(eps >= 0) || !std::isfinite(eps)) return fail(VC_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (hidden > VC_NORM_MAX_HIDDEN) return fail(VC_ERR_UNSUPPORTED, "hidden above VC_NORM_MAX_HIDDEN");
+  rc = check_tokens(nranks, rows, hidden);
+  if (rc != VC_SUCCESS) return rc;
+  const int64_t es = dtype_size(dtype), n = static_cast<int64_t>(rows) * static_cast<int64_t>(hidden);
+  const int os = dtype_size(out_dtype);
+  Buffers b;
+  rc = b.add(send, nranks, n * nranks * es, static_cast<int>(es), false, "send");
+  if (rc == VC_SUCCESS) rc = b.add(weight, nranks, static_cast<int64_t>(hidden) * es, static_cast<int>(es), false, "weight");
+  if (rc == VC_SUCCESS && residual)
+    rc = b.add(residual, nranks, n * es, static_cast<int>(es), false, "residual", residual_out);
+  if (rc == VC_SUCCESS && residual_out) rc = b.add(residual_out, nranks, n * es, static_cast<int>(es), true, "residual_out");
+  if (rc == VC_SUCCESS) rc = b.add(out, nranks, n * os, os, true, "out");
+  const bool aligned = b.aligned16();
+  if (rc == VC_SUCCESS && i8) rc = b.add(const_cast<const void* const*>(reinterpret_cast<void* const*>(scale)), nranks, static_cast<int64_t>(rows) * 4, 4, true, "scale");
+  if (rc == VC_SUCCESS && rstd) rc = b.add(const_cast<const void* const*>(reinterpret_cast<void* const*>(rstd)), nranks, static_cast<int64_t>(rows) * 4, 4, true, "rstd");
+  if (rc == VC_SUCCESS) rc = b.disjoint();
+  if (rc != VC_SUCCESS || n == 0) return rc;
+
+  DeviceState* st = nullptr;
+  int dev = 0;
+  rc = device_state(&st, &dev);
+  if (rc != VC_SUCCESS) return rc;
+  NormParams p = {};
+  for (int r = 0; r < nranks; ++r) {
+    p.send[r] = send[r];
+    p.weight[r] = weight[r];
+    p.out[r] = out[r];
+    if (residual) p.residual[r] = residual[r];
+    if (residual_out) p.residual_out[r] = residual_out[r];
+    if (i8) p.scale[r] = scale[r];
+    if (rstd) p.rstd[r] = rstd[r];
+  }
+  p.nranks = nranks;
+  p.has_residual = residual != nullptr;
+  p.has_residual_out = residual_out != nullptr;
+  p.has_rstd = rstd != nullptr;
+  p.rows = static_cast<uint32_t>(rows);
+  p.hidden = static_cast<int32_t>(hidden);
+  p.eps = static_cast<float>(eps);
+  const int64_t tokens = static_cast<int64_t>(rows) * nranks;
+  const int64_t bytes = n * nranks * (es * (nranks + p.has_residual + p.has_residual_out) + os) +
+                        static_cast<int64_t>(hidden) * es * nranks + tokens * 4 * (p.has_rstd + i8);
+  const unsigned blocks = static_cast<unsigned>(tokens);
+  return for_dtype(dtype, [&](auto code) {
+    constexpr int DT = code();
+    const int64_t nv = static_cast<int64_t>(hidden) / El<DT>::kVec;
+    const bool whole = aligned && hidden % El<DT>::kVec == 0;
+    switch (whole ? vectors_per_thread(nv, 8) : 0) {
+      case 1: return launch_norm<DT, 1>(dev, blocks, nv, i8, stream, p, bytes);
+      case 2: return launch_norm<DT, 2>(dev, blocks, nv, i8, stream, p, bytes);
+      case 4: return launch_norm<DT, 4>(dev, blocks, nv, i8, stream, p, bytes);
+      case 8: return launch_norm<DT, 8>(dev, blocks, nv, i8, stream, p, bytes);
+    }
+    const Shape shape{blocks, any_threads(static_cast<int64_t>(hidden)), hidden * sizeof(float)};
+    return i8 ? launch<norm_any_kernel<DT, true>>(dev, shape, stream, p, kNorm, 0, bytes)
+              : launch<norm_any_kernel<DT, false>>(dev, shape, stream, p, kNorm, 0, bytes);
+  });
+}
+
+// Blocks of each rank: enough to fill the GPU, at most one per row.
+uint32_t blocks_per_rank(int64_t resident, int nranks, uint32_t rows) {
+  return static_cast<uint32_t>(std::max<int64_t>(1, std::min<int64_t>(rows, resident / nranks)));
+}
+
+template <auto K>
+vc_status_t launch_grad(DeviceState* st, int dev, unsigned threads, size_t smem, cudaStream_t s, GradParams& p, int64_t bytes,
+                        float** scratch) {
+  vc_status_t rc = allow<K>(dev, smem, false);
+  if (rc != VC_SUCCESS) return rc;
+  p.per = blocks_per_rank(int64_t(st->nsm) * resident_blocks<K>(dev, static_cast<int>(threads), smem), p.nranks, p.rows);
+  const unsigned blocks = p.per * static_cast<unsigned>(p.nranks);
+  if (p.has_dweight) {
+    cudaMemPool_t pool;
+    rc = scratch_pool(st, dev, &pool);
+    if (rc != VC_SUCCESS) return rc;
+    const size_t need = static_cast<size_t>(blocks) * p.hidden * sizeof(float);
+    cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void**>(scratch), need, pool, s);
+    if (e == cudaErrorMemoryAllocation) {
+      cudaGetLastError();
+      return fail(VC_ERR_NOMEM, "scratch allocation of " + std::to_string(need) + " bytes failed");
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMallocFromPoolAsync");
+    p.part = *scratch;
+  }
+  return launch<K>(dev, Shape{blocks, threads, smem}, s, p, kNormBackward, 0, bytes);
+}
+
+vc_status_t norm_grad(const void* const* dout, const void* const* dres_out, const void* const* h,
+                      const void* const* weight, const float* const* rstd, void* const* dsend, void* const* dres,
+                      float* const* dweight, int nranks, size_t rows, size_t hidden, vc_dtype_t dtype,
+                      cudaStream_t stream) {
+  vc_status_t rc = check_ranks(nranks);
+  if (rc == VC_SUCCESS) rc = check_float(dtype);
+  if (rc != VC_SUCCESS) return rc;
+  if (hidden > VC_NORM_MAX_HIDDEN) return fail(VC_ERR_UNSUPPORTED, "hidden above VC_NORM_MAX_HIDDEN");
+  rc = check_tokens(nranks, rows, hidden);
+  if (rc != VC_SUCCESS) return rc;
+  if (!dsend && !dres && !dweight) return fail(VC_ERR_INVALID_ARG, "no gradient is asked for");
+  const int64_t es = dtype_size(dtype), n = static_cast<int64_t>(rows) * static_cast<int64_t>(hidden);
+  const int a = static_cast<int>(es);
+  Buffers b;
+  rc = b.add(dout, nranks, n * es, a, false, "dout");
+  if (rc == VC_SUCCESS) rc = b.add(h, nranks, n * es, a, false, "h");
+  if (rc == VC_SUCCESS) rc = b.add(weight, nranks, static_cast<int64_t>(hidden) * es, a, false, "weight");
+  if (rc == VC_SUCCESS && dres_out) rc = b.add(dres_out, nranks, n * es, a, false, "dresidual_out", dres);
+  if (rc == VC_SUCCESS && dsend) rc = b.add(dsend, nranks, n * nranks * es, a, true, "dsend");
+  if (rc == VC_SUCCESS && dres) rc = b.add(dres, nranks, n * es, a, true, "dresidual");
+  const bool aligned = b.aligned16();
+  if (rc == VC_SUCCESS) rc = b.add(reinterpret_cast<const void* const*>(rstd), nranks, static_cast<int64_t>(rows) * 4, 4, false, "rstd");
+  if (rc == VC_SUCCESS && dweight) rc = b.add(const_cast<const void* const*>(reinterpret_cast<void* const*>(dweight)), nranks, static_cast<int64_t>(hidden) * 4, 4, true, "dweight");
+  if (rc == VC_SUCCESS) rc = b.disjoint();
+  if (rc != VC_SUCCESS || hidden == 0) return rc;
+  if (rows == 0) {  // the sum over no tokens
+    for (int r = 0; dweight && r < nranks; ++r) {
+      cudaError_t e = cudaMemsetAsync(dweight[r], 0, hidden * sizeof(float), stream);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+    }
+    return VC_SUCCESS;
+  }
+
+  DeviceState* st = nullptr;
+  int dev = 0;
+  rc = device_state(&st, &dev);
+  if (rc != VC_SUCCESS) return rc;
+  GradParams p = {};
+  for (int r = 0; r < nranks; ++r) {
+    p.dout[r] = dout[r];
+    p.h[r] = h[r];
+    p.weight[r] = weight[r];
+    p.rstd[r] = rstd[r];
+    if (dres_out) p.dres_out[r] = dres_out[r];
+    if (dsend) p.dsend[r] = dsend[r];
+    if (dres) p.dres[r] = dres[r];
+  }
+  p.nranks = nranks;
+  p.has_dres_out = dres_out != nullptr;
+  p.has_dsend = dsend != nullptr;
+  p.has_dres = dres != nullptr;
+  p.has_dweight = dweight != nullptr;
+  p.rows = static_cast<uint32_t>(rows);
+  p.hidden = static_cast<int32_t>(hidden);
+  const int64_t bytes = n * nranks * es * (2 + p.has_dres_out + p.has_dres + (dsend ? nranks : 0)) +
+                        static_cast<int64_t>(rows) * nranks * 4 + static_cast<int64_t>(hidden) * nranks * es;
+  float* scratch = nullptr;
+  rc = for_dtype(dtype, [&](auto code) {
+    constexpr int DT = code();
+    const int64_t nv = static_cast<int64_t>(hidden) / El<DT>::kVec;
+    const bool whole = aligned && hidden % El<DT>::kVec == 0;
+    switch (whole ? vectors_per_thread(nv, 4) : 0) {
+      case 1: return launch_grad<norm_grad_kernel<DT, 1>>(st, dev, threads_for(nv, 1, kThreads), 0, stream, p, bytes, &scratch);
+      case 2: return launch_grad<norm_grad_kernel<DT, 2>>(st, dev, threads_for(nv, 2, kThreads), 0, stream, p, bytes, &scratch);
+      case 4: return launch_grad<norm_grad_kernel<DT, 4>>(st, dev, threads_for(nv, 4, kThreads), 0, stream, p, bytes, &scratch);
+    }
+    return launch_grad<norm_grad_any_kernel<DT>>(st, dev, any_threads(static_cast<int64_t>(hidden)),
+                                                 hidden * sizeof(float), stream, p, bytes, &scratch);
+  });
+  if (rc == VC_SUCCESS && dweight) {
+    WeightParams w = {};
+    w.part = scratch;
+    for (int r = 0; r < nranks; ++r) w.dweight[r] = dweight[r];
+    w.per = p.per;
+    w.chunks = static_cast<uint32_t>((hidden + 31) / 32);
+    w.hidden = p.hidden;
+    rc = launch<norm_weight_kernel>(dev, Shape{w.chunks * static_cast<unsigned>(nranks), kSumThreads}, stream, w, kNormWeight, 1,
+                                    static_cast<int64_t>(hidden) * nranks * 4 * (1 + static_cast<int64_t>(p.per)));
+  }
+  if (scratch) {
+    cudaError_t e = cudaFreeAsync(scratch, stream);
+    if (e != cudaSuccess && rc == VC_SUCCESS) rc = cuda_fail(e, "cudaFreeAsync");
+  }
+  return rc;
+}
+
+}  // namespace
+}  // namespace layer
+}  // namespace vc
+
+using namespace vc;
+
+VC_EXPORT vc_status_t vc_reduce_scatter_norm(const void* const* send, const void* const* residual,
+                                             const void* const* weight, void* const* residual_out, void* const* out,
+                                             float* const* scale, float* const* rstd, int nranks, size_t rows,
+                                             size_t hidden, double eps, vc_dtype_t dtype, vc_dtype_t out_dtype,
+                                             vc_stream_t stream) {
+  return entry([&] {
+    return layer::norm(send, residual, weight, residual_out, out, scale, rstd, nranks, rows, hidden, eps, dtype,
+                       out_dtype, reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+VC_EXPORT vc_status_t vc_reduce_scatter_norm_backward(const void* const* dout, const void* const* dresidual_out,
+                                                      const void* const* h, const void* const* weight,
+                                                      const float* const* rstd, void* const* dsend,
+                                                      void* const* dresidual, float* const* dweight, int nranks,
+                                                      size_t rows, size_t hidden, vc_dtype_t dtype,
+                                                      vc_stream_t stream) {
+  return entry([&] {
+    return layer::norm_grad(dout, dresidual_out, h, weight, rstd, dsend, dresidual, dweight, nranks, rows, hidden,
+                            dtype, reinterpret_cast<cudaStream_t>(stream));
+  });
+}

@@ -1,0 +1,493 @@
+// Choice of experts for each token, and its gradient (see vc.h).
+//
+// One warp takes one token: lane l holds experts l*V .. l*V + V - 1 in
+// registers, V the power of 2 that covers all experts, so that the lowest
+// lane, and in it the lowest register, is the lowest index of a tie.  What is
+// compared is computed with the same roundings in the same order everywhere
+// (single operations, and a softmax sum that adds neighbours first), so that
+// the choice is one and the same for any V.
+#include "layer.cuh"
+
+namespace vc {
+namespace layer {
+namespace {
+
+constexpr int kWarps = 8;  // tokens of a block
+constexpr unsigned kAll = 0xffffffffu;
+
+struct RouteParams {
+  const void* logits[VC_MAX_RANKS];
+  const float* bias[VC_MAX_RANKS];
+  int32_t* ids[VC_MAX_RANKS];
+  float* weights[VC_MAX_RANKS];
+  uint32_t rows, tokens;
+  int experts, topk, groups, keep_groups, group_top;
+  int sigmoid, renormalize, has_bias, by_score;  // by_score: experts are compared by scores, not by logits
+  int vec;                                       // each lane's experts are one aligned piece of the row
+  float scale;
+};
+struct RouteGradParams {
+  const float* dweights[VC_MAX_RANKS];
+  const void* logits[VC_MAX_RANKS];
+  const int32_t* ids[VC_MAX_RANKS];
+  void* dlogits[VC_MAX_RANKS];
+  uint32_t rows, tokens;
+  int experts, topk, sigmoid, renormalize, vec;
+  float scale;
+};
+
+constexpr float kNone = -INFINITY;
+
+// Lane's V logits of a row; -inf past the last expert.
+template <int DT, int V>
+__device__ __forceinline__ void load_row(const void* row, int lane, int experts, int vec, float* l) {
+  using E = El<DT>;
+  const int e0 = lane * V;
+  if (vec) {
+    if (e0 < experts) {
+      if constexpr (V % E::kVec == 0) {
+#pragma unroll
+        for (int i = 0; i < V / E::kVec; ++i)
+          E::widen(dev::ld16(static_cast<const uint4*>(row) + lane * (V / E::kVec) + i), l + i * E::kVec);
+      } else if constexpr (V * E::kSize == 8) {
+        const uint2 v = static_cast<const uint2*>(row)[lane];
+        if constexpr (DT == VC_FLOAT32) {
+          l[0] = __uint_as_float(v.x);
+          l[1] = __uint_as_float(v.y);
+        } else {
+          dev::widen2<E::kF16>(v.x, l);
+          dev::widen2<E::kF16>(v.y, l + 2);
+        }
+      } else if constexpr (V * E::kSize == 4 && V == 2) {
+        dev::widen2<E::kF16>(static_cast<const uint32_t*>(row)[lane], l);
+      } else {
+        l[0] = E::load(row, lane);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) l[i] = kNone;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = e0 + i < experts ? E::load(row, e0 + i) : kNone;
+  }
+}
+template <int DT, int V>
+__device__ __forceinline__ void store_row(void* row, int lane, int experts, int vec, const float* x) {
+  using E = El<DT>;
+  const int e0 = lane * V;
+  if constexpr (V % E::kVec == 0) {
+    if (vec) {
+      if (e0 < experts) {
+#pragma unroll
+        for (int i = 0; i < V / E::kVec; ++i)
+          dev::st16_wb(static_cast<uint4*>(row) + lane * (V / E::kVec) + i, E::narrow(x + i * E::kVec));
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (e0 + i < experts) E::store(row, e0 + i, x[i]);
+}
+
+// Sum over all lanes' V values, neighbours first.
+template <int V>
+__device__ __forceinline__ float pair_sum(const float* x) {
+  float s[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) s[i] = x[i];
+#pragma unroll
+  for (int n = V / 2; n > 0; n /= 2)
+#pragma unroll
+    for (int i = 0; i < n; ++i) s[i] = __fadd_rn(s[2 * i], s[2 * i + 1]);
+  float t = s[0];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) t = __fadd_rn(t, __shfl_xor_sync(kAll, t, d));
+  return t;
+}
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, d));
+  return x;
+}
+template <int V>
+__device__ __forceinline__ float row_max(const float* l) {  // NaN is passed over
+  float m = kNone;
+#pragma unroll
+  for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+  return warp_max(m);
+}
+__device__ __forceinline__ bool there(float l) { return l > kNone; }
+// exp(l - most), with the largest itself (infinite ones too) at 1.
+__device__ __forceinline__ float soft(float l, float most) {
+  return !there(l) ? 0.f : l == most ? 1.f : expf(__fsub_rn(l, most));
+}
+__device__ __forceinline__ float sigmoid(float l) {
+  return there(l) ? __fdiv_rn(1.f, __fadd_rn(1.f, expf(-l))) : 0.f;
+}
+// Bits that order as the numbers do; above 0 for every number.
+__device__ __forceinline__ uint32_t order_key(float c) {
+  const uint32_t u = __float_as_uint(__fadd_rn(c, 0.f));  // -0 as 0
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+
+// The two largest of a group so far, and one more value.
+struct Two {
+  float a = kNone, b = kNone;
+  __device__ __forceinline__ void take(float x) {
+    b = fmaxf(b, fminf(a, x));
+    a = fmaxf(a, x);
+  }
+  __device__ __forceinline__ float worth(int top) const { return top == 2 && b > kNone ? __fadd_rn(a, b) : a; }
+};
+
+template <int DT, int V>
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteParams p) {
+  __shared__ float table[kWarps][V * 32];  // a token's c, where a group's experts are not whole lanes
+  stream_order();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t token = blockIdx.x * kWarps + warp;
+  if (token >= p.tokens) return;
+  const uint32_t r = token / p.rows, t = token - r * p.rows;
+  float c[V], s[V];  // c: what experts are compared by, -inf where not to be chosen; s: their scores or logits
+  load_row<DT, V>(static_cast<const char*>(p.logits[r]) + static_cast<int64_t>(t) * p.experts * El<DT>::kSize, lane, p.experts, p.vec, s);
+  float most = 0.f, sum = 1.f;
+  // the softmax's maximum and sum, where a score is wanted (the sum cancels
+  // in weights that are renormalised)
+  if (!p.sigmoid) {
+    most = row_max<V>(s);
+    if (p.by_score || !p.renormalize) {
+      float e[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) e[i] = soft(s[i], most);
+      sum = pair_sum<V>(e);
+      if (p.by_score) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const bool on = there(s[i]);
+          s[i] = on ? __fdiv_rn(e[i], sum) : 0.f;
+          c[i] = on ? s[i] : kNone;
+        }
+      }
+    }
+  } else if (p.by_score) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const bool on = there(s[i]);
+      s[i] = sigmoid(s[i]);
+      c[i] = on ? s[i] : kNone;
+    }
+  }
+  if (!p.by_score) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = there(s[i]) ? s[i] : kNone;
+  }
+  if (p.has_bias) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (c[i] > kNone) {
+        const float x = __fadd_rn(c[i], p.bias[r][lane * V + i]);
+        c[i] = x > kNone ? x : kNone;  // a NaN too
+      }
+    }
+  }
+  if (p.groups > 1) {
+    const int size = p.experts / p.groups, lanes = size / V;
+    if (size % V == 0 && (lanes & (lanes - 1)) == 0) {  // a group is a power of 2 of whole lanes
+      Two two;
+#pragma unroll
+      for (int i = 0; i < V; ++i) two.take(c[i]);
+      for (int d = 1; d < lanes; d <<= 1) {
+        const float a = __shfl_xor_sync(kAll, two.a, d), b = __shfl_xor_sync(kAll, two.b, d);
+        two.take(a);
+        two.take(b);
+      }
+      const float mine = two.worth(p.group_top);
+      const int me = lane / lanes;
+      int better = 0;
+      for (int g = 0; g < p.groups; ++g) {
+        const float w = __shfl_sync(kAll, mine, g * lanes);
+        better += w > mine || (w == mine && g < me);
+      }
+      if (better >= p.keep_groups) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] = kNone;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) table[warp][lane * V + i] = c[i];
+      __syncwarp();
+      Two two;
+      if (lane < p.groups)
+        for (int i = 0; i < size; ++i) two.take(table[warp][lane * size + i]);
+      const float mine = two.worth(p.group_top);
+      int better = 0;
+      for (int g = 0; g < p.groups; ++g) {
+        const float w = __shfl_sync(kAll, mine, g);
+        better += w > mine || (w == mine && g < lane);
+      }
+      const uint32_t kept = __ballot_sync(kAll, lane < p.groups && better < p.keep_groups);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = lane * V + i;
+        if (e < p.experts && !(kept >> (e / size) & 1)) c[i] = kNone;
+      }
+    }
+  }
+  uint32_t key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) key[i] = c[i] > kNone ? order_key(c[i]) : 0u;
+  int my_id = -1;
+  float mine = 0.f;  // lane j: the score or logit of choice j
+  uint32_t best;
+  int at;
+  float value;
+  const auto look = [&] {
+    best = key[0];
+    at = 0;
+    value = s[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
+        value = s[i];
+      }
+  };
+  look();
+  for (int j = 0; j < p.topk; ++j) {
+    const uint32_t top = __reduce_max_sync(kAll, best);
+    if (top == 0) break;
+    const int from = __ffs(__ballot_sync(kAll, best == top)) - 1;
+    const int id = __shfl_sync(kAll, lane * V + at, from);
+    const float v = __shfl_sync(kAll, value, from);
+    if (lane == j) {
+      my_id = id;
+      mine = v;
+    }
+    if (lane == from) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i == at) key[i] = 0;
+      look();
+    }
+  }
+  float w = 0.f;
+  if (my_id >= 0) w = p.by_score ? mine : p.sigmoid ? sigmoid(mine) : __fdiv_rn(soft(mine, most), sum);
+  if (p.renormalize) w = w / fmaxf(warp_sum(w), 0x1p-126f);
+  if (lane < p.topk) {
+    const int64_t to = static_cast<int64_t>(t) * p.topk + lane;
+    p.ids[r][to] = my_id;
+    p.weights[r][to] = w * p.scale;
+  }
+}
+
+template <int DT, int V>
+__global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_constant__ RouteGradParams p) {
+  stream_order();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t token = blockIdx.x * kWarps + warp;
+  if (token >= p.tokens) return;
+  const uint32_t r = token / p.rows, t = token - r * p.rows;
+  const int64_t at = static_cast<int64_t>(t) * p.experts * El<DT>::kSize;
+  const char* row = static_cast<const char*>(p.logits[r]) + at;
+  // lane j: choice j's expert, its logit and the gradient of scale * (its share or score)
+  int id = -1;
+  float l = kNone, d = 0.f;
+  if (lane < p.topk) {
+    const int64_t from = static_cast<int64_t>(t) * p.topk + lane;
+    id = p.ids[r][from];
+    if (id >= 0 && id < p.experts) {
+      l = El<DT>::load(row, id);
+      d = p.dweights[r][from] * p.scale;
+    } else {
+      id = -1;
+    }
+  }
+  float x[V];  // the row's gradient
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = 0.f;
+  float give = 0.f;  // lane j: what its choice adds to its expert's gradient
+  if (p.renormalize) {
+    // shares of the chosen scores; of a softmax they depend on the chosen
+    // logits alone, and the gradient stays among them
+    const float e = p.sigmoid ? sigmoid(l) : soft(l, warp_max(l));
+    const float total = warp_sum(e);
+    if (total >= 0x1p-126f) {
+      const float share = e / total;
+      give = share * (d - warp_sum(d * share));
+      if (p.sigmoid) give *= 1.f / (1.f + expf(l));
+    }
+  } else if (p.sigmoid) {
+    give = d * sigmoid(l) / (1.f + expf(l));
+  } else {
+    float all[V];
+    load_row<DT, V>(row, lane, p.experts, p.vec, all);
+    const float most = row_max<V>(all);
+#pragma unroll
+    for (int i = 0; i < V; ++i) all[i] = soft(all[i], most);
+    const float sum = pair_sum<V>(all);
+    const float s = there(l) ? soft(l, most) / sum : 0.f;
+    const float dot = warp_sum(d * s);
+    give = d * s;
+    if (sum > 0.f) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = -(all[i] / sum) * dot;
+    }
+  }
+  if (!there(l)) give = 0.f;
+  for (int j = 0; j < p.topk; ++j) {
+    const int e = __shfl_sync(kAll, id, j);
+    const float g = __shfl_sync(kAll, give, j);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (e == lane * V + i) x[i] += g;
+  }
+  store_row<DT, V>(static_cast<char*>(p.dlogits[r]) + at, lane, p.experts, p.vec, x);
+}
+
+// Runs f with the experts a lane holds as a compile-time constant.
+template <class F>
+vc_status_t for_width(int experts, F&& f) {
+  if (experts <= 32) return f(std::integral_constant<int, 1>{});
+  if (experts <= 64) return f(std::integral_constant<int, 2>{});
+  if (experts <= 128) return f(std::integral_constant<int, 4>{});
+  if (experts <= 256) return f(std::integral_constant<int, 8>{});
+  if (experts <= 512) return f(std::integral_constant<int, 16>{});
+  return f(std::integral_constant<int, 32>{});
+}
+
+vc_status_t check_route(int nranks, size_t rows, int nexperts, const vc_route_t* how, vc_dtype_t dtype) {
+  vc_status_t rc = check_ranks(nranks);
+  if (rc == VC_SUCCESS) rc = check_float(dtype);
+  if (rc != VC_SUCCESS) return rc;
+  if (!how) return fail(VC_ERR_INVALID_ARG, "null route description");
+  if (how->score != VC_SCORE_SOFTMAX && how->score != VC_SCORE_SIGMOID) return fail(VC_ERR_INVALID_ARG, "unknown score");
+  if (nexperts < 1 || nexperts > VC_ROUTE_MAX_EXPERTS) return fail(VC_ERR_INVALID_ARG, "nexperts outside [1, 1024]");
+  if (how->topk < 1 || how->topk > VC_ROUTE_MAX_TOPK || how->topk > nexperts)
+    return fail(VC_ERR_INVALID_ARG, "topk outside [1, min(nexperts, 32)]");
+  if (!std::isfinite(how->scale)) return fail(VC_ERR_INVALID_ARG, "scale must be finite");
+  return check_tokens(nranks, rows, static_cast<size_t>(nexperts));
+}
+// Whether a lane's V experts are whole, aligned pieces of every row.
+bool whole_lanes(bool aligned, int experts, int v) { return aligned && experts % v == 0; }
+
+vc_status_t route(const void* const* logits, const float* const* bias, int32_t* const* ids, float* const* weights,
+                  int nranks, size_t rows, int nexperts, const vc_route_t* how, vc_dtype_t dtype, cudaStream_t stream) {
+  vc_status_t rc = check_route(nranks, rows, nexperts, how, dtype);
+  if (rc != VC_SUCCESS) return rc;
+  if (how->ngroups < 1 || how->ngroups > 32 || nexperts % how->ngroups)
+    return fail(VC_ERR_INVALID_ARG, "ngroups must be in [1, 32] and divide nexperts");
+  if (how->topk_groups < 1 || how->topk_groups > how->ngroups) return fail(VC_ERR_INVALID_ARG, "topk_groups outside [1, ngroups]");
+  if (how->group_top != 1 && how->group_top != 2) return fail(VC_ERR_INVALID_ARG, "group_top must be 1 or 2");
+  const int es = dtype_size(dtype);
+  const int64_t n = static_cast<int64_t>(rows), k = how->topk;
+  Buffers b;
+  rc = b.add(logits, nranks, n * nexperts * es, es, false, "logits");
+  const bool aligned = b.aligned16();
+  if (rc == VC_SUCCESS && bias) rc = b.add(reinterpret_cast<const void* const*>(bias), nranks, int64_t(nexperts) * 4, 4, false, "bias");
+  if (rc == VC_SUCCESS) rc = b.add(reinterpret_cast<const void* const*>(ids), nranks, n * k * 4, 4, true, "ids");
+  if (rc == VC_SUCCESS) rc = b.add(reinterpret_cast<const void* const*>(weights), nranks, n * k * 4, 4, true, "weights");
+  if (rc == VC_SUCCESS) rc = b.disjoint();
+  if (rc != VC_SUCCESS || rows == 0) return rc;
+  DeviceState* st = nullptr;
+  int dev = 0;
+  rc = device_state(&st, &dev);
+  if (rc != VC_SUCCESS) return rc;
+  RouteParams p = {};
+  for (int r = 0; r < nranks; ++r) {
+    p.logits[r] = logits[r];
+    if (bias) p.bias[r] = bias[r];
+    p.ids[r] = ids[r];
+    p.weights[r] = weights[r];
+  }
+  p.rows = static_cast<uint32_t>(rows);
+  p.tokens = p.rows * static_cast<uint32_t>(nranks);
+  p.experts = nexperts;
+  p.topk = how->topk;
+  p.groups = how->ngroups;
+  p.keep_groups = how->topk_groups;
+  p.group_top = how->group_top;
+  p.sigmoid = how->score == VC_SCORE_SIGMOID;
+  p.renormalize = how->renormalize != 0;
+  p.has_bias = bias != nullptr;
+  p.by_score = bias != nullptr || (how->ngroups > 1 && how->group_top == 2);
+  p.scale = how->scale;
+  const int64_t bytes = int64_t(p.tokens) * (int64_t(nexperts) * es + k * 8) + (bias ? int64_t(nexperts) * nranks * 4 : 0);
+  const Shape shape{(p.tokens + kWarps - 1) / kWarps, kWarps * 32};
+  return for_dtype(dtype, [&](auto code) {
+    return for_width(nexperts, [&](auto width) {
+      p.vec = whole_lanes(aligned, nexperts, width());
+      return launch<route_kernel<code(), width()>>(dev, shape, stream, p, kRoute, 0, bytes);
+    });
+  });
+}
+
+vc_status_t route_grad(const float* const* dweights, const void* const* logits, const int32_t* const* ids,
+                       void* const* dlogits, int nranks, size_t rows, int nexperts, const vc_route_t* how,
+                       vc_dtype_t dtype, cudaStream_t stream) {
+  vc_status_t rc = check_route(nranks, rows, nexperts, how, dtype);
+  if (rc != VC_SUCCESS) return rc;
+  const int es = dtype_size(dtype);
+  const int64_t n = static_cast<int64_t>(rows), k = how->topk;
+  Buffers b;
+  rc = b.add(logits, nranks, n * nexperts * es, es, false, "logits");
+  if (rc == VC_SUCCESS) rc = b.add(dlogits, nranks, n * nexperts * es, es, true, "dlogits");
+  const bool aligned = b.aligned16();
+  if (rc == VC_SUCCESS) rc = b.add(reinterpret_cast<const void* const*>(dweights), nranks, n * k * 4, 4, false, "dweights");
+  if (rc == VC_SUCCESS) rc = b.add(reinterpret_cast<const void* const*>(ids), nranks, n * k * 4, 4, false, "ids");
+  if (rc == VC_SUCCESS) rc = b.disjoint();
+  if (rc != VC_SUCCESS || rows == 0) return rc;
+  DeviceState* st = nullptr;
+  int dev = 0;
+  rc = device_state(&st, &dev);
+  if (rc != VC_SUCCESS) return rc;
+  RouteGradParams p = {};
+  for (int r = 0; r < nranks; ++r) {
+    p.dweights[r] = dweights[r];
+    p.logits[r] = logits[r];
+    p.ids[r] = ids[r];
+    p.dlogits[r] = dlogits[r];
+  }
+  p.rows = static_cast<uint32_t>(rows);
+  p.tokens = p.rows * static_cast<uint32_t>(nranks);
+  p.experts = nexperts;
+  p.topk = how->topk;
+  p.sigmoid = how->score == VC_SCORE_SIGMOID;
+  p.renormalize = how->renormalize != 0;
+  p.scale = how->scale;
+  const bool dense = !p.sigmoid && !p.renormalize;
+  const int64_t bytes = int64_t(p.tokens) * ((int64_t(nexperts) + (dense ? nexperts : k)) * es + k * 8);
+  const Shape shape{(p.tokens + kWarps - 1) / kWarps, kWarps * 32};
+  return for_dtype(dtype, [&](auto code) {
+    return for_width(nexperts, [&](auto width) {
+      p.vec = whole_lanes(aligned, nexperts, width());
+      return launch<route_grad_kernel<code(), width()>>(dev, shape, stream, p, kRouteBackward, 0, bytes);
+    });
+  });
+}
+
+}  // namespace
+}  // namespace layer
+}  // namespace vc
+
+using namespace vc;
+
+VC_EXPORT vc_status_t vc_route(const void* const* logits, const float* const* bias, int32_t* const* ids,
+                               float* const* weights, int nranks, size_t rows, int nexperts, const vc_route_t* how,
+                               vc_dtype_t dtype, vc_stream_t stream) {
+  return entry([&] {
+    return layer::route(logits, bias, ids, weights, nranks, rows, nexperts, how, dtype,
+                        reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+VC_EXPORT vc_status_t vc_route_backward(const float* const* dweights, const void* const* logits,
+                                        const int32_t* const* ids, void* const* dlogits, int nranks, size_t rows,
+                                        int nexperts, const vc_route_t* how, vc_dtype_t dtype, vc_stream_t stream) {
+  return entry([&] {
+    return layer::route_grad(dweights, logits, ids, dlogits, nranks, rows, nexperts, how, dtype,
+                             reinterpret_cast<cudaStream_t>(stream));
+  });
+}

@@ -27,12 +27,11 @@
 #include <string>
 #include <vector>
 
+#include "host.h"
 #include "kernels.cuh"
 #include "slice.cuh"
 #include "plan.h"
 #include "vc.h"
-
-#define VC_EXPORT extern "C" __attribute__((visibility("default")))
 
 namespace vc {
 
@@ -41,6 +40,7 @@ namespace vc {
 // ---------------------------------------------------------------------------
 namespace {
 thread_local std::string g_last_error;
+}  // namespace
 
 vc_status_t fail(vc_status_t s, const std::string& msg) {
   g_last_error = msg;
@@ -49,7 +49,7 @@ vc_status_t fail(vc_status_t s, const std::string& msg) {
 vc_status_t cuda_fail(cudaError_t e, const char* what) {
   return fail(VC_ERR_CUDA, std::string(what) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")");
 }
-// VC_PDL=0 launches every step in plain stream order (for comparison).
+void clear_error() { g_last_error.clear(); }
 bool pdl_enabled() {
   static const bool on = [] {
     const char* v = std::getenv("VC_PDL");
@@ -57,12 +57,14 @@ bool pdl_enabled() {
   }();
   return on;
 }
+namespace {
 // Copy launches writing at least this many bytes take the bulk-copy pipeline
 // (vc_set_copy_pipeline).
 std::atomic<size_t> g_copy_pipeline{VC_COPY_PIPELINE_DEFAULT};
 // Steps after one that writes at least this many bytes are ordered for L2
 // reuse (vc_set_reuse_order); read when a plan is built.
 std::atomic<size_t> g_reuse_min{VC_REUSE_ORDER_DEFAULT};
+}  // namespace
 bool log_enabled() {
   static const bool on = [] {
     const char* v = std::getenv("VC_LOG");
@@ -70,27 +72,14 @@ bool log_enabled() {
   }();
   return on;
 }
-}  // namespace
-
-
 
 // ---------------------------------------------------------------------------
 // per-device state: SM count, occupancy, scratch pool
 // ---------------------------------------------------------------------------
 namespace {
-
-// Blocks of one kernel resident per SM.
-struct Residency {
-  int blocks = 1;
-};
-struct DeviceState {
-  bool init = false;
-  int nsm = 0;
-  cudaMemPool_t pool = nullptr;
-  std::map<const void*, Residency> occupancy;
-};
 std::mutex g_mu;
 DeviceState g_dev[64];
+}  // namespace
 
 vc_status_t device_state(DeviceState** out, int* dev_out) {
   int dev = 0;
@@ -127,6 +116,8 @@ vc_status_t scratch_pool(DeviceState* st, int dev, cudaMemPool_t* pool) {
   *pool = st->pool;
   return VC_SUCCESS;
 }
+
+namespace {
 
 // Resident blocks per SM of a kernel (its occupancy limit), queried once.
 template <class K>
@@ -180,6 +171,33 @@ cudaError_t take_event(cudaEvent_t* ev) {
   }
   return cudaEventCreate(ev);
 }
+
+}  // namespace
+
+vc_status_t launch_traced(cudaStream_t stream, const vc_trace_record_t& rec, cudaError_t (*launch)(void*), void* arg) {
+  std::unique_lock<std::mutex> lk(g_trace_mu);
+  const bool trace = trace_slot();
+  if (!trace) lk.unlock();
+  Pending pend{};
+  if (trace) {
+    cudaError_t e = take_event(&pend.start);
+    if (e == cudaSuccess) e = take_event(&pend.stop);
+    if (e == cudaSuccess) e = cudaEventRecord(pend.start, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "trace event");
+  }
+  cudaError_t e = launch(arg);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "kernel launch");
+  if (trace) {
+    e = cudaEventRecord(pend.stop, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "trace event");
+    pend.rec = rec;
+    g_trace.push_back(pend);
+  }
+  return VC_SUCCESS;
+}
+
+namespace {
 
 int64_t launch_bytes(const Step& st, size_t i, size_t j) {
   int64_t b = 0;
@@ -536,10 +554,14 @@ struct Call {
   cudaStream_t stream = nullptr;
 };
 
+}  // namespace
+
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
 }
+
+namespace {
 
 vc_status_t plan_status(PlanStatus ps, const std::string& why) {
   if (ps == PlanStatus::Invalid) return fail(VC_ERR_INVALID_ARG, why);
@@ -562,6 +584,7 @@ vc_status_t to_dt(vc_dtype_t d, DT* out) {
     case VC_BFLOAT16: *out = DT::BF16; return VC_SUCCESS;
     case VC_INT32: *out = DT::I32; return VC_SUCCESS;
     case VC_FLOAT16: *out = DT::F16; return VC_SUCCESS;
+    case VC_INT8: break;  // rows of the layer operators only
   }
   return fail(VC_ERR_INVALID_ARG, "unknown dtype");
 }
@@ -1590,18 +1613,6 @@ vc_status_t run(const Call& c) {
                  static_cast<long long>(plan.scratch_bytes));
   }
   return rc;
-}
-
-template <class F>
-vc_status_t entry(F&& f) {
-  g_last_error.clear();
-  try {
-    return f();
-  } catch (const std::bad_alloc&) {
-    return fail(VC_ERR_NOMEM, "host allocation failed");
-  } catch (...) {
-    return fail(VC_ERR_INVALID_ARG, "internal error");
-  }
 }
 
 }  // namespace

@@ -68,7 +68,9 @@ typedef enum {
   VC_ERR_TIMEOUT = 5
 } vc_status_t;
 
-typedef enum { VC_FLOAT32 = 0, VC_BFLOAT16 = 1, VC_INT32 = 2, VC_FLOAT16 = 3 } vc_dtype_t;
+/* VC_INT8 is a format of rows for the layer operators (vc_reduce_scatter_norm's
+ * output, vc_dispatch's rows); the collectives refuse it. */
+typedef enum { VC_FLOAT32 = 0, VC_BFLOAT16 = 1, VC_INT32 = 2, VC_FLOAT16 = 3, VC_INT8 = 4 } vc_dtype_t;
 
 /*
  * Reduction ops, as the hccl article lists them (SUM / MAX / MIN).  MAX and
@@ -392,9 +394,13 @@ vc_status_t vc_plan_exec_order(vc_coll_t coll, vc_algo_t algo, int nranks, size_
  *   whole call, step -1, bytes and nops of all steps; bits 0-2 then give the
  *   mode of the plan's reduction steps), bit 8 set as well when that launch
  *   ran the sliced form (vc_set_slice_limit).
+ *   A layer operator's launch has bit 9 set, its kernel's index in bits 0-3
+ *   (0 norm, 1 norm backward, 2 the sum of its weight gradients, 3 route, 4
+ *   route backward, 5 dispatch plan, 6 dispatch, 7 combine, 8 combine
+ *   backward), coll -1, algo -1 and step the launch within the call.
  */
 typedef struct {
-  int32_t coll;   /* vc_coll_t */
+  int32_t coll;   /* vc_coll_t; -1: a layer operator */
   int32_t algo;   /* vc_algo_t */
   int32_t step;
   int32_t kernel;
@@ -603,6 +609,178 @@ vc_status_t vc_copy_selftest(vc_stream_t stream, uint32_t* flags);
 vc_status_t vc_reduce_scatter_noalloc(const void* const* send, void* const* recv, int nranks,
                                       size_t recvcount, vc_dtype_t dtype, vc_op_t op,
                                       vc_stream_t stream);
+
+/*
+ * Layer operators.
+ *
+ * What a transformer layer does around its collectives, on the same virtual
+ * ranks (no counterpart on the source pages, which stop at the collectives):
+ * the norm that follows a tensor-parallel ReduceScatter, the choice of experts
+ * for each token, and the exchange of tokens between the ranks that hold them
+ * and the ranks that hold the experts -- an AllToAll whose counts the choice
+ * decides.  Each rank holds `rows` tokens.
+ *
+ * The common rules above hold: host arrays with one device pointer per rank,
+ * work only enqueued, errors returned, graph capture allowed, scratch from
+ * the library's pool.  Rows lie one behind another; any alignment of element
+ * size is accepted, and rows that start on 16-byte boundaries run faster.
+ * Tensors are dense.  Data are VC_FLOAT32, VC_BFLOAT16 or VC_FLOAT16, widened
+ * to fp32, computed in fp32 and rounded once at the end; another dtype is
+ * VC_ERR_UNSUPPORTED.  More than 2^31 - 1 tokens over all ranks, or sizes
+ * that overflow, are VC_ERR_INVALID_ARG.  Results are reproducible bit for
+ * bit on one GPU model: no sum depends on the order in which blocks run.
+ */
+
+/* Largest `hidden` of the norm operators: a row is held on chip in fp32. */
+#define VC_NORM_MAX_HIDDEN 49152
+
+/*
+ * ReduceScatter, residual and RMS norm in one pass over the partial sums
+ * (with nranks = 1: the residual's addition and the norm).  Rank r owns token
+ * block r.  For token t of rank r, over i < hidden:
+ *   h[i]   = sum over q of send[q][(r*rows + t)*hidden + i]   (rank order)
+ *            + residual[r][t*hidden + i]
+ *   rs     = 1 / sqrt(mean of h[i]^2 + eps)
+ *   y[i]   = h[i] * rs * weight[r][i]
+ *   residual_out[r] = h, out[r] = y, rstd[r][t] = rs.
+ * y comes from h before its rounding to the data type.
+ *   send[q]: nranks*rows*hidden elements; weight[r]: hidden elements.
+ *   residual: NULL adds none.  residual_out: NULL writes none;
+ *   residual_out[r] == residual[r] is allowed.
+ *   out_dtype: dtype, or VC_INT8 with
+ *     scale[r][t] = max |y| / 127,  out = y / scale rounded to nearest even;
+ *   a row of zeros has scale 0 and zeros, a row with a NaN has scale NaN.
+ *   scale: required with VC_INT8, else not looked at.  rstd: fp32, NULL
+ *   writes none.
+ *   eps: finite and >= 0.  hidden above VC_NORM_MAX_HIDDEN is
+ *   VC_ERR_UNSUPPORTED.
+ */
+vc_status_t vc_reduce_scatter_norm(const void* const* send, const void* const* residual, const void* const* weight,
+                                   void* const* residual_out, void* const* out, float* const* scale,
+                                   float* const* rstd, int nranks, size_t rows, size_t hidden, double eps,
+                                   vc_dtype_t dtype, vc_dtype_t out_dtype, vc_stream_t stream);
+
+/*
+ * Its gradient (of the output in the data type).  With dy = dout[r], h and rs
+ * the forward call's residual_out[r] and rstd[r], g = dy * weight[r]:
+ *   dh = rs * (g - h * rs^2 * mean of g*h) + dresidual_out[r]
+ *   dsend[q][r*rows + t] = dh for every q (the ReduceScatter's gradient is an
+ *   AllGather), dresidual[r] = dh,
+ *   dweight[r] = sum over the rank's tokens of dy * h * rs   (fp32).
+ *   dresidual_out: NULL adds none; dresidual[r] == dresidual_out[r] is
+ *   allowed.  dsend, dresidual, dweight: NULL is not written, one at least is
+ *   wanted.  The weight's gradient over all ranks is their sum
+ *   (vc_allreduce).  With rows = 0 dweight is set to 0.
+ */
+vc_status_t vc_reduce_scatter_norm_backward(const void* const* dout, const void* const* dresidual_out,
+                                            const void* const* h, const void* const* weight,
+                                            const float* const* rstd, void* const* dsend, void* const* dresidual,
+                                            float* const* dweight, int nranks, size_t rows, size_t hidden,
+                                            vc_dtype_t dtype, vc_stream_t stream);
+
+/*
+ * Choice of `topk` of `nexperts` experts for each token.
+ *   s = softmax of the token's logits, or 1 / (1 + exp(-logit)) for each;
+ *   c = s + bias, what the experts are compared by; without a bias (and
+ *       without sums of two, below) the logits themselves, which s follows;
+ *   an expert whose logit is -inf or NaN is not there: s = 0, never chosen;
+ *   one whose c is -inf or NaN is not chosen either.
+ * With ngroups > 1 the experts are ngroups groups of nexperts / ngroups
+ * neighbours.  A group is worth its largest c (group_top 1) or the sum of its
+ * two largest (group_top 2; of one, where it has one), and experts are chosen
+ * from the topk_groups best groups.  Ties go to the lower index, of groups
+ * and of experts.  For choice j, best first:
+ *   ids[r][t*topk + j] = the expert,
+ *   weights[r][t*topk + j] = scale * s, or with renormalize
+ *     scale * s / max(sum of the chosen s, 2^-126).
+ * Where fewer than topk can be chosen (a padding token: every logit -inf) the
+ * rest have id -1 and weight 0.
+ * The softmax's sum adds neighbours first: over experts 2i and 2i+1, then
+ * over neighbouring sums, and so on, with zeros up to a power of 2.
+ *   logits[r]: rows*nexperts; bias: NULL, or fp32 [nexperts] per rank.
+ *   nexperts <= VC_ROUTE_MAX_EXPERTS, topk <= min(nexperts,
+ *   VC_ROUTE_MAX_TOPK), ngroups <= 32 and dividing nexperts, topk_groups in
+ *   [1, ngroups], group_top 1 or 2, scale finite; else VC_ERR_INVALID_ARG.
+ */
+#define VC_ROUTE_MAX_EXPERTS 1024
+#define VC_ROUTE_MAX_TOPK 32
+typedef enum { VC_SCORE_SOFTMAX = 0, VC_SCORE_SIGMOID = 1 } vc_score_t;
+typedef struct {
+  vc_score_t score;
+  int topk;
+  int ngroups;
+  int topk_groups;
+  int group_top;
+  int renormalize;
+  float scale;
+} vc_route_t;
+vc_status_t vc_route(const void* const* logits, const float* const* bias, int32_t* const* ids, float* const* weights,
+                     int nranks, size_t rows, int nexperts, const vc_route_t* how, vc_dtype_t dtype,
+                     vc_stream_t stream);
+
+/*
+ * Its gradient: dlogits (every one written) from dweights, with the logits
+ * and the ids of the forward call.  The choice is held fixed, and the bias,
+ * which only guides the choice, has none.  An id outside [0, nexperts) takes
+ * no part.  Of `how`, topk, score, renormalize and scale are looked at.  A
+ * token whose chosen scores sum to less than 2^-126 gets 0 with renormalize.
+ */
+vc_status_t vc_route_backward(const float* const* dweights, const void* const* logits, const int32_t* const* ids,
+                              void* const* dlogits, int nranks, size_t rows, int nexperts, const vc_route_t* how,
+                              vc_dtype_t dtype, vc_stream_t stream);
+
+/*
+ * Where each token's rows go.  Expert e lives on rank e / (nexperts/nranks);
+ * nranks must divide nexperts.  Each rank receives the rows of its experts in
+ * the order (expert, source rank, token, choice), `capacity` of them at most:
+ *   slots[r][t*topk + j] = d*capacity + row, the row of rank d's receive
+ *     buffer for choice j of rank r's token t, or -1 where the id is outside
+ *     [0, nexperts) or the row would be past the capacity;
+ *   offsets[d][i], i <= nexperts/nranks: where rank d's expert i begins, and
+ *     last the end of the last one (at most `capacity`).
+ * A token may choose an expert twice; it is sent twice then.
+ *   nexperts <= VC_ROUTE_MAX_EXPERTS, topk <= VC_ROUTE_MAX_TOPK,
+ *   nranks*rows*topk and nranks*capacity <= 2^31 - 1, capacity >= 1.
+ * With rows = 0 the offsets are set to 0.
+ */
+vc_status_t vc_dispatch_plan(const int32_t* const* ids, int32_t* const* slots, int32_t* const* offsets, int nranks,
+                             size_t rows, int topk, int nexperts, size_t capacity, vc_stream_t stream);
+
+/*
+ * Tokens to their experts' ranks: for every slots[r][t*topk + j] = d*capacity
+ * + p >= 0, row p of recv[d] = row t of send[r], and recv_scale[d][p] =
+ * scale[r][t] where scale is not NULL.  Rows that no slot names keep what they
+ * hold.  Slots outside [0, nranks*capacity) are skipped; two equal slots (never
+ * from a plan) leave either row.
+ *   send[r]: rows*hidden; recv[d]: capacity*hidden; scale, recv_scale: fp32,
+ *   both or neither.  dtype: also VC_INT8.
+ * The gradient is vc_combine of recv's gradient with weights NULL.
+ */
+vc_status_t vc_dispatch(const void* const* send, const float* const* scale, const int32_t* const* slots,
+                        void* const* recv, float* const* recv_scale, int nranks, size_t rows, size_t hidden, int topk,
+                        size_t capacity, vc_dtype_t dtype, vc_stream_t stream);
+
+/*
+ * The experts' answers back to the tokens: out[r][t] = sum over j, in order,
+ * of weights[r][t*topk + j] * (row p of recv[d]), in fp32, over the slots as
+ * in vc_dispatch; 0 for a token without one.  weights (fp32): NULL for 1.
+ * A skipped slot's weight and rows are not read.
+ */
+vc_status_t vc_combine(const void* const* recv, const int32_t* const* slots, const float* const* weights,
+                       void* const* out, int nranks, size_t rows, size_t hidden, int topk, size_t capacity,
+                       vc_dtype_t dtype, vc_stream_t stream);
+
+/*
+ * Its gradient: for every slot taken, row p of drecv[d] = weight * dout[r][t]
+ * and dweights[r][t*topk + j] = sum over i of dout[r][t][i] * recv[d][p][i]
+ * (fp32; 0 for a skipped slot).  Rows of drecv that no slot names keep what
+ * they hold.  weights: NULL for 1.  drecv, dweights: NULL is not written, one
+ * at least is wanted; recv may be NULL without dweights.
+ */
+vc_status_t vc_combine_backward(const void* const* dout, const void* const* recv, const int32_t* const* slots,
+                                const float* const* weights, void* const* drecv, float* const* dweights, int nranks,
+                                size_t rows, size_t hidden, int topk, size_t capacity, vc_dtype_t dtype,
+                                vc_stream_t stream);
 
 /* Library version, major*10000 + minor*100 + patch. */
 int vc_version(void);
