@@ -16,6 +16,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
+import sys
 from typing import Sequence
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -74,12 +76,6 @@ class PlanEntry(ctypes.Structure):
                 ("elem0", ctypes.c_int64)]
 
 
-class RouteHow(ctypes.Structure):
-    _fields_ = [("score", ctypes.c_int), ("topk", ctypes.c_int), ("ngroups", ctypes.c_int),
-                ("topk_groups", ctypes.c_int), ("group_top", ctypes.c_int), ("renormalize", ctypes.c_int),
-                ("scale", ctypes.c_float)]
-
-
 _lib = None
 
 
@@ -102,14 +98,15 @@ def lib() -> ctypes.CDLL:
             "vc_broadcast_pipelined": [P, PP, I, Z, I, I, I, I, V],
             "vc_gather": [PP, P, I, Z, I, I, I, V],
             "vc_reduce": [PP, P, I, Z, I, I, I, I, V],
-            "vc_reduce_scatter_norm": [PP, PP, PP, PP, PP, PP, PP, I, Z, Z, ctypes.c_double, I, I, V],
-            "vc_reduce_scatter_norm_backward": [PP, PP, PP, PP, PP, PP, PP, PP, I, Z, Z, I, V],
-            "vc_route": [PP, PP, PP, PP, I, Z, I, ctypes.POINTER(RouteHow), I, V],
-            "vc_route_backward": [PP, PP, PP, PP, I, Z, I, ctypes.POINTER(RouteHow), I, V],
-            "vc_dispatch_plan": [PP, PP, PP, I, Z, I, I, Z, V],
-            "vc_dispatch": [PP, PP, PP, PP, PP, I, Z, Z, I, Z, I, V],
-            "vc_combine": [PP, PP, PP, PP, I, Z, Z, I, Z, I, V],
-            "vc_combine_backward": [PP, PP, PP, PP, PP, PP, I, Z, Z, I, Z, I, V],
+            # pointer arrays as packed bytes
+            "vc_reduce_scatter_norm": [V, V, V, V, V, V, V, I, Z, Z, ctypes.c_double, I, I, V],
+            "vc_reduce_scatter_norm_backward": [V, V, V, V, V, V, V, V, I, Z, Z, I, V],
+            "vc_route": [V, V, V, V, I, Z, I, V, I, V],
+            "vc_route_backward": [V, V, V, V, I, Z, I, V, I, V],
+            "vc_dispatch_plan": [V, V, V, I, Z, I, I, Z, V],
+            "vc_dispatch": [V, V, V, V, V, I, Z, Z, I, Z, I, V],
+            "vc_combine": [V, V, V, V, I, Z, Z, I, Z, I, V],
+            "vc_combine_backward": [V, V, V, V, V, V, I, Z, Z, I, Z, I, V],
         }.items():
             f = getattr(L, name)
             f.argtypes = args
@@ -350,64 +347,90 @@ def vc_reduce(send, recv_root, root=0, algo="fused", op="sum", stream=None) -> N
 # contiguous tensor whose first dimension is the ranks (rank r's buffer is its
 # slice r).  Sizes come from the tensors' shapes.
 
+# Pointer arrays go to the library as packed bytes, and the checks compare
+# attributes in place: the smallest calls spend most of their time here, and a
+# ctypes array per argument took twice as long.
+
+_PACK: dict = {}
+
+
 def _invalid(msg: str):
     return VCError(VC_ERR_INVALID_ARG, msg)
 
 
-def _any(a):
-    """A tensor of a per-rank argument to take the dtype and device from."""
-    return a[0] if isinstance(a, (list, tuple)) else a
+def _refuse(x, what: str, shape: tuple, dtype, dev: int):
+    raise _invalid(f"{what}: want contiguous {tuple(shape)} {dtype} on cuda:{dev}, not {tuple(x.shape)} {x.dtype} on "
+                   f"{x.device}" + ("" if x.is_contiguous() else " (not contiguous)"))
 
 
-def _per_rank(a, N: int, what: str, shape: tuple, dtype, dev: int, shared: bool = False):
-    """The pointer array of a per-rank argument (None stays None): each rank's
-    tensor contiguous, of `shape` and `dtype`, on device `dev`.  `shared`: one
-    tensor of `shape` may stand for every rank."""
-    if a is None:
-        return None
-    if not isinstance(a, (list, tuple)):
-        whole = (N, *shape)
-        same = shared and tuple(a.shape) == shape
-        if CHECK_TENSORS and ((tuple(a.shape) != whole and not same) or a.dtype is not dtype or a.get_device() != dev
-                              or not a.is_contiguous()):
-            raise _invalid(f"{what}: want contiguous {whole} {dtype} on cuda:{dev}, not {tuple(a.shape)} {a.dtype} "
-                           f"on {a.device}" + ("" if a.is_contiguous() else " (not contiguous)"))
-        p = a.data_ptr()
-        if same:
-            return _ptr_array([p] * N)
-        n = a.element_size()
-        for s in shape:
-            n *= s
-        return _ptr_array([p + r * n for r in range(N)])
-    if len(a) != N:
-        raise _invalid(f"{what}: {len(a)} tensors for {N} ranks")
-    if CHECK_TENSORS:
-        for x in a:
-            if tuple(x.shape) != shape or x.dtype is not dtype or x.get_device() != dev or not x.is_contiguous():
-                raise _invalid(f"{what}: want contiguous {shape} {dtype} on cuda:{dev}, not {tuple(x.shape)} {x.dtype} "
-                               f"on {x.device}" + ("" if x.is_contiguous() else " (not contiguous)"))
-    return _ptr_array([x.data_ptr() for x in a])
+def _bad(x, shape, dtype, dev) -> bool:
+    return x.shape != shape or x.dtype is not dtype or x.get_device() != dev or not x.is_contiguous()
 
 
-def _device(t) -> int:
-    dev = t.get_device()
-    if dev < 0:
-        raise _invalid(f"tensors must be on a CUDA device, not {t.device}")
-    return dev
-
-
-def _dims(a, n: int, what: str) -> tuple:
-    """The shape of each rank's tensor of a per-rank argument."""
-    shape = tuple(a[0].shape) if isinstance(a, (list, tuple)) else tuple(a.shape[1:])
-    if len(shape) != n:
-        raise _invalid(f"{what}: want {n} dimensions for each rank, not {shape}")
+def _shape(a, n: int, what: str) -> tuple:
+    """(ranks, the n dimensions of each rank's tensor) of a per-rank argument."""
+    shape = (len(a), *a[0].shape) if a.__class__ in (list, tuple) else a.shape
+    if len(shape) != n + 1:
+        raise _invalid(f"{what}: want {n} dimensions for each rank, not {tuple(shape[1:])}")
     return shape
 
 
-def _torch():
-    import torch
+def _start(a):
+    """What a call's checks go by: a tensor of the per-rank argument, its
+    dtype, element size and CUDA device."""
+    x = a[0] if a.__class__ in (list, tuple) else a
+    dev = x.get_device()
+    if dev < 0:
+        raise _invalid(f"tensors must be on a CUDA device, not {x.device}")
+    dt = x.dtype
+    return x, dt, dt.itemsize, dev
 
-    return torch
+
+def _ptrs(a, what: str, full: tuple, size: int, dtype, dev: int):
+    """The pointer array of a per-rank argument (None stays None): `full` is
+    the shape of all ranks' tensors stacked, `size` the bytes of each rank's."""
+    if a is None:
+        return None
+    N = full[0]
+    pack = _PACK.get(N)
+    if pack is None:
+        pack = _PACK[N] = struct.Struct(f"={N}Q").pack
+    if a.__class__ in (list, tuple):
+        if len(a) != N:
+            raise _invalid(f"{what}: {len(a)} tensors for {N} ranks")
+        if CHECK_TENSORS:
+            for x in a:
+                if _bad(x, full[1:], dtype, dev):
+                    _refuse(x, what, full[1:], dtype, dev)
+        return pack(*[x.data_ptr() for x in a])
+    if CHECK_TENSORS and (a.shape != full or a.dtype is not dtype or a.get_device() != dev or not a.is_contiguous()):
+        _refuse(a, what, full, dtype, dev)
+    p = a.data_ptr()
+    return pack(*range(p, p + N * size, size)) if size else bytes(8 * N)
+
+
+def _shared(a, what: str, full: tuple, size: int, dtype, dev: int):
+    """As _ptrs, or one tensor that stands for every rank."""
+    if a is None or a.__class__ in (list, tuple) or len(a.shape) == len(full):
+        return _ptrs(a, what, full, size, dtype, dev)
+    if CHECK_TENSORS and _bad(a, full[1:], dtype, dev):
+        _refuse(a, what, full[1:], dtype, dev)
+    return a.data_ptr().to_bytes(8, sys.byteorder) * full[0]
+
+
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
+
+
+_pack_how = struct.Struct("=6if").pack  # vc_route_t: score, topk, ngroups, topk_groups, group_top, renormalize, scale
 
 
 def vc_reduce_scatter_norm(send, weight, out, residual=None, residual_out=None, scale=None, rstd=None,
@@ -420,23 +443,22 @@ def vc_reduce_scatter_norm(send, weight, out, residual=None, residual_out=None, 
     ``residual_out[r]`` (which may be the residual), 1/rms to ``rstd[r]``
     (rows,) fp32."""
     torch = _torch()
-    N, x = len(send), _any(send)
-    dev = _device(x)
-    rows, hidden = _dims(out, 2, "out")
-    dt, i8 = x.dtype, _any(out).dtype is torch.int8
-    row = (rows, hidden)
+    x, dt, es, dev = _start(send)
+    N, rows, hidden = row = tuple(_shape(out, 2, "out"))
+    odt = (out[0] if out.__class__ in (list, tuple) else out).dtype
+    code, i8, f32 = _dtype_code(x), odt is torch.int8, torch.float32
     if i8 and scale is None:
         raise _invalid("an int8 output wants a scale")
+    size, one = rows * hidden * es, (N, rows)
     check(lib().vc_reduce_scatter_norm(
-        _per_rank(send, N, "send", (N * rows, hidden), dt, dev),
-        _per_rank(residual, N, "residual", row, dt, dev),
-        _per_rank(weight, N, "weight", (hidden,), dt, dev, shared=True),
-        _per_rank(residual_out, N, "residual_out", row, dt, dev),
-        _per_rank(out, N, "out", row, torch.int8 if i8 else dt, dev),
-        _per_rank(scale, N, "scale", (rows,), torch.float32, dev) if i8 else None,
-        _per_rank(rstd, N, "rstd", (rows,), torch.float32, dev),
-        N, rows, hidden, float(eps), _dtype_code(x), DTYPES["i8"] if i8 else _dtype_code(x),
-        _stream_handle(stream, x)))
+        _ptrs(send, "send", (N, N * rows, hidden), N * size, dt, dev),
+        _ptrs(residual, "residual", row, size, dt, dev),
+        _shared(weight, "weight", (N, hidden), hidden * es, dt, dev),
+        _ptrs(residual_out, "residual_out", row, size, dt, dev),
+        _ptrs(out, "out", row, rows * hidden if i8 else size, torch.int8 if i8 else dt, dev),
+        _ptrs(scale, "scale", one, rows * 4, f32, dev) if i8 else None,
+        _ptrs(rstd, "rstd", one, rows * 4, f32, dev),
+        N, rows, hidden, eps, code, DTYPES["i8"] if i8 else code, _stream_handle(stream, x)))
 
 
 def vc_reduce_scatter_norm_backward(dout, h, weight, rstd, dsend=None, dresidual=None, dweight=None,
@@ -446,20 +468,19 @@ def vc_reduce_scatter_norm_backward(dout, h, weight, rstd, dsend=None, dresidual
     ``dsend[q]`` (N * rows, hidden), ``dresidual[r]`` (rows, hidden) and
     ``dweight[r]`` (hidden,) fp32, this rank's part, are written where given;
     ``dresidual_out`` is the gradient that reaches the sum itself."""
-    torch = _torch()
-    N, x = len(dout), _any(dout)
-    dev = _device(x)
-    rows, hidden = _dims(dout, 2, "dout")
-    dt, row = x.dtype, (rows, hidden)
+    x, dt, es, dev = _start(dout)
+    f32 = _torch().float32
+    N, rows, hidden = row = tuple(_shape(dout, 2, "dout"))
+    size = rows * hidden * es
     check(lib().vc_reduce_scatter_norm_backward(
-        _per_rank(dout, N, "dout", row, dt, dev),
-        _per_rank(dresidual_out, N, "dresidual_out", row, dt, dev),
-        _per_rank(h, N, "h", row, dt, dev),
-        _per_rank(weight, N, "weight", (hidden,), dt, dev, shared=True),
-        _per_rank(rstd, N, "rstd", (rows,), torch.float32, dev),
-        _per_rank(dsend, N, "dsend", (N * rows, hidden), dt, dev),
-        _per_rank(dresidual, N, "dresidual", row, dt, dev),
-        _per_rank(dweight, N, "dweight", (hidden,), torch.float32, dev),
+        _ptrs(dout, "dout", row, size, dt, dev),
+        _ptrs(dresidual_out, "dresidual_out", row, size, dt, dev),
+        _ptrs(h, "h", row, size, dt, dev),
+        _shared(weight, "weight", (N, hidden), hidden * es, dt, dev),
+        _ptrs(rstd, "rstd", (N, rows), rows * 4, f32, dev),
+        _ptrs(dsend, "dsend", (N, N * rows, hidden), N * size, dt, dev),
+        _ptrs(dresidual, "dresidual", row, size, dt, dev),
+        _ptrs(dweight, "dweight", (N, hidden), hidden * 4, f32, dev),
         N, rows, hidden, _dtype_code(x), _stream_handle(stream, x)))
 
 
@@ -470,18 +491,17 @@ def vc_route(logits, ids, weights, bias=None, score="softmax", ngroups: int = 1,
 
     ``bias`` is (experts,) fp32 for each rank or one for all."""
     torch = _torch()
-    N, x = len(logits), _any(logits)
-    dev = _device(x)
-    rows, experts = _dims(logits, 2, "logits")
-    topk = _dims(ids, 2, "ids")[1]
-    how = RouteHow(_code(SCORES, score), topk, int(ngroups), int(topk_groups), int(group_top), int(bool(renormalize)),
-                   float(scale))
+    x, dt, es, dev = _start(logits)
+    N, rows, experts = every = tuple(_shape(logits, 2, "logits"))
+    topk = _shape(ids, 2, "ids")[2]
+    chosen, size = (N, rows, topk), rows * topk * 4
+    how = _pack_how(_code(SCORES, score), topk, ngroups, topk_groups, group_top, bool(renormalize), scale)
     check(lib().vc_route(
-        _per_rank(logits, N, "logits", (rows, experts), x.dtype, dev),
-        _per_rank(bias, N, "bias", (experts,), torch.float32, dev, shared=True),
-        _per_rank(ids, N, "ids", (rows, topk), torch.int32, dev),
-        _per_rank(weights, N, "weights", (rows, topk), torch.float32, dev),
-        N, rows, experts, ctypes.byref(how), _dtype_code(x), _stream_handle(stream, x)))
+        _ptrs(logits, "logits", every, rows * experts * es, dt, dev),
+        _shared(bias, "bias", (N, experts), experts * 4, torch.float32, dev),
+        _ptrs(ids, "ids", chosen, size, torch.int32, dev),
+        _ptrs(weights, "weights", chosen, size, torch.float32, dev),
+        N, rows, experts, how, _dtype_code(x), _stream_handle(stream, x)))
 
 
 def vc_route_backward(dweights, logits, ids, dlogits, score="softmax", renormalize: bool = True, scale: float = 1.0,
@@ -489,17 +509,17 @@ def vc_route_backward(dweights, logits, ids, dlogits, score="softmax", renormali
     """``dlogits[r]`` (rows, experts) from ``dweights[r]`` (rows, topk) fp32,
     with vc_route's logits and ids."""
     torch = _torch()
-    N, x = len(logits), _any(logits)
-    dev = _device(x)
-    rows, experts = _dims(logits, 2, "logits")
-    topk = _dims(ids, 2, "ids")[1]
-    how = RouteHow(_code(SCORES, score), topk, 1, 1, 1, int(bool(renormalize)), float(scale))
+    x, dt, es, dev = _start(logits)
+    N, rows, experts = every = tuple(_shape(logits, 2, "logits"))
+    topk = _shape(ids, 2, "ids")[2]
+    chosen, size = (N, rows, topk), rows * topk * 4
+    how = _pack_how(_code(SCORES, score), topk, 1, 1, 1, bool(renormalize), scale)
     check(lib().vc_route_backward(
-        _per_rank(dweights, N, "dweights", (rows, topk), torch.float32, dev),
-        _per_rank(logits, N, "logits", (rows, experts), x.dtype, dev),
-        _per_rank(ids, N, "ids", (rows, topk), torch.int32, dev),
-        _per_rank(dlogits, N, "dlogits", (rows, experts), x.dtype, dev),
-        N, rows, experts, ctypes.byref(how), _dtype_code(x), _stream_handle(stream, x)))
+        _ptrs(dweights, "dweights", chosen, size, torch.float32, dev),
+        _ptrs(logits, "logits", every, rows * experts * es, dt, dev),
+        _ptrs(ids, "ids", chosen, size, torch.int32, dev),
+        _ptrs(dlogits, "dlogits", every, rows * experts * es, dt, dev),
+        N, rows, experts, how, _dtype_code(x), _stream_handle(stream, x)))
 
 
 def vc_dispatch_plan(ids, slots, offsets, capacity: int, stream=None) -> None:
@@ -507,18 +527,17 @@ def vc_dispatch_plan(ids, slots, offsets, capacity: int, stream=None) -> None:
     ``offsets[d]`` (experts of a rank + 1,) int32, where rank d's experts'
     rows begin, from ``ids[r]`` (rows, topk) int32.  ``capacity`` rows a rank
     at most."""
-    torch = _torch()
-    N, x = len(ids), _any(ids)
-    dev = _device(x)
-    rows, topk = _dims(ids, 2, "ids")
-    each = _dims(offsets, 1, "offsets")[0] - 1
-    if capacity < 1:
-        raise _invalid("capacity must be at least 1")
+    i32 = _torch().int32
+    x, _, _, dev = _start(ids)
+    N, rows, topk = chosen = tuple(_shape(ids, 2, "ids"))
+    ends = _shape(offsets, 1, "offsets")[1]
+    if capacity < 1 or ends < 1:
+        raise _invalid("capacity and the offsets' length must be at least 1")
     check(lib().vc_dispatch_plan(
-        _per_rank(ids, N, "ids", (rows, topk), torch.int32, dev),
-        _per_rank(slots, N, "slots", (rows, topk), torch.int32, dev),
-        _per_rank(offsets, N, "offsets", (each + 1,), torch.int32, dev),
-        N, rows, topk, each * N, int(capacity), _stream_handle(stream, x)))
+        _ptrs(ids, "ids", chosen, rows * topk * 4, i32, dev),
+        _ptrs(slots, "slots", chosen, rows * topk * 4, i32, dev),
+        _ptrs(offsets, "offsets", (N, ends), ends * 4, i32, dev),
+        N, rows, topk, (ends - 1) * N, capacity, _stream_handle(stream, x)))
 
 
 def vc_dispatch(send, slots, recv, scale=None, recv_scale=None, stream=None) -> None:
@@ -526,18 +545,16 @@ def vc_dispatch(send, slots, recv, scale=None, recv_scale=None, stream=None) -> 
     (capacity, hidden), and ``scale[r]`` (rows,) fp32 to ``recv_scale[d]``
     (capacity,) where given.  fp32, bf16, fp16 or int8 rows."""
     torch = _torch()
-    N, x = len(send), _any(send)
-    dev = _device(x)
-    rows, hidden = _dims(send, 2, "send")
-    topk, cap = _dims(slots, 2, "slots")[1], _dims(recv, 2, "recv")[0]
+    x, dt, es, dev = _start(send)
+    N, rows, hidden = row = tuple(_shape(send, 2, "send"))
+    topk, cap = _shape(slots, 2, "slots")[2], _shape(recv, 2, "recv")[1]
     check(lib().vc_dispatch(
-        _per_rank(send, N, "send", (rows, hidden), x.dtype, dev),
-        _per_rank(scale, N, "scale", (rows,), torch.float32, dev),
-        _per_rank(slots, N, "slots", (rows, topk), torch.int32, dev),
-        _per_rank(recv, N, "recv", (cap, hidden), x.dtype, dev),
-        _per_rank(recv_scale, N, "recv_scale", (cap,), torch.float32, dev),
-        N, rows, hidden, topk, cap, DTYPES["i8"] if x.dtype is torch.int8 else _dtype_code(x),
-        _stream_handle(stream, x)))
+        _ptrs(send, "send", row, rows * hidden * es, dt, dev),
+        _ptrs(scale, "scale", (N, rows), rows * 4, torch.float32, dev),
+        _ptrs(slots, "slots", (N, rows, topk), rows * topk * 4, torch.int32, dev),
+        _ptrs(recv, "recv", (N, cap, hidden), cap * hidden * es, dt, dev),
+        _ptrs(recv_scale, "recv_scale", (N, cap), cap * 4, torch.float32, dev),
+        N, rows, hidden, topk, cap, DTYPES["i8"] if dt is torch.int8 else _dtype_code(x), _stream_handle(stream, x)))
 
 
 def vc_combine(recv, slots, out, weights=None, stream=None) -> None:
@@ -545,15 +562,15 @@ def vc_combine(recv, slots, out, weights=None, stream=None) -> None:
     hidden), weighted by ``weights[r]`` (rows, topk) fp32 (1 where None) and
     summed.  With the gradient of recv and no weights: dispatch's gradient."""
     torch = _torch()
-    N, x = len(out), _any(out)
-    dev = _device(x)
-    rows, hidden = _dims(out, 2, "out")
-    topk, cap = _dims(slots, 2, "slots")[1], _dims(recv, 2, "recv")[0]
+    x, dt, es, dev = _start(out)
+    N, rows, hidden = row = tuple(_shape(out, 2, "out"))
+    topk, cap = _shape(slots, 2, "slots")[2], _shape(recv, 2, "recv")[1]
+    chosen, size = (N, rows, topk), rows * topk * 4
     check(lib().vc_combine(
-        _per_rank(recv, N, "recv", (cap, hidden), x.dtype, dev),
-        _per_rank(slots, N, "slots", (rows, topk), torch.int32, dev),
-        _per_rank(weights, N, "weights", (rows, topk), torch.float32, dev),
-        _per_rank(out, N, "out", (rows, hidden), x.dtype, dev),
+        _ptrs(recv, "recv", (N, cap, hidden), cap * hidden * es, dt, dev),
+        _ptrs(slots, "slots", chosen, size, torch.int32, dev),
+        _ptrs(weights, "weights", chosen, size, torch.float32, dev),
+        _ptrs(out, "out", row, rows * hidden * es, dt, dev),
         N, rows, hidden, topk, cap, _dtype_code(x), _stream_handle(stream, x)))
 
 
@@ -562,20 +579,20 @@ def vc_combine_backward(dout, recv, slots, weights=None, drecv=None, dweights=No
     ``dweights[r]`` (rows, topk) fp32, where given.  ``recv`` may be None
     without dweights."""
     torch = _torch()
-    N, x = len(dout), _any(dout)
-    dev = _device(x)
-    rows, hidden = _dims(dout, 2, "dout")
-    topk = _dims(slots, 2, "slots")[1]
+    x, dt, es, dev = _start(dout)
+    N, rows, hidden = row = tuple(_shape(dout, 2, "dout"))
     if recv is None and drecv is None:
         raise _invalid("no gradient is asked for")
-    cap = _dims(recv if recv is not None else drecv, 2, "recv")[0]
+    topk, cap = _shape(slots, 2, "slots")[2], _shape(recv if recv is not None else drecv, 2, "recv")[1]
+    chosen, size = (N, rows, topk), rows * topk * 4
+    there, bulk = (N, cap, hidden), cap * hidden * es
     check(lib().vc_combine_backward(
-        _per_rank(dout, N, "dout", (rows, hidden), x.dtype, dev),
-        _per_rank(recv, N, "recv", (cap, hidden), x.dtype, dev),
-        _per_rank(slots, N, "slots", (rows, topk), torch.int32, dev),
-        _per_rank(weights, N, "weights", (rows, topk), torch.float32, dev),
-        _per_rank(drecv, N, "drecv", (cap, hidden), x.dtype, dev),
-        _per_rank(dweights, N, "dweights", (rows, topk), torch.float32, dev),
+        _ptrs(dout, "dout", row, rows * hidden * es, dt, dev),
+        _ptrs(recv, "recv", there, bulk, dt, dev),
+        _ptrs(slots, "slots", chosen, size, torch.int32, dev),
+        _ptrs(weights, "weights", chosen, size, torch.float32, dev),
+        _ptrs(drecv, "drecv", there, bulk, dt, dev),
+        _ptrs(dweights, "dweights", chosen, size, torch.float32, dev),
         N, rows, hidden, topk, cap, _dtype_code(x), _stream_handle(stream, x)))
 
 

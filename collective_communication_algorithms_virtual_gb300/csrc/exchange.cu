@@ -32,10 +32,14 @@ struct DispatchPlanParams {
   uint32_t total;     // of all ranks
   uint32_t piece;     // of each warp, a multiple of 32
   int experts, each;  // experts, and of each rank
+  int bits;           // of the largest expert
   uint32_t capacity;
 };
 
-size_t plan_smem(int experts) { return static_cast<size_t>(experts) * (kPlanWarps + 3) * sizeof(uint32_t); }
+constexpr int kPlanRow = kPlanWarps + 1;  // counts of one expert, a bank apart from the next expert's
+constexpr int kPlanAhead = 4;             // choices of a lane whose loads are in flight together
+
+size_t plan_smem(int experts) { return static_cast<size_t>(experts) * (kPlanRow + 3) * sizeof(uint32_t); }
 
 // The choices, in order of (source rank, token, choice), are cut into one
 // contiguous piece per warp.  Each warp counts its piece by expert; the counts
@@ -47,11 +51,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   __shared__ uint32_t part[32];
   cg::cluster_group cluster = cg::this_cluster();
   const int E = p.experts, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t* count = sm + warp * E;              // [warps][E]: this warp's row
-  uint32_t* total = sm + kPlanWarps * E;        // [E]: this block's counts
+  uint32_t* count = sm + warp;                  // [E] of stride kPlanRow: this warp's counts
+  uint32_t* total = sm + kPlanRow * E;          // [E]: this block's counts
   uint32_t* first = total + E;                  // [E]: where the expert begins, over all ranks
   uint32_t* base = first + E;                   // [E]: row of this block's first choice of the expert
-  for (int i = tid; i < kPlanWarps * E; i += kPlanThreads) sm[i] = 0;
+  for (int i = tid; i < kPlanRow * E; i += kPlanThreads) sm[i] = 0;
   __syncthreads();
   stream_order();
   const uint32_t lo = (cluster.block_rank() * kPlanWarps + warp) * p.piece;
@@ -62,21 +66,25 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     const int e = p.ids[r][a - r * p.per];
     return e >= 0 && e < E ? e : -1;
   };
-  for (uint32_t a = lo; a < hi; a += 32) {
-    const int e = expert(a + lane);
-    const unsigned same = __match_any_sync(kAll, e);
-    if (e >= 0 && lane == __ffs(same) - 1) count[e] += __popc(same);
-    __syncwarp();
+  for (uint32_t a = lo; a < hi; a += 32 * kPlanAhead) {
+    int e[kPlanAhead];
+#pragma unroll
+    for (int i = 0; i < kPlanAhead; ++i) e[i] = expert(a + i * 32 + lane);
+#pragma unroll
+    for (int i = 0; i < kPlanAhead; ++i)
+      if (e[i] >= 0) atomicAdd(count + e[i] * kPlanRow, 1u);  // this warp's own count: whole numbers, in any order
   }
   __syncthreads();
-  uint32_t sum = 0;
-  if (tid < E) {
-    for (int w = 0; w < kPlanWarps; ++w) {
-      const uint32_t n = sm[w * E + tid];
-      sm[w * E + tid] = sum;
-      sum += n;
+  for (int e = warp; e < E; e += kPlanWarps) {  // lane w: what the warps before w counted
+    const uint32_t n = sm[e * kPlanRow + lane];
+    uint32_t upto = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t m = __shfl_up_sync(kAll, upto, d);
+      if (lane >= d) upto += m;
     }
-    total[tid] = sum;
+    sm[e * kPlanRow + lane] = upto - n;
+    if (lane == 31) total[e] = upto;
   }
   cluster.sync();
   uint32_t before = 0, all = 0;
@@ -118,18 +126,30 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
   }
   __syncthreads();
-  for (uint32_t a = lo; a < hi; a += 32) {
-    const int e = expert(a + lane);
-    const unsigned same = __match_any_sync(kAll, e);
-    uint32_t row = 0;
-    if (e >= 0) row = base[e] + count[e] + __popc(same & ((1u << lane) - 1));
-    __syncwarp();
-    if (e >= 0 && lane == __ffs(same) - 1) count[e] += __popc(same);
-    __syncwarp();
-    if (a + lane < hi) {
-      const uint32_t r = (a + lane) / p.per;
-      p.slots[r][a + lane - r * p.per] =
-          e >= 0 && row < p.capacity ? static_cast<int32_t>(static_cast<uint32_t>(e / p.each) * p.capacity + row) : -1;
+  for (uint32_t a = lo; a < hi; a += 32 * kPlanAhead) {
+    int e[kPlanAhead];
+#pragma unroll
+    for (int i = 0; i < kPlanAhead; ++i) e[i] = expert(a + i * 32 + lane);
+#pragma unroll
+    for (int i = 0; i < kPlanAhead; ++i) {
+      const uint32_t at = a + i * 32 + lane;
+      // lanes with the same expert, a ballot for each bit of it
+      unsigned same = __ballot_sync(kAll, e[i] >= 0);
+      for (int b = 0; b < p.bits; ++b) {
+        const bool on = e[i] >> b & 1;
+        const unsigned with = __ballot_sync(kAll, on);
+        same &= on ? with : ~with;
+      }
+      uint32_t row = 0;
+      if (e[i] >= 0) row = base[e[i]] + count[e[i] * kPlanRow] + __popc(same & ((1u << lane) - 1));
+      __syncwarp();
+      if (e[i] >= 0 && lane == __ffs(same) - 1) count[e[i] * kPlanRow] += __popc(same);
+      __syncwarp();
+      if (at < hi) {
+        const uint32_t r = at / p.per;
+        p.slots[r][at - r * p.per] =
+            e[i] >= 0 && row < p.capacity ? static_cast<int32_t>(static_cast<uint32_t>(e[i] / p.each) * p.capacity + row) : -1;
+      }
     }
   }
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // no block ends while its counts are read
@@ -140,7 +160,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
 constexpr int kMoveWarps = kMoveThreads / 32;
-constexpr int kUnits = 4;  // units of a thread in one piece of a row
+constexpr int kUnits = 2;  // 16-byte units of a thread in one piece of a row
+// and of smaller ones
+template <class U>
+constexpr int kUnitsOf = sizeof(U) == 16 ? kUnits : sizeof(U) == 1 ? 16 : 8;
 
 // A slot's rank and row; the address of `width` bytes per row, or null where
 // the slot is skipped.
@@ -162,16 +185,19 @@ struct DispatchParams {
   void* recv[VC_MAX_RANKS];
   float* recv_scale[VC_MAX_RANKS];
   Slots s;
-  int64_t units;  // of a row
-  uint32_t pieces;
+  int64_t n;  // units of a row (bulk copies: bytes)
+  uint32_t pieces, piece_bytes;
   int64_t tiles;  // tokens * pieces
   int has_scale;
 };
 
-// One warp moves one piece (kUnits units a lane) of one token's row to all its
-// places.  U: the unit, 16 bytes or an element.
+// One warp moves one piece of one token's row to all its places.  U: 16-byte
+// vectors, or an element where rows are not made of aligned ones (elements of
+// 2 bytes: 62 us for 4096 tokens, 8 choices, 4099 elements; cutting each
+// place's vectors out of the row, as combine does, took 76).
 template <class U>
 __global__ void __launch_bounds__(kMoveThreads) dispatch_kernel(const __grid_constant__ DispatchParams p) {
+  constexpr int kU = kUnitsOf<U>;
   stream_order();
   const int lane = threadIdx.x & 31;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kMoveWarps;
@@ -179,17 +205,20 @@ __global__ void __launch_bounds__(kMoveThreads) dispatch_kernel(const __grid_con
     const uint32_t token = static_cast<uint32_t>(tile / p.pieces);
     const uint32_t piece = static_cast<uint32_t>(tile - static_cast<int64_t>(token) * p.pieces);
     const uint32_t r = token / p.s.rows, t = token - r * p.s.rows;
-    const int64_t at = static_cast<int64_t>(piece) * 32 * kUnits + lane;
-    const U* from = static_cast<const U*>(p.send[r]) + static_cast<int64_t>(t) * p.units;
-    U v[kUnits];
+    const int64_t at = static_cast<int64_t>(piece) * 32 * kU + lane;
+    const U* from = static_cast<const U*>(p.send[r]) + t * p.n;
+    U v[kU];
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u)
-      if (at + u * 32 < p.units) v[u] = from[at + u * 32];
-    char* to = nullptr;  // lane j: where choice j goes
+    for (int u = 0; u < kU; ++u)
+      if (at + u * 32 < p.n) {
+        if constexpr (sizeof(U) == 16) v[u] = dev::ld16(from + at + u * 32);
+        else v[u] = from[at + u * 32];
+      }
+    U* to = nullptr;  // lane j: where choice j goes
     if (lane < p.s.topk) {
       uint32_t rank, row;
       if (locate(p.s, p.s.slots[r][static_cast<int64_t>(t) * p.s.topk + lane], &rank, &row)) {
-        to = reinterpret_cast<char*>(static_cast<U*>(p.recv[rank]) + static_cast<int64_t>(row) * p.units);
+        to = static_cast<U*>(p.recv[rank]) + row * p.n;
         if (p.has_scale && piece == 0) p.recv_scale[rank][row] = p.scale[r][t];
       }
     }
@@ -197,9 +226,110 @@ __global__ void __launch_bounds__(kMoveThreads) dispatch_kernel(const __grid_con
       U* d = reinterpret_cast<U*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(to), j));
       if (!d) continue;
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u)
-        if (at + u * 32 < p.units) d[at + u * 32] = v[u];
+      for (int u = 0; u < kU; ++u)
+        if (at + u * 32 < p.n) {
+          if constexpr (sizeof(U) == 16) dev::st16(d + at + u * 32, v[u]);
+          else d[at + u * 32] = v[u];
+        }
     }
+  }
+}
+
+// Rows of whole 16-byte vectors by bulk copies: each warp keeps kBulkStages
+// pieces of rows in flight, global to shared memory (lane 0), and lane j writes
+// each landed piece to choice j's place (cp.async.bulk both ways, so no data
+// passes through registers).  A stage is refilled once the stores of the piece
+// it held have read it.  Waits are bounded as in tma_copy_kernel.
+constexpr int kBulkWarps = 4;
+constexpr int kBulkStages = 3;
+constexpr int kBulkBytes = 8 << 10;  // largest piece
+// Taken where it measured faster: long rows to several places, together more
+// than L2 holds (4096 tokens, 8 choices: rows of 8 KB 48.6 us against 53.9
+// through registers, 4 KB 25.0 against 28.9, 2 KB 12.9 against 7.8 at 4
+// choices; 512 tokens of 8 KB 7.8 against 6.8).
+constexpr int64_t kBulkMinRow = 4 << 10, kBulkMinBytes = int64_t(128) << 20;
+constexpr int kBulkMinChoices = 4;
+constexpr size_t kBulkSmem = static_cast<size_t>(kBulkWarps) * kBulkStages * kBulkBytes;
+
+__global__ void __launch_bounds__(kBulkWarps * 32) dispatch_bulk_kernel(const __grid_constant__ DispatchParams p) {
+  extern __shared__ __align__(128) unsigned char stages[];
+  __shared__ uint64_t bars[kBulkWarps][kBulkStages];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned char* stage = stages + warp * kBulkStages * kBulkBytes;
+  uint64_t* bar = bars[warp];
+  if (lane == 0) {
+    for (int k = 0; k < kBulkStages; ++k)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(dev::smem_addr(bar + k)) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
+  stream_order();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kBulkWarps + warp;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kBulkWarps;
+  const int64_t n = first < p.tiles ? (p.tiles - first + step - 1) / step : 0;
+  const int64_t width = p.n, piece_bytes = p.piece_bytes;
+  struct Piece {
+    uint32_t r, t, piece, bytes;
+  };
+  const auto piece_of = [&](int64_t i) {
+    const int64_t tile = first + i * step;
+    const uint32_t token = static_cast<uint32_t>(tile / p.pieces);
+    Piece x;
+    x.piece = static_cast<uint32_t>(tile - static_cast<int64_t>(token) * p.pieces);
+    x.r = token / p.s.rows;
+    x.t = token - x.r * p.s.rows;
+    x.bytes = static_cast<uint32_t>(min(piece_bytes, width - x.piece * piece_bytes));
+    return x;
+  };
+  const auto load = [&](int64_t i) {  // lane 0
+    const int k = static_cast<int>(i % kBulkStages);
+    const Piece x = piece_of(i);
+    const char* from = static_cast<const char*>(p.send[x.r]) + static_cast<int64_t>(x.t) * width + x.piece * piece_bytes;
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(dev::smem_addr(bar + k)), "r"(x.bytes) : "memory");
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+                     dev::smem_addr(stage + k * kBulkBytes)),
+                 "l"(from), "r"(x.bytes), "r"(dev::smem_addr(bar + k)), "l"(dev::l2_evict_first())
+                 : "memory");
+  };
+  int64_t issued = min(n, static_cast<int64_t>(kBulkStages));
+  if (lane == 0)
+    for (int64_t i = 0; i < issued; ++i) load(i);
+  bool ok = true;
+  int64_t i = 0;
+  for (; i < n; ++i) {
+    const int k = static_cast<int>(i % kBulkStages);
+    const Piece x = piece_of(i);
+    char* to = nullptr;  // lane j: where choice j goes
+    if (lane < p.s.topk) {
+      uint32_t rank, row;
+      if (locate(p.s, p.s.slots[x.r][static_cast<int64_t>(x.t) * p.s.topk + lane], &rank, &row)) {
+        to = static_cast<char*>(p.recv[rank]) + static_cast<int64_t>(row) * width + x.piece * piece_bytes;
+        if (p.has_scale && x.piece == 0) p.recv_scale[rank][row] = p.scale[x.r][x.t];
+      }
+    }
+    ok = dev::mbar_wait(dev::smem_addr(bar + k), static_cast<uint32_t>(i / kBulkStages & 1));
+    if (!__all_sync(kAll, ok)) {
+      ok = false;
+      break;
+    }
+    if (to)
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to),
+                   "r"(dev::smem_addr(stage + k * kBulkBytes)), "r"(x.bytes)
+                   : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    if (i >= 1 && issued < n) {  // the stage of piece i - 1, once its stores have read it
+      asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) load(issued);
+      ++issued;
+    }
+  }
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  if (!ok && lane == 0) {
+    atomicOr(&dev::g_device_error, 2u);
+    // loads under way land before the block's shared memory is released
+    for (int64_t j = i; j < issued; ++j)
+      dev::mbar_wait(dev::smem_addr(bar + j % kBulkStages), static_cast<uint32_t>(j / kBulkStages & 1));
   }
 }
 
@@ -208,87 +338,82 @@ struct CombineParams {
   const float* weights[VC_MAX_RANKS];
   void* out[VC_MAX_RANKS];
   Slots s;
-  int64_t units;
+  int64_t n;  // elements of a row
   uint32_t pieces;
   int64_t tiles;
   int has_weights;
 };
 
-// One unit of a row in fp32: a 16-byte vector, or an element.
-template <int DT, bool VEC>
-struct Unit {
-  static constexpr int kN = VEC ? El<DT>::kVec : 1;
-  static constexpr int kBytes = VEC ? 16 : El<DT>::kSize;
-  static __device__ __forceinline__ void load(const char* row, int64_t i, float* f) {
-    if constexpr (VEC) El<DT>::widen(dev::ld16(row + i * 16), f);
-    else f[0] = El<DT>::load(row, i);
-  }
-  static __device__ __forceinline__ void store(char* row, int64_t i, const float* f) {
-    if constexpr (VEC) dev::st16_wb(row + i * 16, El<DT>::narrow(f));
-    else El<DT>::store(row, i, f[0]);
-  }
-};
-
-constexpr int kCombineUnits = 2;  // units of a thread in one piece
 constexpr int kCombineBatch = 4;  // choices whose loads are in flight together
 
+// One warp sums one piece of one token's row over its choices, in order.
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kMoveThreads) combine_kernel(const __grid_constant__ CombineParams p) {
-  using X = Unit<DT, VEC>;
+__global__ void __launch_bounds__(kMoveThreads, VEC ? 4 : 2) combine_kernel(const __grid_constant__ CombineParams p) {
+  using E = El<DT>;
+  using R = Row<E::kSize, VEC>;
+  using Out = Span<E::kSize, 16, VEC>;
+  constexpr int kN = E::kVec, kU = kUnits;
+  __shared__ __align__(16) unsigned char room[kMoveWarps][Out::kRoom];
   stream_order();
   const int lane = threadIdx.x & 31;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kMoveWarps;
-  const int64_t width = p.units * X::kBytes;
+  const int count = static_cast<int>((p.n + kN - 1) / kN);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kMoveWarps, width = p.n * E::kSize;
   for (int64_t tile = static_cast<int64_t>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5); tile < p.tiles; tile += step) {
     const uint32_t token = static_cast<uint32_t>(tile / p.pieces);
     const uint32_t piece = static_cast<uint32_t>(tile - static_cast<int64_t>(token) * p.pieces);
     const uint32_t r = token / p.s.rows, t = token - r * p.s.rows;
-    const int64_t at = static_cast<int64_t>(piece) * 32 * kCombineUnits + lane;
-    const char* from = nullptr;  // lane j: choice j's row and weight
+    char* to = static_cast<char*>(p.out[r]) + t * width;
+    const int at = static_cast<int>(piece) * 32 * kU + lane;
+    int rank = -1;  // lane j: choice j's row and weight
+    uint32_t row = 0;
     float weight = 0.f;
     if (lane < p.s.topk) {
-      uint32_t rank, row;
+      uint32_t d;
       const int64_t j = static_cast<int64_t>(t) * p.s.topk + lane;
-      if (locate(p.s, p.s.slots[r][j], &rank, &row)) {
-        from = static_cast<const char*>(p.recv[rank]) + static_cast<int64_t>(row) * width;
+      if (locate(p.s, p.s.slots[r][j], &d, &row)) {
+        rank = static_cast<int>(d);
         weight = p.has_weights ? p.weights[r][j] : 1.f;
       }
     }
-    float sum[kCombineUnits][X::kN];
+    float sum[kU][kN];
 #pragma unroll
-    for (int u = 0; u < kCombineUnits; ++u)
+    for (int u = 0; u < kU; ++u)
 #pragma unroll
-      for (int i = 0; i < X::kN; ++i) sum[u][i] = 0.f;
+      for (int i = 0; i < kN; ++i) sum[u][i] = 0.f;
     for (int j0 = 0; j0 < p.s.topk; j0 += kCombineBatch) {
-      float v[kCombineBatch][kCombineUnits][X::kN], w[kCombineBatch];
+      typename R::Raw v[kCombineBatch][kU];
+      float w[kCombineBatch];
+      const char *recv[kCombineBatch], *s[kCombineBatch];
 #pragma unroll
-      for (int b = 0; b < kCombineBatch; ++b) {  // lanes past topk hold no row
-        const int j = (j0 + b) & 31;
-        const char* s = reinterpret_cast<const char*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(from), j));
+      for (int b = 0; b < kCombineBatch; ++b) {
+        const int j = min(j0 + b, 31);  // lanes past topk hold no row
+        const int d = j0 + b < 32 ? __shfl_sync(kAll, rank, j) : -1;
+        recv[b] = d >= 0 ? static_cast<const char*>(p.recv[d]) : nullptr;
+        s[b] = recv[b] + __shfl_sync(kAll, row, j) * width;
         w[b] = __shfl_sync(kAll, weight, j);
-        if (j0 + b >= p.s.topk) s = nullptr;
+        const R from(s[b], Bytes{recv[b], recv[b] + p.s.capacity * width});
 #pragma unroll
-        for (int u = 0; u < kCombineUnits; ++u) {
-          if (s && at + u * 32 < p.units) {
-            X::load(s, at + u * 32, v[b][u]);
-          } else {
-            if (!s) w[b] = 0.f;
-#pragma unroll
-            for (int i = 0; i < X::kN; ++i) v[b][u][i] = 0.f;
-          }
+        for (int u = 0; u < kU; ++u) {
+          v[b][u] = R::zero();
+          if (recv[b] && at + u * 32 < count) v[b][u] = from.load(at + u * 32);
         }
       }
 #pragma unroll
-      for (int b = 0; b < kCombineBatch; ++b)
+      for (int b = 0; b < kCombineBatch; ++b) {
+        if (!recv[b]) continue;
+        const R from(s[b], Bytes{recv[b], recv[b] + p.s.capacity * width});
 #pragma unroll
-        for (int u = 0; u < kCombineUnits; ++u)
+        for (int u = 0; u < kU; ++u) {
+          if (at + u * 32 >= count) continue;
+          float f[kN];
+          E::widen(from.finish(v[b][u], at + u * 32, p.n), f);
 #pragma unroll
-          for (int i = 0; i < X::kN; ++i) sum[u][i] += w[b] * v[b][u][i];
+          for (int i = 0; i < kN; ++i) sum[u][i] += w[b] * f[i];
+        }
+      }
     }
-    char* to = static_cast<char*>(p.out[r]) + static_cast<int64_t>(t) * width;
 #pragma unroll
-    for (int u = 0; u < kCombineUnits; ++u)
-      if (at + u * 32 < p.units) X::store(to, at + u * 32, sum[u]);
+    for (int u = 0; u < kU; ++u) Out(room[threadIdx.x >> 5], E::narrow(sum[u])).write(to, at - lane + u * 32, p.n);
   }
 }
 
@@ -299,77 +424,97 @@ struct CombineGradParams {
   void* drecv[VC_MAX_RANKS];
   float* dweights[VC_MAX_RANKS];
   Slots s;
-  int64_t units;
+  int64_t n;
   int has_weights, has_drecv, has_dweights;
 };
-constexpr int kGradBatch = 8;  // choices whose dot products are in registers together
+constexpr int kGradBatch = 4;  // choices whose loads are in flight together
 
 // One block takes one token.
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kMoveThreads) combine_grad_kernel(const __grid_constant__ CombineGradParams p) {
-  using X = Unit<DT, VEC>;
+__global__ void __launch_bounds__(kMoveThreads, VEC ? 6 : 4) combine_grad_kernel(const __grid_constant__ CombineGradParams p) {
+  using E = El<DT>;
+  using R = Row<E::kSize, VEC>;
+  using Out = Span<E::kSize, 16, VEC>;
+  constexpr int kN = E::kVec;
   __shared__ const char* from[VC_ROUTE_MAX_TOPK];
+  __shared__ const char* base[VC_ROUTE_MAX_TOPK];
   __shared__ char* to[VC_ROUTE_MAX_TOPK];
   __shared__ float weight[VC_ROUTE_MAX_TOPK];
   __shared__ float dots[kMoveWarps][VC_ROUTE_MAX_TOPK];
+  __shared__ __align__(16) unsigned char room[kMoveWarps][Out::kRoom];
   stream_order();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const uint32_t token = blockIdx.x;
-  const uint32_t r = token / p.s.rows, t = token - r * p.s.rows;
-  const int k = p.s.topk;
-  const int64_t width = p.units * X::kBytes;
+  const uint32_t r = blockIdx.y, t = blockIdx.x;
+  const int k = p.s.topk, count = static_cast<int>((p.n + kN - 1) / kN);
+  const int64_t width = p.n * E::kSize;
   if (warp == 0 && lane < k) {
     uint32_t rank, row;
     const int64_t j = static_cast<int64_t>(t) * k + lane;
     from[lane] = nullptr;
     to[lane] = nullptr;
     if (locate(p.s, p.s.slots[r][j], &rank, &row)) {
-      if (p.has_dweights) from[lane] = static_cast<const char*>(p.recv[rank]) + static_cast<int64_t>(row) * width;
-      if (p.has_drecv) to[lane] = static_cast<char*>(p.drecv[rank]) + static_cast<int64_t>(row) * width;
+      if (p.has_dweights) {
+        base[lane] = static_cast<const char*>(p.recv[rank]);
+        from[lane] = base[lane] + row * width;
+      }
+      if (p.has_drecv) to[lane] = static_cast<char*>(p.drecv[rank]) + row * width;
       weight[lane] = p.has_weights ? p.weights[r][j] : 1.f;
     }
   }
   __syncthreads();
-  const char* dout = static_cast<const char*>(p.dout[r]) + static_cast<int64_t>(t) * width;
+  const char* gradient = static_cast<const char*>(p.dout[r]);
+  const R dout(gradient + t * width, Bytes{gradient, gradient + p.s.rows * width});
+  const auto answer = [&](int j) { return R(from[j], Bytes{base[j], base[j] + p.s.capacity * width}); };
   for (int j0 = 0; j0 < k; j0 += kGradBatch) {
     float dot[kGradBatch];
 #pragma unroll
     for (int b = 0; b < kGradBatch; ++b) dot[b] = 0.f;
-    for (int64_t c = threadIdx.x; c < p.units; c += blockDim.x) {
-      float g[X::kN];
-      X::load(dout, c, g);
+    for (int c0 = warp * 32; c0 < count; c0 += blockDim.x) {  // the warp's 32 units
+      const int c = c0 + lane;
+      typename R::Raw graw = R::zero(), y[kGradBatch];
+      if (c < count) graw = dout.load(c);
 #pragma unroll
       for (int b = 0; b < kGradBatch; ++b) {
-        if (j0 + b < k) {
-          if (from[j0 + b]) {
-            float y[X::kN];
-            X::load(from[j0 + b], c, y);
+        y[b] = R::zero();
+        if (j0 + b < k && from[j0 + b] && c < count) y[b] = answer(j0 + b).load(c);
+      }
+      float g[kN];
 #pragma unroll
-            for (int i = 0; i < X::kN; ++i) dot[b] += g[i] * y[i];
-          }
-          if (to[j0 + b]) {
-            float d[X::kN];
+      for (int i = 0; i < kN; ++i) g[i] = 0.f;
+      if (c < count) E::widen(dout.finish(graw, c, p.n), g);
+      mask_unit<E::kSize, VEC>(c, p.n, g);
 #pragma unroll
-            for (int i = 0; i < X::kN; ++i) d[i] = weight[j0 + b] * g[i];
-            X::store(to[j0 + b], c, d);
-          }
+      for (int b = 0; b < kGradBatch; ++b) {
+        if (j0 + b >= k) break;
+        if (from[j0 + b] && c < count) {
+          float f[kN];
+          E::widen(answer(j0 + b).finish(y[b], c, p.n), f);
+          mask_unit<E::kSize, VEC>(c, p.n, f);
+#pragma unroll
+          for (int i = 0; i < kN; ++i) dot[b] += g[i] * f[i];
+        }
+        if (to[j0 + b]) {
+          float d[kN];
+#pragma unroll
+          for (int i = 0; i < kN; ++i) d[i] = weight[j0 + b] * g[i];
+          Out(room[warp], E::narrow(d)).write(to[j0 + b], c0, p.n);
         }
       }
     }
     if (p.has_dweights) {
 #pragma unroll
       for (int b = 0; b < kGradBatch; ++b) {
-        const float x = warp_sum(dot[b]);
-        if (lane == 0 && j0 + b < k) dots[warp][j0 + b] = x;
+        const float s = warp_sum(dot[b]);
+        if (lane == 0 && j0 + b < k) dots[warp][j0 + b] = s;
       }
     }
   }
   if (p.has_dweights) {
     __syncthreads();
     if (warp == 0 && lane < k) {
-      float x = 0.f;
-      for (int w = 0; w < warps; ++w) x += dots[w][lane];
-      p.dweights[r][static_cast<int64_t>(t) * k + lane] = x;  // a skipped choice's dot is 0
+      float s = 0.f;
+      for (int w = 0; w < warps; ++w) s += dots[w][lane];
+      p.dweights[r][static_cast<int64_t>(t) * k + lane] = from[lane] ? s : 0.f;  // a skipped choice's row was not read
     }
   }
 }
@@ -393,8 +538,14 @@ const void* const* untyped(T* const* a) {
   return reinterpret_cast<const void* const*>(const_cast<const std::remove_const_t<T>* const*>(a));
 }
 
-// Warps of a cluster that sorts `total` choices.
-unsigned plan_blocks(int64_t total) { return total <= 4096 ? 1 : total <= 32768 ? 8 : 16; }
+// Blocks of the cluster that sorts `total` choices: a choice per thread up to
+// 16 (32768 choices: 1 block 66 us, 8 blocks 8.8 us, 16 blocks 7.1 us; 128
+// choices: 1 block 3.8 us, 16 blocks 4.4 us).
+unsigned plan_blocks(int64_t total) {
+  unsigned b = 1;
+  while (b < 16 && total > static_cast<int64_t>(b) * kPlanThreads) b *= 2;
+  return b;
+}
 
 vc_status_t dispatch_plan(const int32_t* const* ids, int32_t* const* slots, int32_t* const* offsets, int nranks,
                           size_t rows, int topk, int nexperts, size_t capacity, cudaStream_t stream) {
@@ -434,6 +585,7 @@ vc_status_t dispatch_plan(const int32_t* const* ids, int32_t* const* slots, int3
   p.piece = static_cast<uint32_t>(((total + warps - 1) / warps + 31) / 32 * 32);
   p.experts = nexperts;
   p.each = static_cast<int>(each);
+  while (nexperts - 1 >> p.bits) ++p.bits;
   p.capacity = static_cast<uint32_t>(capacity);
   return launch<plan_kernel>(dev, Shape{blocks, kPlanThreads, plan_smem(nexperts), blocks}, stream, p, kPlan, 0,
                              total * 8 + (int64_t(nexperts) + nranks) * 4);
@@ -463,11 +615,13 @@ unsigned move_blocks(DeviceState* st, int dev, int64_t tiles) {
 }
 
 template <class U>
-vc_status_t launch_dispatch(DeviceState* st, int dev, DispatchParams& p, int64_t row_bytes, int64_t bytes, cudaStream_t s) {
-  p.units = row_bytes / static_cast<int64_t>(sizeof(U));
-  p.pieces = static_cast<uint32_t>((p.units + 32 * kUnits - 1) / (32 * kUnits));
-  p.tiles = p.tiles * p.pieces;
-  return launch<dispatch_kernel<U>>(dev, Shape{move_blocks<dispatch_kernel<U>>(st, dev, p.tiles), kMoveThreads}, s, p, kDispatch, 0, bytes);
+vc_status_t launch_dispatch(DeviceState* st, int dev, DispatchParams& p, int64_t row, int64_t bytes, cudaStream_t s) {
+  constexpr int64_t kPiece = 32 * kUnitsOf<U>;
+  p.n = row / static_cast<int64_t>(sizeof(U));
+  p.pieces = static_cast<uint32_t>((p.n + kPiece - 1) / kPiece);
+  p.tiles *= p.pieces;
+  return launch<dispatch_kernel<U>>(dev, Shape{move_blocks<dispatch_kernel<U>>(st, dev, p.tiles), kMoveThreads}, s, p, kDispatch, 0,
+                                    bytes);
 }
 
 vc_status_t dispatch(const void* const* send, const float* const* scale, const int32_t* const* slots,
@@ -503,6 +657,15 @@ vc_status_t dispatch(const void* const* send, const float* const* scale, const i
   p.has_scale = scale != nullptr;
   p.tiles = n * nranks;
   const int64_t bytes = p.tiles * (row * (1 + topk) + topk * 4 + (scale ? 4 + 4 * topk : 0));
+  if (whole && row >= kBulkMinRow && topk >= kBulkMinChoices && n * nranks * topk * row >= kBulkMinBytes) {
+    p.n = row;
+    p.pieces = static_cast<uint32_t>((row + kBulkBytes - 1) / kBulkBytes);
+    p.piece_bytes = static_cast<uint32_t>((row / 16 + p.pieces - 1) / p.pieces) * 16;
+    p.tiles *= p.pieces;
+    const int64_t fit = int64_t(st->nsm) * resident_blocks<dispatch_bulk_kernel>(dev, kBulkWarps * 32, kBulkSmem);
+    const Shape shape{static_cast<unsigned>(std::min<int64_t>((p.tiles + kBulkWarps - 1) / kBulkWarps, fit)), kBulkWarps * 32, kBulkSmem};
+    return launch<dispatch_bulk_kernel>(dev, shape, stream, p, kDispatch, 0, bytes);
+  }
   if (whole) return launch_dispatch<uint4>(st, dev, p, row, bytes, stream);
   if (es == 4) return launch_dispatch<uint32_t>(st, dev, p, row, bytes, stream);
   if (es == 2) return launch_dispatch<uint16_t>(st, dev, p, row, bytes, stream);
@@ -542,8 +705,9 @@ vc_status_t combine(const void* const* recv, const int32_t* const* slots, const 
     constexpr int DT = code();
     const auto go = [&](auto vec) {
       constexpr bool VEC = vec();
-      p.units = row / Unit<DT, VEC>::kBytes;
-      p.pieces = static_cast<uint32_t>((p.units + 32 * kCombineUnits - 1) / (32 * kCombineUnits));
+      constexpr int64_t kPiece = 32 * kUnits;
+      p.n = static_cast<int64_t>(hidden);
+      p.pieces = static_cast<uint32_t>((units_of(p.n, es) + kPiece - 1) / kPiece);
       p.tiles = n * nranks * p.pieces;
       return launch<combine_kernel<DT, VEC>>(dev, Shape{move_blocks<combine_kernel<DT, VEC>>(st, dev, p.tiles), kMoveThreads}, stream, p,
                                              kCombine, 0, bytes);
@@ -592,9 +756,11 @@ vc_status_t combine_grad(const void* const* dout, const void* const* recv, const
     constexpr int DT = code();
     const auto go = [&](auto vec) {
       constexpr bool VEC = vec();
-      p.units = row / Unit<DT, VEC>::kBytes;
-      const unsigned threads = static_cast<unsigned>(std::max<int64_t>(32, std::min<int64_t>(kMoveThreads, (p.units + 31) / 32 * 32)));
-      return launch<combine_grad_kernel<DT, VEC>>(dev, Shape{static_cast<unsigned>(n * nranks), threads}, stream, p, kCombineBackward, 0, bytes);
+      p.n = static_cast<int64_t>(hidden);
+      const int64_t units = units_of(p.n, es);
+      const unsigned threads = static_cast<unsigned>(std::max<int64_t>(32, std::min<int64_t>(kMoveThreads, (units + 31) / 32 * 32)));
+      return launch<combine_grad_kernel<DT, VEC>>(dev, Shape{p.s.rows, threads, 0, 1, static_cast<unsigned>(nranks)}, stream, p,
+                                                  kCombineBackward, 0, bytes);
     };
     return whole ? go(std::true_type{}) : go(std::false_type{});
   });

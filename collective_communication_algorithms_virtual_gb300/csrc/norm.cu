@@ -45,92 +45,142 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
   return (a & 255) | (b & 255) << 8 | (c & 255) << 16 | static_cast<uint32_t>(d) << 24;
 }
 
-// One block per row; VPT vectors of the row in each thread.
-template <int DT, int VPT, bool I8>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ NormParams p) {
+// One block per row; VPT units of the row in each thread.
+template <int DT, bool VEC, int VPT, bool I8>
+__global__ void __launch_bounds__(kThreads, VPT <= (VEC ? 2 : 1) ? 2 : 1) norm_kernel(const __grid_constant__ NormParams p) {
   using E = El<DT>;
-  constexpr int kVec = E::kVec;
-  constexpr int kBatch = VPT == 1 ? 8 : VPT == 2 ? 4 : 2;  // ranks whose loads are in flight together
+  constexpr int kN = E::kVec;
+  constexpr int kBatch = (VEC ? 8 : 4) / VPT > 0 ? (VEC ? 8 : 4) / VPT : 1;  // ranks whose loads are in flight together
+  using Out = Span<E::kSize, 16, VEC>;
+  using Quants = Span<1, kN, VEC>;
   __shared__ float part[32];
   __shared__ uint32_t most[32];
+  __shared__ __align__(16) unsigned char room[kThreads / 32][Out::kRoom];
   stream_order();
-  const uint32_t row = blockIdx.x;
-  const uint32_t r = row / p.rows, t = row - r * p.rows;
-  const int nv = p.hidden / kVec;
-  const int64_t at = static_cast<int64_t>(row) * nv;  // the row's first vector in each send buffer
-  const int64_t own = static_cast<int64_t>(t) * nv;   // and in rank r's own buffers
-  float h[VPT][kVec];
+  const uint32_t r = blockIdx.y, t = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = static_cast<int64_t>(r) * p.rows + t;
+  const int64_t width = static_cast<int64_t>(p.hidden) * E::kSize;
+  const int64_t at = row * width;                    // the row's place in each send buffer
+  const int64_t own = static_cast<int64_t>(t) * width;  // and in rank r's own buffers
+  char* sums = p.has_residual_out ? static_cast<char*>(p.residual_out[r]) + own : nullptr;
+  const int nu = (p.hidden + kN - 1) / kN;
+  const int64_t sent = static_cast<int64_t>(p.nranks) * p.rows;
+  const auto row_of = [&](const void* buffer, int64_t at_byte, int64_t rows) {
+    const char* b = static_cast<const char*>(buffer);
+    return Row<E::kSize, VEC>(b + at_byte, Bytes{b, b + rows * width});
+  };
+  const auto residual = row_of(p.has_residual ? p.residual[r] : p.out[r], own, p.rows);
+  const auto weights = row_of(p.weight[r], 0, 1);
+  // the residual and the weight are asked for well before they are used,
+  // where registers allow it
+  constexpr bool kAhead = VPT <= (VEC ? 4 : 2);
+  using R = Row<E::kSize, VEC>;
+  typename R::Raw res[VPT], weight[VPT];
+  const auto load_res = [&] {
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+      const int c = threadIdx.x + u * blockDim.x;
+      res[u] = R::zero();
+      if (p.has_residual && c < nu) res[u] = residual.load_plain(c);
+    }
+  };
+  const auto load_weight = [&] {
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+      const int c = threadIdx.x + u * blockDim.x;
+      weight[u] = R::zero();
+      if (c < nu) weight[u] = weights.load_kept(c);
+    }
+  };
+  if (kAhead) load_res();
+  float h[VPT][kN];
 #pragma unroll
   for (int u = 0; u < VPT; ++u)
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) h[u][i] = 0.f;
+    for (int i = 0; i < kN; ++i) h[u][i] = 0.f;
   for (int q0 = 0; q0 < p.nranks; q0 += kBatch) {
-    uint4 v[kBatch][VPT];
+    typename R::Raw v[kBatch][VPT];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b)
+    for (int b = 0; b < kBatch; ++b) {
+      if (q0 + b >= p.nranks) break;
+      const R from = row_of(p.send[q0 + b], at, sent);
 #pragma unroll
       for (int u = 0; u < VPT; ++u) {
         const int c = threadIdx.x + u * blockDim.x;
-        if (q0 + b < p.nranks && c < nv) v[b][u] = dev::ld16(static_cast<const uint4*>(p.send[q0 + b]) + at + c);
-        else v[b][u] = make_uint4(0, 0, 0, 0);
+        v[b][u] = R::zero();
+        if (c < nu) v[b][u] = from.load(c);
       }
+    }
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b)
+    for (int b = 0; b < kBatch; ++b) {
+      if (q0 + b >= p.nranks) break;
+      const R from = row_of(p.send[q0 + b], at, sent);
 #pragma unroll
       for (int u = 0; u < VPT; ++u) {
-        float f[kVec];
-        E::widen(v[b][u], f);
+        const int c = threadIdx.x + u * blockDim.x;
+        if (c < nu) {
+          float f[kN];
+          E::widen(from.finish(v[b][u], c, p.hidden), f);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) h[u][i] += f[i];
+          for (int i = 0; i < kN; ++i) h[u][i] += f[i];
+        }
       }
+    }
   }
+  if (!kAhead) load_res();
+  if (kAhead) load_weight();
   float ss = 0.f;
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {
     const int c = threadIdx.x + u * blockDim.x;
-    if (c < nv) {
-      if (p.has_residual) {
-        float f[kVec];
-        E::widen(ld16_plain(static_cast<const uint4*>(p.residual[r]) + own + c), f);
+    if (p.has_residual && c < nu) {
+      float f[kN];
+      E::widen(residual.finish(res[u], c, p.hidden), f);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) h[u][i] += f[i];
-      }
-      if (p.has_residual_out) dev::st16_wb(static_cast<uint4*>(p.residual_out[r]) + own + c, E::narrow(h[u]));
+      for (int i = 0; i < kN; ++i) h[u][i] += f[i];
     }
+    mask_unit<E::kSize, VEC>(c, p.hidden, h[u]);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) ss += h[u][i] * h[u][i];
+    for (int i = 0; i < kN; ++i) ss += h[u][i] * h[u][i];
+    if (sums) Out(room[warp], E::narrow(h[u])).write(sums, c - lane, p.hidden);
   }
   const float rs = 1.f / sqrtf(block_sum(ss, part) / static_cast<float>(p.hidden) + p.eps);
   if (p.has_rstd && threadIdx.x == 0) p.rstd[r][t] = rs;
+  if (!kAhead) load_weight();
   uint32_t top = 0;
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {
     const int c = threadIdx.x + u * blockDim.x;
-    if (c < nv) {
-      float w[kVec];
-      E::widen(ld16_plain(static_cast<const uint4*>(p.weight[r]) + c), w);
+    float w[kN];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        h[u][i] = h[u][i] * rs * w[i];
-        top = max(top, __float_as_uint(fabsf(h[u][i])));
+    for (int i = 0; i < kN; ++i) w[i] = 0.f;
+    if (c < nu) E::widen(weights.finish(weight[u], c, p.hidden), w);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) h[u][i] = h[u][i] * rs * w[i];
+    if (I8) {
+      mask_unit<E::kSize, VEC>(c, p.hidden, h[u]);
+      if (c < nu) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) top = max(top, __float_as_uint(fabsf(h[u][i])));
       }
-      if (!I8) dev::st16_wb(static_cast<uint4*>(p.out[r]) + own + c, E::narrow(h[u]));
+    } else {
+      Out(room[warp], E::narrow(h[u])).write(static_cast<char*>(p.out[r]) + own, c - lane, p.hidden);
     }
   }
   if (I8) {
     const Quant quant(block_max_bits(top, most));
     if (threadIdx.x == 0) p.scale[r][t] = quant.scale;
+    int8_t* to = static_cast<int8_t*>(p.out[r]) + static_cast<int64_t>(t) * p.hidden;
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       const int c = threadIdx.x + u * blockDim.x;
-      if (c < nv) {
-        uint32_t w[kVec / 4];
+      uint32_t w[2];
 #pragma unroll
-        for (int i = 0; i < kVec / 4; ++i)
-          w[i] = pack4(quant(h[u][4 * i]), quant(h[u][4 * i + 1]), quant(h[u][4 * i + 2]), quant(h[u][4 * i + 3]));
-        if constexpr (kVec == 8) static_cast<uint2*>(p.out[r])[own + c] = make_uint2(w[0], w[1]);
-        else static_cast<uint32_t*>(p.out[r])[own + c] = w[0];
-      }
+      for (int i = 0; i < kN / 4; ++i)
+        w[i] = pack4(quant(h[u][4 * i]), quant(h[u][4 * i + 1]), quant(h[u][4 * i + 2]), quant(h[u][4 * i + 3]));
+      if constexpr (kN == 8) Quants(room[warp], make_uint2(w[0], w[1])).write(to, c - lane, p.hidden);
+      else Quants(room[warp], w[0]).write(to, c - lane, p.hidden);
     }
   }
 }
@@ -143,9 +193,9 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
   __shared__ float part[32];
   __shared__ uint32_t most[32];
   stream_order();
-  const uint32_t row = blockIdx.x;
-  const uint32_t r = row / p.rows, t = row - r * p.rows;
-  const int64_t at = static_cast<int64_t>(row) * p.hidden, own = static_cast<int64_t>(t) * p.hidden;
+  const uint32_t r = blockIdx.y, t = blockIdx.x;
+  const int64_t row = static_cast<int64_t>(r) * p.rows + t;
+  const int64_t at = row * p.hidden, own = static_cast<int64_t>(t) * p.hidden;
   float ss = 0.f;
   for (int c = threadIdx.x; c < p.hidden; c += blockDim.x) {
     float x = 0.f;
@@ -191,60 +241,89 @@ struct GradParams {
 };
 
 // Block b of rank r takes the rank's rows b, b + per, ...; each thread keeps
-// the weight's gradient of its columns over them.
-template <int DT, int VPT>
+// the weight's gradient of its columns over them (so the columns are fixed, and
+// rows off 16-byte boundaries are written element by element).
+template <int DT, bool VEC, int VPT>
 __global__ void __launch_bounds__(kThreads) norm_grad_kernel(const __grid_constant__ GradParams p) {
   using E = El<DT>;
-  constexpr int kVec = E::kVec;
+  constexpr int kN = E::kVec;
+  using R = Row<E::kSize, VEC>;
+  using Out = Span<E::kSize, 16, VEC>;
   __shared__ float part[2][32];
+  __shared__ __align__(16) unsigned char room[kThreads / 32][Out::kRoom];
   stream_order();
   const uint32_t r = blockIdx.x / p.per, b = blockIdx.x - r * p.per;
-  const int nv = p.hidden / kVec;
-  float dw[VPT][kVec];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nu = (p.hidden + kN - 1) / kN;
+  const int64_t width = static_cast<int64_t>(p.hidden) * E::kSize;
+  const auto row_of = [&](const void* buffer, int64_t at_byte, int64_t rows) {
+    const char* b = static_cast<const char*>(buffer);
+    return R(b + at_byte, Bytes{b, b + rows * width});
+  };
+  const R weights = row_of(p.weight[r], 0, 1);
+  float dw[VPT][kN];
 #pragma unroll
   for (int u = 0; u < VPT; ++u)
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) dw[u][i] = 0.f;
+    for (int i = 0; i < kN; ++i) dw[u][i] = 0.f;
   int flip = 0;
   for (uint32_t t = b; t < p.rows; t += p.per, flip ^= 1) {
-    const int64_t own = static_cast<int64_t>(t) * nv;
-    const float rs = p.rstd[r][t];
-    float g[VPT][kVec], h[VPT][kVec], gh = 0.f;
+    const int64_t own = static_cast<int64_t>(t) * width;
+    const R dout = row_of(p.dout[r], own, p.rows), hs = row_of(p.h[r], own, p.rows),
+            dres = row_of(p.has_dres_out ? p.dres_out[r] : p.h[r], own, p.rows);
+    typename R::Raw graw[VPT], hraw[VPT], draw[VPT], wraw[VPT];
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       const int c = threadIdx.x + u * blockDim.x;
-      if (c < nv) {
-        float w[kVec];
-        E::widen(dev::ld16(static_cast<const uint4*>(p.dout[r]) + own + c), g[u]);
-        E::widen(dev::ld16(static_cast<const uint4*>(p.h[r]) + own + c), h[u]);
-        E::widen(ld16_plain(static_cast<const uint4*>(p.weight[r]) + c), w);
+      graw[u] = hraw[u] = draw[u] = wraw[u] = R::zero();
+      if (c < nu) {
+        graw[u] = dout.load(c);
+        hraw[u] = hs.load(c);
+        wraw[u] = weights.load_kept(c);
+        if (p.has_dres_out) draw[u] = dres.load_plain(c);
+      }
+    }
+    const float rs = p.rstd[r][t];
+    float g[VPT][kN], h[VPT][kN], gh = 0.f;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          dw[u][i] += g[u][i] * h[u][i] * rs;
-          g[u][i] *= w[i];
-          gh += g[u][i] * h[u][i];
-        }
+    for (int u = 0; u < VPT; ++u) {
+      const int c = threadIdx.x + u * blockDim.x;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) g[u][i] = h[u][i] = 0.f;
+      if (c >= nu) continue;
+      float w[kN];
+      E::widen(dout.finish(graw[u], c, p.hidden), g[u]);
+      E::widen(hs.finish(hraw[u], c, p.hidden), h[u]);
+      E::widen(weights.finish(wraw[u], c, p.hidden), w);
+      mask_unit<E::kSize, VEC>(c, p.hidden, g[u]);
+      mask_unit<E::kSize, VEC>(c, p.hidden, h[u]);
+      mask_unit<E::kSize, VEC>(c, p.hidden, w);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        dw[u][i] += g[u][i] * h[u][i] * rs;
+        g[u][i] *= w[i];
+        gh += g[u][i] * h[u][i];
       }
     }
     const float mean = block_sum(gh, part[flip]) / static_cast<float>(p.hidden) * rs * rs;
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       const int c = threadIdx.x + u * blockDim.x;
-      if (c < nv) {
-        float d[kVec];
+      float d[kN];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) d[i] = rs * (g[u][i] - h[u][i] * mean);
-        if (p.has_dres_out) {
-          float f[kVec];
-          E::widen(ld16_plain(static_cast<const uint4*>(p.dres_out[r]) + own + c), f);
+      for (int i = 0; i < kN; ++i) d[i] = rs * (g[u][i] - h[u][i] * mean);
+      if (p.has_dres_out && c < nu) {
+        float f[kN];
+        E::widen(dres.finish(draw[u], c, p.hidden), f);
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) d[i] += f[i];
-        }
-        const uint4 x = E::narrow(d);
-        if (p.has_dres) dev::st16_wb(static_cast<uint4*>(p.dres[r]) + own + c, x);
+        for (int i = 0; i < kN; ++i) d[i] += f[i];
+      }
+      if (p.has_dres || p.has_dsend) {
+        const Out v(room[warp], E::narrow(d));
+        if (p.has_dres) v.write(static_cast<char*>(p.dres[r]) + own, c - lane, p.hidden);
         if (p.has_dsend) {
-          const int64_t at = (static_cast<int64_t>(r) * p.rows + t) * nv + c;
-          for (int q = 0; q < p.nranks; ++q) dev::st16(static_cast<uint4*>(p.dsend[q]) + at, x);
+          const int64_t at = (static_cast<int64_t>(r) * p.rows + t) * width;
+          for (int q = 0; q < p.nranks; ++q) v.template write<true>(static_cast<char*>(p.dsend[q]) + at, c - lane, p.hidden);
         }
       }
     }
@@ -254,10 +333,16 @@ __global__ void __launch_bounds__(kThreads) norm_grad_kernel(const __grid_consta
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       const int c = threadIdx.x + u * blockDim.x;
-      if (c < nv) {
+      if (c < nu) {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < kVec; i += 4)
-          *reinterpret_cast<float4*>(to + c * kVec + i) = make_float4(dw[u][i], dw[u][i + 1], dw[u][i + 2], dw[u][i + 3]);
+          for (int i = 0; i < kN; i += 4)
+            *reinterpret_cast<float4*>(to + c * kN + i) = make_float4(dw[u][i], dw[u][i + 1], dw[u][i + 2], dw[u][i + 3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kN; ++i)
+            if (c * kN + i < p.hidden) to[c * kN + i] = dw[u][i];
+        }
       }
     }
   }
@@ -329,11 +414,11 @@ __global__ void __launch_bounds__(kSumThreads) norm_weight_kernel(const __grid_c
   }
 }
 
-// Vectors a thread holds for a row of nv vectors: the fewest that keep the
-// block within kThreads; 0 where that is more than `most`.
-int vectors_per_thread(int64_t nv, int most) {
+// Units a thread holds for a row of n units: the fewest that keep the block
+// within kThreads; 0 where that is more than `most`.
+int units_per_thread(int64_t n, int most) {
   for (int v = 1; v <= most; v *= 2)
-    if (nv <= static_cast<int64_t>(v) * kThreads) return v;
+    if (n <= static_cast<int64_t>(v) * kThreads) return v;
   return 0;
 }
 unsigned threads_for(int64_t n, int per_thread, int most) {
@@ -343,11 +428,11 @@ unsigned threads_for(int64_t n, int per_thread, int most) {
 // Threads of a block that takes a row element by element.
 unsigned any_threads(int64_t hidden) { return threads_for(hidden, 4, 1024); }
 
-template <int DT, int VPT>
-vc_status_t launch_norm(int dev, unsigned blocks, int64_t nv, bool i8, cudaStream_t s, const NormParams& p, int64_t bytes) {
-  const Shape shape{blocks, threads_for(nv, VPT, kThreads)};
-  return i8 ? launch<norm_kernel<DT, VPT, true>>(dev, shape, s, p, kNorm, 0, bytes)
-            : launch<norm_kernel<DT, VPT, false>>(dev, shape, s, p, kNorm, 0, bytes);
+template <int DT, bool VEC, int VPT>
+vc_status_t launch_norm(int dev, int64_t n, bool i8, cudaStream_t s, const NormParams& p, int64_t bytes) {
+  const Shape shape{p.rows, threads_for(n, VPT, kThreads), 0, 1, static_cast<unsigned>(p.nranks)};
+  return i8 ? launch<norm_kernel<DT, VEC, VPT, true>>(dev, shape, s, p, kNorm, 0, bytes)
+            : launch<norm_kernel<DT, VEC, VPT, false>>(dev, shape, s, p, kNorm, 0, bytes);
 }
 
 vc_status_t norm(const void* const* send, const void* const* residual, const void* const* weight,
@@ -401,18 +486,24 @@ vc_status_t norm(const void* const* send, const void* const* residual, const voi
   const int64_t tokens = static_cast<int64_t>(rows) * nranks;
   const int64_t bytes = n * nranks * (es * (nranks + p.has_residual + p.has_residual_out) + os) +
                         static_cast<int64_t>(hidden) * es * nranks + tokens * 4 * (p.has_rstd + i8);
-  const unsigned blocks = static_cast<unsigned>(tokens);
   return for_dtype(dtype, [&](auto code) {
     constexpr int DT = code();
-    const int64_t nv = static_cast<int64_t>(hidden) / El<DT>::kVec;
-    const bool whole = aligned && hidden % El<DT>::kVec == 0;
-    switch (whole ? vectors_per_thread(nv, 8) : 0) {
-      case 1: return launch_norm<DT, 1>(dev, blocks, nv, i8, stream, p, bytes);
-      case 2: return launch_norm<DT, 2>(dev, blocks, nv, i8, stream, p, bytes);
-      case 4: return launch_norm<DT, 4>(dev, blocks, nv, i8, stream, p, bytes);
-      case 8: return launch_norm<DT, 8>(dev, blocks, nv, i8, stream, p, bytes);
-    }
-    const Shape shape{blocks, any_threads(static_cast<int64_t>(hidden)), hidden * sizeof(float)};
+    const auto go = [&](auto vec) {  // VC_ERR_UNSUPPORTED: too long for registers
+      constexpr bool VEC = vec();
+      const int64_t n = units_of(static_cast<int64_t>(hidden), El<DT>::kSize);
+      switch (units_per_thread(n, VEC ? 8 : 4)) {
+        case 1: return launch_norm<DT, VEC, 1>(dev, n, i8, stream, p, bytes);
+        case 2: return launch_norm<DT, VEC, 2>(dev, n, i8, stream, p, bytes);
+        case 4: return launch_norm<DT, VEC, 4>(dev, n, i8, stream, p, bytes);
+        case 8:
+          if constexpr (VEC) return launch_norm<DT, VEC, 8>(dev, n, i8, stream, p, bytes);
+      }
+      return VC_ERR_UNSUPPORTED;
+    };
+    const vc_status_t rc = aligned && hidden % El<DT>::kVec == 0 ? go(std::true_type{}) : go(std::false_type{});
+    if (rc != VC_ERR_UNSUPPORTED) return rc;
+    const Shape shape{p.rows, any_threads(static_cast<int64_t>(hidden)), hidden * sizeof(float), 1,
+                      static_cast<unsigned>(nranks)};
     return i8 ? launch<norm_any_kernel<DT, true>>(dev, shape, stream, p, kNorm, 0, bytes)
               : launch<norm_any_kernel<DT, false>>(dev, shape, stream, p, kNorm, 0, bytes);
   });
@@ -505,13 +596,20 @@ vc_status_t norm_grad(const void* const* dout, const void* const* dres_out, cons
   float* scratch = nullptr;
   rc = for_dtype(dtype, [&](auto code) {
     constexpr int DT = code();
-    const int64_t nv = static_cast<int64_t>(hidden) / El<DT>::kVec;
-    const bool whole = aligned && hidden % El<DT>::kVec == 0;
-    switch (whole ? vectors_per_thread(nv, 4) : 0) {
-      case 1: return launch_grad<norm_grad_kernel<DT, 1>>(st, dev, threads_for(nv, 1, kThreads), 0, stream, p, bytes, &scratch);
-      case 2: return launch_grad<norm_grad_kernel<DT, 2>>(st, dev, threads_for(nv, 2, kThreads), 0, stream, p, bytes, &scratch);
-      case 4: return launch_grad<norm_grad_kernel<DT, 4>>(st, dev, threads_for(nv, 4, kThreads), 0, stream, p, bytes, &scratch);
-    }
+    const auto go = [&](auto vec) {
+      constexpr bool VEC = vec();
+      const int64_t n = units_of(static_cast<int64_t>(hidden), El<DT>::kSize);
+      switch (units_per_thread(n, VEC ? 4 : 2)) {
+        case 1: return launch_grad<norm_grad_kernel<DT, VEC, 1>>(st, dev, threads_for(n, 1, kThreads), 0, stream, p, bytes, &scratch);
+        case 2: return launch_grad<norm_grad_kernel<DT, VEC, 2>>(st, dev, threads_for(n, 2, kThreads), 0, stream, p, bytes, &scratch);
+        case 4:
+          if constexpr (VEC)
+            return launch_grad<norm_grad_kernel<DT, VEC, 4>>(st, dev, threads_for(n, 4, kThreads), 0, stream, p, bytes, &scratch);
+      }
+      return VC_ERR_UNSUPPORTED;
+    };
+    const vc_status_t rc = aligned && hidden % El<DT>::kVec == 0 ? go(std::true_type{}) : go(std::false_type{});
+    if (rc != VC_ERR_UNSUPPORTED) return rc;
     return launch_grad<norm_grad_any_kernel<DT>>(st, dev, any_threads(static_cast<int64_t>(hidden)),
                                                  hidden * sizeof(float), stream, p, bytes, &scratch);
   });

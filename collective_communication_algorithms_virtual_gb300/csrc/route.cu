@@ -20,10 +20,11 @@ struct RouteParams {
   const float* bias[VC_MAX_RANKS];
   int32_t* ids[VC_MAX_RANKS];
   float* weights[VC_MAX_RANKS];
-  uint32_t rows, tokens;
+  uint32_t rows;
   int experts, topk, groups, keep_groups, group_top;
+  int group_size, group_lanes;  // group_lanes: lanes of a group, where that is a power of 2 of whole lanes, else 0
   int sigmoid, renormalize, has_bias, by_score;  // by_score: experts are compared by scores, not by logits
-  int vec;                                       // each lane's experts are one aligned piece of the row
+  int vec, vec_bias;                             // each lane's experts are one aligned piece of the row
   float scale;
 };
 struct RouteGradParams {
@@ -31,7 +32,7 @@ struct RouteGradParams {
   const void* logits[VC_MAX_RANKS];
   const int32_t* ids[VC_MAX_RANKS];
   void* dlogits[VC_MAX_RANKS];
-  uint32_t rows, tokens;
+  uint32_t rows;
   int experts, topk, sigmoid, renormalize, vec;
   float scale;
 };
@@ -39,7 +40,9 @@ struct RouteGradParams {
 constexpr float kNone = -INFINITY;
 
 // Lane's V logits of a row; -inf past the last expert.
-template <int DT, int V>
+// KEPT: through L1, for what is read again: the bias by every warp (16384
+// tokens with one bias of 256: 24 us with every read from L2, 17 us from L1).
+template <int DT, int V, bool KEPT = false>
 __device__ __forceinline__ void load_row(const void* row, int lane, int experts, int vec, float* l) {
   using E = El<DT>;
   const int e0 = lane * V;
@@ -47,8 +50,10 @@ __device__ __forceinline__ void load_row(const void* row, int lane, int experts,
     if (e0 < experts) {
       if constexpr (V % E::kVec == 0) {
 #pragma unroll
-        for (int i = 0; i < V / E::kVec; ++i)
-          E::widen(dev::ld16(static_cast<const uint4*>(row) + lane * (V / E::kVec) + i), l + i * E::kVec);
+        for (int i = 0; i < V / E::kVec; ++i) {
+          const uint4* at = static_cast<const uint4*>(row) + lane * (V / E::kVec) + i;
+          E::widen(KEPT ? __ldg(at) : dev::ld16(at), l + i * E::kVec);
+        }
       } else if constexpr (V * E::kSize == 8) {
         const uint2 v = static_cast<const uint2*>(row)[lane];
         if constexpr (DT == VC_FLOAT32) {
@@ -106,10 +111,11 @@ __device__ __forceinline__ float pair_sum(const float* x) {
   for (int d = 1; d < 32; d <<= 1) t = __fadd_rn(t, __shfl_xor_sync(kAll, t, d));
   return t;
 }
+// The largest over the warp (NaN is passed over).
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, d));
-  return x;
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
 }
 template <int V>
 __device__ __forceinline__ float row_max(const float* l) {  // NaN is passed over
@@ -123,13 +129,8 @@ __device__ __forceinline__ bool there(float l) { return l > kNone; }
 __device__ __forceinline__ float soft(float l, float most) {
   return !there(l) ? 0.f : l == most ? 1.f : expf(__fsub_rn(l, most));
 }
-__device__ __forceinline__ float sigmoid(float l) {
-  return there(l) ? __fdiv_rn(1.f, __fadd_rn(1.f, expf(-l))) : 0.f;
-}
-// Bits that order as the numbers do; above 0 for every number.
-__device__ __forceinline__ uint32_t order_key(float c) {
-  const uint32_t u = __float_as_uint(__fadd_rn(c, 0.f));  // -0 as 0
-  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+__device__ __forceinline__ float sigmoid(float l) {  // not for NaN; 0 at -inf
+  return __frcp_rn(__fadd_rn(1.f, expf(-l)));
 }
 
 // The two largest of a group so far, and one more value.
@@ -142,79 +143,165 @@ struct Two {
   __device__ __forceinline__ float worth(int top) const { return top == 2 && b > kNone ? __fadd_rn(a, b) : a; }
 };
 
+// An expert that may be among the chosen.
+struct Candidate {
+  float c;
+  int expert;
+};
+
+// The choice proper: lane j's `place` is where its expert `id` stands among
+// the chosen, best first, or -1 (some lanes hold none); returns how many are
+// chosen.  With several experts a lane the k-th best of the lanes' bests
+// bounds the k-th best of all from below; what reaches it, a little more than
+// k experts as a rule, is laid out one to a lane in index order, and each
+// counts those before it.  More than 32 of them (ties, or fewer lanes with an
+// expert than k) are taken one by one instead.
+template <int V>
+__device__ __forceinline__ int choose(float* c, int topk, int lane, Candidate* list, int* id, int* place) {
+  float best = c[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) best = fmaxf(best, c[i]);
+  *id = -1;
+  *place = -1;
+  float bound = kNone, rest = best;
+  int found = 0;
+  for (; found < topk; ++found) {
+    const float top = warp_max(rest);
+    if (!(top > kNone)) break;
+    const int from = __ffs(__ballot_sync(kAll, rest == top)) - 1;
+    if (lane == from) rest = kNone;
+    if constexpr (V == 1) {
+      const int e = from;
+      if (lane == found) {
+        *id = e;
+        *place = found;
+      }
+    }
+    bound = top;
+  }
+  if constexpr (V == 1) return found;
+  if (found < topk) bound = kNone;
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) mine += c[i] >= bound && c[i] > kNone;
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int m = __shfl_up_sync(kAll, upto, d);
+    if (lane >= d) upto += m;
+  }
+  const int n = __shfl_sync(kAll, upto, 31);
+  if (n <= 32) {
+    int at = upto - mine;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (c[i] >= bound && c[i] > kNone) list[at++] = Candidate{c[i], lane * V + i};
+    __syncwarp();
+    Candidate x{kNone, -1};
+    if (lane < n) x = list[lane];
+    int before = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const float y = __shfl_sync(kAll, x.c, j);
+      before += j < lane ? y >= x.c : y > x.c;
+    }
+    if (lane < n && before < topk) {
+      *id = x.expert;
+      *place = before;
+    }
+    return min(n, topk);
+  }
+  for (found = 0; found < topk; ++found) {
+    const float top = warp_max(best);
+    if (!(top > kNone)) break;
+    const int from = __ffs(__ballot_sync(kAll, best == top)) - 1;
+    int i0 = 0;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i)
+      if (c[i] == top) i0 = i;
+    const int e = __shfl_sync(kAll, lane * V + i0, from);
+    if (lane == found) {
+      *id = e;
+      *place = found;
+    }
+    if (lane == from) {
+      best = kNone;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (i == i0) c[i] = kNone;
+        best = fmaxf(best, c[i]);
+      }
+    }
+  }
+  return found;
+}
+
 template <int DT, int V>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteParams p) {
   __shared__ float table[kWarps][V * 32];  // a token's c, where a group's experts are not whole lanes
+  __shared__ Candidate list[kWarps][32];
   stream_order();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t token = blockIdx.x * kWarps + warp;
-  if (token >= p.tokens) return;
-  const uint32_t r = token / p.rows, t = token - r * p.rows;
-  float c[V], s[V];  // c: what experts are compared by, -inf where not to be chosen; s: their scores or logits
-  load_row<DT, V>(static_cast<const char*>(p.logits[r]) + static_cast<int64_t>(t) * p.experts * El<DT>::kSize, lane, p.experts, p.vec, s);
+  const uint32_t r = blockIdx.y, t = blockIdx.x * kWarps + warp;
+  if (t >= p.rows) return;
+  const char* row = static_cast<const char*>(p.logits[r]) + static_cast<int64_t>(t) * p.experts * El<DT>::kSize;
+  float c[V];  // what experts are compared by, -inf where not to be chosen
+  load_row<DT, V, true>(row, lane, p.experts, p.vec, c);  // the chosen logits are read again
   float most = 0.f, sum = 1.f;
   // the softmax's maximum and sum, where a score is wanted (the sum cancels
   // in weights that are renormalised)
   if (!p.sigmoid) {
-    most = row_max<V>(s);
+    most = row_max<V>(c);
     if (p.by_score || !p.renormalize) {
       float e[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) e[i] = soft(s[i], most);
+      for (int i = 0; i < V; ++i) e[i] = soft(c[i], most);
       sum = pair_sum<V>(e);
       if (p.by_score) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const bool on = there(s[i]);
-          s[i] = on ? __fdiv_rn(e[i], sum) : 0.f;
-          c[i] = on ? s[i] : kNone;
-        }
+        for (int i = 0; i < V; ++i) c[i] = there(c[i]) ? __fdiv_rn(e[i], sum) : kNone;
       }
     }
   } else if (p.by_score) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const bool on = there(s[i]);
-      s[i] = sigmoid(s[i]);
-      c[i] = on ? s[i] : kNone;
-    }
+    for (int i = 0; i < V; ++i) c[i] = there(c[i]) ? sigmoid(c[i]) : kNone;
   }
   if (!p.by_score) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) c[i] = there(s[i]) ? s[i] : kNone;
+    for (int i = 0; i < V; ++i) c[i] = there(c[i]) ? c[i] : kNone;  // NaN
   }
   if (p.has_bias) {
+    float b[V];
+    load_row<VC_FLOAT32, V, true>(p.bias[r], lane, p.experts, p.vec_bias, b);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (c[i] > kNone) {
-        const float x = __fadd_rn(c[i], p.bias[r][lane * V + i]);
-        c[i] = x > kNone ? x : kNone;  // a NaN too
-      }
+      const float x = __fadd_rn(c[i], b[i]);
+      c[i] = c[i] > kNone && x > kNone ? x : kNone;  // a NaN is not chosen either
     }
   }
   if (p.groups > 1) {
-    const int size = p.experts / p.groups, lanes = size / V;
-    if (size % V == 0 && (lanes & (lanes - 1)) == 0) {  // a group is a power of 2 of whole lanes
+    if (p.group_lanes) {
       Two two;
 #pragma unroll
       for (int i = 0; i < V; ++i) two.take(c[i]);
-      for (int d = 1; d < lanes; d <<= 1) {
+      for (int d = 1; d < p.group_lanes; d <<= 1) {
         const float a = __shfl_xor_sync(kAll, two.a, d), b = __shfl_xor_sync(kAll, two.b, d);
         two.take(a);
         two.take(b);
       }
       const float mine = two.worth(p.group_top);
-      const int me = lane / lanes;
       int better = 0;
-      for (int g = 0; g < p.groups; ++g) {
-        const float w = __shfl_sync(kAll, mine, g * lanes);
-        better += w > mine || (w == mine && g < me);
+#pragma unroll 4
+      for (int from = 0; from < p.groups * p.group_lanes; from += p.group_lanes) {
+        const float w = __shfl_sync(kAll, mine, from);
+        better += from + p.group_lanes <= lane ? w >= mine : w > mine;  // of groups before this lane's, a tie too
       }
       if (better >= p.keep_groups) {
 #pragma unroll
         for (int i = 0; i < V; ++i) c[i] = kNone;
       }
     } else {
+      const int size = p.group_size;
 #pragma unroll
       for (int i = 0; i < V; ++i) table[warp][lane * V + i] = c[i];
       __syncwarp();
@@ -225,7 +312,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
       int better = 0;
       for (int g = 0; g < p.groups; ++g) {
         const float w = __shfl_sync(kAll, mine, g);
-        better += w > mine || (w == mine && g < lane);
+        better += g < lane ? w >= mine : w > mine;
       }
       const uint32_t kept = __ballot_sync(kAll, lane < p.groups && better < p.keep_groups);
 #pragma unroll
@@ -235,51 +322,22 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
       }
     }
   }
-  uint32_t key[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) key[i] = c[i] > kNone ? order_key(c[i]) : 0u;
-  int my_id = -1;
-  float mine = 0.f;  // lane j: the score or logit of choice j
-  uint32_t best;
-  int at;
-  float value;
-  const auto look = [&] {
-    best = key[0];
-    at = 0;
-    value = s[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-        value = s[i];
-      }
-  };
-  look();
-  for (int j = 0; j < p.topk; ++j) {
-    const uint32_t top = __reduce_max_sync(kAll, best);
-    if (top == 0) break;
-    const int from = __ffs(__ballot_sync(kAll, best == top)) - 1;
-    const int id = __shfl_sync(kAll, lane * V + at, from);
-    const float v = __shfl_sync(kAll, value, from);
-    if (lane == j) {
-      my_id = id;
-      mine = v;
-    }
-    if (lane == from) {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i == at) key[i] = 0;
-      look();
-    }
-  }
+  int id, place;
+  const int n = choose<V>(c, p.topk, lane, list[warp], &id, &place);
   float w = 0.f;
-  if (my_id >= 0) w = p.by_score ? mine : p.sigmoid ? sigmoid(mine) : __fdiv_rn(soft(mine, most), sum);
+  if (place >= 0) {  // the score, again from the logit
+    const float l = El<DT>::load(row, id);
+    w = p.sigmoid ? sigmoid(l) : __fdiv_rn(soft(l, most), sum);
+  }
   if (p.renormalize) w = w / fmaxf(warp_sum(w), 0x1p-126f);
-  if (lane < p.topk) {
-    const int64_t to = static_cast<int64_t>(t) * p.topk + lane;
-    p.ids[r][to] = my_id;
-    p.weights[r][to] = w * p.scale;
+  const int64_t to = static_cast<int64_t>(t) * p.topk;
+  if (place >= 0) {
+    p.ids[r][to + place] = id;
+    p.weights[r][to + place] = w * p.scale;
+  }
+  if (lane >= n && lane < p.topk) {
+    p.ids[r][to + lane] = -1;
+    p.weights[r][to + lane] = 0.f;
   }
 }
 
@@ -287,9 +345,8 @@ template <int DT, int V>
 __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_constant__ RouteGradParams p) {
   stream_order();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t token = blockIdx.x * kWarps + warp;
-  if (token >= p.tokens) return;
-  const uint32_t r = token / p.rows, t = token - r * p.rows;
+  const uint32_t r = blockIdx.y, t = blockIdx.x * kWarps + warp;
+  if (t >= p.rows) return;
   const int64_t at = static_cast<int64_t>(t) * p.experts * El<DT>::kSize;
   const char* row = static_cast<const char*>(p.logits[r]) + at;
   // lane j: choice j's expert, its logit and the gradient of scale * (its share or score)
@@ -312,7 +369,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
   if (p.renormalize) {
     // shares of the chosen scores; of a softmax they depend on the chosen
     // logits alone, and the gradient stays among them
-    const float e = p.sigmoid ? sigmoid(l) : soft(l, warp_max(l));
+    const float most = warp_max(l);
+    const float e = !there(l) ? 0.f : p.sigmoid ? sigmoid(l) : soft(l, most);
     const float total = warp_sum(e);
     if (total >= 0x1p-126f) {
       const float share = e / total;
@@ -320,7 +378,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
       if (p.sigmoid) give *= 1.f / (1.f + expf(l));
     }
   } else if (p.sigmoid) {
-    give = d * sigmoid(l) / (1.f + expf(l));
+    give = there(l) ? d * sigmoid(l) / (1.f + expf(l)) : 0.f;
   } else {
     float all[V];
     load_row<DT, V>(row, lane, p.experts, p.vec, all);
@@ -331,10 +389,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
     const float s = there(l) ? soft(l, most) / sum : 0.f;
     const float dot = warp_sum(d * s);
     give = d * s;
-    if (sum > 0.f) {
+    const float by = sum > 0.f ? dot / sum : 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) x[i] = -(all[i] / sum) * dot;
-    }
+    for (int i = 0; i < V; ++i) x[i] = -all[i] * by;
   }
   if (!there(l)) give = 0.f;
   for (int j = 0; j < p.topk; ++j) {
@@ -386,6 +443,8 @@ vc_status_t route(const void* const* logits, const float* const* bias, int32_t* 
   Buffers b;
   rc = b.add(logits, nranks, n * nexperts * es, es, false, "logits");
   const bool aligned = b.aligned16();
+  bool bias_aligned = true;
+  for (int r = 0; bias && r < nranks; ++r) bias_aligned &= (reinterpret_cast<uintptr_t>(bias[r]) & 15) == 0;
   if (rc == VC_SUCCESS && bias) rc = b.add(reinterpret_cast<const void* const*>(bias), nranks, int64_t(nexperts) * 4, 4, false, "bias");
   if (rc == VC_SUCCESS) rc = b.add(reinterpret_cast<const void* const*>(ids), nranks, n * k * 4, 4, true, "ids");
   if (rc == VC_SUCCESS) rc = b.add(reinterpret_cast<const void* const*>(weights), nranks, n * k * 4, 4, true, "weights");
@@ -403,10 +462,10 @@ vc_status_t route(const void* const* logits, const float* const* bias, int32_t* 
     p.weights[r] = weights[r];
   }
   p.rows = static_cast<uint32_t>(rows);
-  p.tokens = p.rows * static_cast<uint32_t>(nranks);
   p.experts = nexperts;
   p.topk = how->topk;
   p.groups = how->ngroups;
+  p.group_size = nexperts / how->ngroups;
   p.keep_groups = how->topk_groups;
   p.group_top = how->group_top;
   p.sigmoid = how->score == VC_SCORE_SIGMOID;
@@ -414,11 +473,14 @@ vc_status_t route(const void* const* logits, const float* const* bias, int32_t* 
   p.has_bias = bias != nullptr;
   p.by_score = bias != nullptr || (how->ngroups > 1 && how->group_top == 2);
   p.scale = how->scale;
-  const int64_t bytes = int64_t(p.tokens) * (int64_t(nexperts) * es + k * 8) + (bias ? int64_t(nexperts) * nranks * 4 : 0);
-  const Shape shape{(p.tokens + kWarps - 1) / kWarps, kWarps * 32};
+  const int64_t bytes = n * nranks * (int64_t(nexperts) * es + k * 8) + (bias ? int64_t(nexperts) * nranks * 4 : 0);
+  const Shape shape{(p.rows + kWarps - 1) / kWarps, kWarps * 32, 0, 1, static_cast<unsigned>(nranks)};
   return for_dtype(dtype, [&](auto code) {
     return for_width(nexperts, [&](auto width) {
       p.vec = whole_lanes(aligned, nexperts, width());
+      p.vec_bias = whole_lanes(bias_aligned, nexperts, width());
+      const int lanes = p.group_size % width() ? 0 : p.group_size / width();
+      p.group_lanes = lanes & (lanes - 1) ? 0 : lanes;
       return launch<route_kernel<code(), width()>>(dev, shape, stream, p, kRoute, 0, bytes);
     });
   });
@@ -451,15 +513,14 @@ vc_status_t route_grad(const float* const* dweights, const void* const* logits, 
     p.dlogits[r] = dlogits[r];
   }
   p.rows = static_cast<uint32_t>(rows);
-  p.tokens = p.rows * static_cast<uint32_t>(nranks);
   p.experts = nexperts;
   p.topk = how->topk;
   p.sigmoid = how->score == VC_SCORE_SIGMOID;
   p.renormalize = how->renormalize != 0;
   p.scale = how->scale;
   const bool dense = !p.sigmoid && !p.renormalize;
-  const int64_t bytes = int64_t(p.tokens) * ((int64_t(nexperts) + (dense ? nexperts : k)) * es + k * 8);
-  const Shape shape{(p.tokens + kWarps - 1) / kWarps, kWarps * 32};
+  const int64_t bytes = n * nranks * ((int64_t(nexperts) + (dense ? nexperts : k)) * es + k * 8);
+  const Shape shape{(p.rows + kWarps - 1) / kWarps, kWarps * 32, 0, 1, static_cast<unsigned>(nranks)};
   return for_dtype(dtype, [&](auto code) {
     return for_width(nexperts, [&](auto width) {
       p.vec = whole_lanes(aligned, nexperts, width());

@@ -628,7 +628,8 @@ vc_status_t vc_reduce_scatter_noalloc(const void* const* send, void* const* recv
  * to fp32, computed in fp32 and rounded once at the end; another dtype is
  * VC_ERR_UNSUPPORTED.  More than 2^31 - 1 tokens over all ranks, or sizes
  * that overflow, are VC_ERR_INVALID_ARG.  Results are reproducible bit for
- * bit on one GPU model: no sum depends on the order in which blocks run.
+ * bit on one GPU model, for buffers of the same alignment: no sum depends on
+ * the order in which blocks run.
  */
 
 /* Largest `hidden` of the norm operators: a row is held on chip in fp32. */

@@ -34,10 +34,10 @@ def some_ids(seed, N, rows, k, E, lo=-1):
     return torch.randint(lo, E + 1, (N, rows, k), generator=g, dtype=torch.int32).cuda()
 
 
-PLANS = [  # N, rows, k, E, capacity: one choice, one warp's worth, more than one step of a warp, all cluster sizes
+PLANS = [  # N, rows, k, E, capacity: one choice, one warp's worth, more than one step of a warp, all cluster sizes, shared memory about 48 KB
     (1, 1, 1, 1, 1), (1, 5, 2, 3, 100), (2, 1, 4, 8, 3), (8, 4, 4, 64, 16), (3, 33, 5, 33, 40), (4, 100, 6, 128, 170),
     (8, 63, 8, 256, 500), (2, 1025, 2, 1024, 2000), (8, 500, 8, 64, 700), (5, 3000, 3, 20, 1800), (64, 70, 8, 1024, 70),
-    (1, 20000, 6, 7, 30000),
+    (1, 20000, 6, 7, 30000), (1, 90, 4, 341, 200), (1, 90, 4, 342, 200),
 ]
 
 
@@ -97,7 +97,7 @@ def test_dispatch(N, rows, k, E, cap, H, dt):
     slots, _ = make_plan(ids, E, cap)
     sl = slots.cpu().numpy().reshape(-1)
     for shift in (0, 1):
-        send, recv = shifted(values(g, dt, N, rows, H), shift), shifted(values(g, dt, N, cap, H), shift)
+        send, recv = shifted(values(g, dt, N, rows, H), shift), shifted(values(g, dt, N, cap, H), 5 * shift)
         scale, rscale = torch.rand(N, rows, device="cuda"), torch.full((N, cap), -1.0, device="cuda")
         want, want_s = recv.cpu().clone().view(-1, H), rscale.cpu().clone().view(-1)
         for a in np.nonzero(sl >= 0)[0]:
@@ -116,7 +116,7 @@ def test_combine_and_backward(N, rows, k, E, cap, H, dt):
     sl = slots.cpu().numpy().reshape(-1, k)
     on = sl >= 0
     for shift in (0, 1):
-        recv, out = shifted(values(g, dt, N, cap, H), shift), shifted(values(g, dt, N, rows, H), shift)
+        recv, out = shifted(values(g, dt, N, cap, H), shift), shifted(values(g, dt, N, rows, H), 3 * shift)
         w = torch.rand(N, rows, k, generator=g).cuda()
         # rows and weights that no slot takes are never looked at
         w.view(-1, k)[torch.from_numpy(~on).cuda()] = float("nan")
@@ -134,7 +134,7 @@ def test_combine_and_backward(N, rows, k, E, cap, H, dt):
             assert np.all(off <= bound), (weights is None, float((off - bound).max()))
         # backward
         dout = shifted(values(g, dt, N, rows, H), shift)
-        drecv = shifted(values(g, dt, N, cap, H), shift)
+        drecv = shifted(values(g, dt, N, cap, H), 2 * shift)
         before = drecv.clone()
         dw = torch.full((N, rows, k), -7.0, device="cuda")
         vc.vc_combine_backward(dout, recv, slots, weights=w, drecv=drecv, dweights=dw)

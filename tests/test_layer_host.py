@@ -2,6 +2,8 @@
 checks come before any CUDA call, and the binding's tensor checks before the
 library.  Buffers are made-up addresses that nothing reads."""
 import ctypes
+import math
+import struct
 
 import pytest
 import torch
@@ -60,8 +62,8 @@ def test_norm_refuses(L, over, status):
 
 def test_empty_calls_are_accepted_without_a_gpu(L):
     assert norm(L, rows=0) == OK and norm(L, H=0) == OK
-    how = b.RouteHow(0, 1, 1, 1, 1, 1, 1.0)
-    assert L.vc_route(ptrs(area(0)), None, ptrs(area(1)), ptrs(area(2)), 2, 0, 8, ctypes.byref(how), F32, None) == OK
+    how = b._pack_how(0, 1, 1, 1, 1, 1, 1.0)
+    assert L.vc_route(ptrs(area(0)), None, ptrs(area(1)), ptrs(area(2)), 2, 0, 8, how, F32, None) == OK
     assert L.vc_combine(ptrs(area(0)), ptrs(area(1)), None, ptrs(area(2)), 2, 0, 8, 2, 4, F32, None) == OK
 
 
@@ -88,7 +90,7 @@ def route(L, back=False, N=2, rows=4, E=16, dt=F32, bias=None, how=True, **over)
     a = dict(logits=ptrs(area(0)), ids=ptrs(area(1)), weights=ptrs(area(2)), dlogits=ptrs(area(3)))
     a.update({k: v for k, v in over.items() if k in a})
     h.update({k: v for k, v in over.items() if k in h})
-    ref = ctypes.byref(b.RouteHow(*h.values())) if how else None
+    ref = b._pack_how(*h.values()) if how else None
     if back:
         return L.vc_route_backward(a["weights"], a["logits"], a["ids"], a["dlogits"], N, rows, E, ref, dt, None)
     return L.vc_route(a["logits"], bias, a["ids"], a["weights"], N, rows, E, ref, dt, None)
@@ -186,8 +188,9 @@ class Fake:
     def data_ptr(self):
         return self._ptr
 
-    def element_size(self):
-        return self.dtype.itemsize
+    @property
+    def nbytes(self):
+        return math.prod(self.shape) * self.dtype.itemsize
 
     def __len__(self):
         return self.shape[0]
@@ -221,7 +224,8 @@ def test_sizes_reach_the_library(rec):
     assert args[4][5:11] == (2, 3, 8, 4, 12, F32)
     assert args[5][4:10] == (2, 3, 8, 4, 12, F32)
     # a stacked tensor's ranks lie one behind another; one weight stands for all
-    assert list(args[0][0]) == [1 << 20, (1 << 20) + 6 * 8 * 4] and list(args[0][2]) == [1 << 20] * 2
+    assert struct.unpack("2Q", args[0][0]) == (1 << 20, (1 << 20) + 6 * 8 * 4)
+    assert struct.unpack("2Q", args[0][2]) == (1 << 20, 1 << 20)
 
 
 @pytest.mark.parametrize("bad", [
