@@ -767,6 +767,15 @@ vc_status_t combine_grad(const void* const* dout, const void* const* recv, const
 }
 
 }  // namespace
+
+cudaError_t take_exchange_errors(cudaStream_t stream, uint32_t* flags) {
+  static const uint32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(flags, dev::g_device_error, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess)
+    e = cudaMemcpyToSymbolAsync(dev::g_device_error, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, stream);
+  return e;
+}
+
 }  // namespace layer
 }  // namespace vc
 

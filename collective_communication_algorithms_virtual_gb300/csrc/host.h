@@ -1,6 +1,6 @@
 // Host services the library's translation units share: error reporting, the
 // C entry guard, per-device state with the scratch pool, and the launch trace.
-// Defined in vc.cu.
+// Defined in vc.cu but for what says otherwise.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -44,6 +44,12 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb);
 // One launch on `stream`, bracketed by events and recorded while the trace
 // is on (`rec` without its time).
 vc_status_t launch_traced(cudaStream_t stream, const vc_trace_record_t& rec, cudaError_t (*launch)(void*), void* arg);
+
+namespace layer {
+// Copies the exchange kernels' own device error word to *flags and clears it,
+// in stream order (exchange.cu).
+cudaError_t take_exchange_errors(cudaStream_t stream, uint32_t* flags);
+}  // namespace layer
 
 // No exception leaves a C entry point.
 template <class F>

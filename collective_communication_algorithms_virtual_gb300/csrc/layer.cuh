@@ -6,6 +6,8 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <cstdio>
+#include <type_traits>
 
 #include "host.h"
 #include "kernels.cuh"
@@ -190,6 +192,9 @@ vc_status_t launch(int dev, const Shape& s, cudaStream_t stream, const P& p, Ker
     attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
     attr[cfg.numAttrs++].val.clusterDim = {s.cluster, 1, 1};
   }
+  if (log_enabled())
+    std::fprintf(stderr, "[vc] layer kernel=%d grid=%ux%u block=%u cluster=%u smem=%zu bytes=%lld\n", static_cast<int>(what), s.grid,
+                 s.ranks, s.block, s.cluster, s.smem, static_cast<long long>(bytes));
   struct Arg {
     cudaLaunchConfig_t* cfg;
     const P* p;

@@ -240,17 +240,20 @@ struct GradParams {
   int32_t hidden;
 };
 
+// Most threads of a block of the gradient whose threads hold `vpt` units.
+__host__ __device__ constexpr int grad_threads(int vpt) { return 128 * vpt; }
+
 // Block b of rank r takes the rank's rows b, b + per, ...; each thread keeps
 // the weight's gradient of its columns over them (so the columns are fixed, and
 // rows off 16-byte boundaries are written element by element).
 template <int DT, bool VEC, int VPT>
-__global__ void __launch_bounds__(kThreads) norm_grad_kernel(const __grid_constant__ GradParams p) {
+__global__ void __launch_bounds__(grad_threads(VPT)) norm_grad_kernel(const __grid_constant__ GradParams p) {
   using E = El<DT>;
   constexpr int kN = E::kVec;
   using R = Row<E::kSize, VEC>;
   using Out = Span<E::kSize, 16, VEC>;
   __shared__ float part[2][32];
-  __shared__ __align__(16) unsigned char room[kThreads / 32][Out::kRoom];
+  __shared__ __align__(16) unsigned char room[grad_threads(VPT) / 32][Out::kRoom];
   stream_order();
   const uint32_t r = blockIdx.x / p.per, b = blockIdx.x - r * p.per;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -266,24 +269,51 @@ __global__ void __launch_bounds__(kThreads) norm_grad_kernel(const __grid_consta
   for (int u = 0; u < VPT; ++u)
 #pragma unroll
     for (int i = 0; i < kN; ++i) dw[u][i] = 0.f;
-  int flip = 0;
-  for (uint32_t t = b; t < p.rows; t += p.per, flip ^= 1) {
-    const int64_t own = static_cast<int64_t>(t) * width;
-    const R dout = row_of(p.dout[r], own, p.rows), hs = row_of(p.h[r], own, p.rows),
-            dres = row_of(p.has_dres_out ? p.dres_out[r] : p.h[r], own, p.rows);
-    typename R::Raw graw[VPT], hraw[VPT], draw[VPT], wraw[VPT];
+  typename R::Raw wraw[VPT];
+#pragma unroll
+  for (int u = 0; u < VPT; ++u) {
+    const int c = threadIdx.x + u * blockDim.x;
+    wraw[u] = R::zero();
+    if (c < nu) wraw[u] = weights.load_kept(c);
+  }
+  // A row's loads are asked for while the row before is worked, where
+  // registers allow it (4 ranks x 1024 x 4096 bf16: 53.2 us without, 51.7 with).
+  constexpr bool kAhead = VEC && VPT <= 2;
+  struct Loaded {
+    typename R::Raw g[VPT], h[VPT], d[VPT];
+    float rs;
+  };
+  const auto rows_at = [&](uint32_t t, const void* buffer) { return row_of(buffer, static_cast<int64_t>(t) * width, p.rows); };
+  const void* dres_out = p.has_dres_out ? p.dres_out[r] : p.h[r];
+  const auto fetch = [&](uint32_t t, Loaded& l) {
+    const R dout = rows_at(t, p.dout[r]), hs = rows_at(t, p.h[r]), dres = rows_at(t, dres_out);
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       const int c = threadIdx.x + u * blockDim.x;
-      graw[u] = hraw[u] = draw[u] = wraw[u] = R::zero();
+      l.g[u] = l.h[u] = l.d[u] = R::zero();
       if (c < nu) {
-        graw[u] = dout.load(c);
-        hraw[u] = hs.load(c);
-        wraw[u] = weights.load_kept(c);
-        if (p.has_dres_out) draw[u] = dres.load_plain(c);
+        l.g[u] = dout.load(c);
+        l.h[u] = hs.load(c);
+        if (p.has_dres_out) l.d[u] = dres.load_plain(c);
       }
     }
-    const float rs = p.rstd[r][t];
+    l.rs = p.rstd[r][t];
+  };
+  const float inv = 1.f / static_cast<float>(p.hidden);
+  Loaded next;
+  if (kAhead) fetch(b, next);
+  int flip = 0;
+  for (uint32_t t = b; t < p.rows; t += p.per, flip ^= 1) {
+    const int64_t own = static_cast<int64_t>(t) * width;
+    const R dout = rows_at(t, p.dout[r]), hs = rows_at(t, p.h[r]), dres = rows_at(t, dres_out);
+    Loaded now;
+    if (kAhead) {
+      now = next;
+      if (t + p.per < p.rows) fetch(t + p.per, next);
+    } else {
+      fetch(t, now);
+    }
+    const float rs = now.rs;
     float g[VPT][kN], h[VPT][kN], gh = 0.f;
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
@@ -292,8 +322,8 @@ __global__ void __launch_bounds__(kThreads) norm_grad_kernel(const __grid_consta
       for (int i = 0; i < kN; ++i) g[u][i] = h[u][i] = 0.f;
       if (c >= nu) continue;
       float w[kN];
-      E::widen(dout.finish(graw[u], c, p.hidden), g[u]);
-      E::widen(hs.finish(hraw[u], c, p.hidden), h[u]);
+      E::widen(dout.finish(now.g[u], c, p.hidden), g[u]);
+      E::widen(hs.finish(now.h[u], c, p.hidden), h[u]);
       E::widen(weights.finish(wraw[u], c, p.hidden), w);
       mask_unit<E::kSize, VEC>(c, p.hidden, g[u]);
       mask_unit<E::kSize, VEC>(c, p.hidden, h[u]);
@@ -305,7 +335,7 @@ __global__ void __launch_bounds__(kThreads) norm_grad_kernel(const __grid_consta
         gh += g[u][i] * h[u][i];
       }
     }
-    const float mean = block_sum(gh, part[flip]) / static_cast<float>(p.hidden) * rs * rs;
+    const float mean = block_sum(gh, part[flip]) * inv * rs * rs;
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       const int c = threadIdx.x + u * blockDim.x;
@@ -314,7 +344,7 @@ __global__ void __launch_bounds__(kThreads) norm_grad_kernel(const __grid_consta
       for (int i = 0; i < kN; ++i) d[i] = rs * (g[u][i] - h[u][i] * mean);
       if (p.has_dres_out && c < nu) {
         float f[kN];
-        E::widen(dres.finish(draw[u], c, p.hidden), f);
+        E::widen(dres.finish(now.d[u], c, p.hidden), f);
 #pragma unroll
         for (int i = 0; i < kN; ++i) d[i] += f[i];
       }
@@ -388,28 +418,36 @@ struct WeightParams {
   uint32_t per, chunks;  // parts of each rank; blocks of each rank
   int32_t hidden;
 };
-constexpr int kSumThreads = 256;
+constexpr int kSumAhead = 8;   // parts of a thread whose loads are in flight together
+constexpr int kSumWarps = 16;  // of a block, at most
 
 // dweight[r] = the sum of rank r's parts: 32 columns a block, its warps take
 // the parts in turn, and the warps' sums are added in warp order.
-__global__ void __launch_bounds__(kSumThreads) norm_weight_kernel(const __grid_constant__ WeightParams p) {
-  __shared__ float sums[kSumThreads / 32][32];
+__global__ void __launch_bounds__(kSumWarps * 32) norm_weight_kernel(const __grid_constant__ WeightParams p) {
+  __shared__ float sums[kSumWarps][32];
   stream_order();
   const uint32_t r = blockIdx.x / p.chunks, chunk = blockIdx.x - r * p.chunks;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int c = static_cast<int>(chunk) * 32 + lane;
   float x = 0.f;
   if (c < p.hidden) {
-#pragma unroll 8
-    for (uint32_t b = warp; b < p.per; b += kSumThreads / 32)
-      x += p.part[(static_cast<int64_t>(r) * p.per + b) * p.hidden + c];
+    const float* from = p.part + static_cast<int64_t>(r) * p.per * p.hidden + c;
+    for (uint32_t b0 = warp; b0 < p.per; b0 += warps * kSumAhead) {  // loads in flight together
+      float v[kSumAhead];
+#pragma unroll
+      for (int i = 0; i < kSumAhead; ++i) {
+        const uint32_t b = b0 + i * warps;
+        v[i] = b < p.per ? from[static_cast<int64_t>(b) * p.hidden] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kSumAhead; ++i) x += v[i];
+    }
   }
   sums[warp][lane] = x;
   __syncthreads();
   if (warp == 0 && c < p.hidden) {
     x = 0.f;
-#pragma unroll
-    for (int w = 0; w < kSumThreads / 32; ++w) x += sums[w][lane];
+    for (int w = 0; w < warps; ++w) x += sums[w][lane];
     p.dweight[r][c] = x;
   }
 }
@@ -599,12 +637,13 @@ vc_status_t norm_grad(const void* const* dout, const void* const* dres_out, cons
     const auto go = [&](auto vec) {
       constexpr bool VEC = vec();
       const int64_t n = units_of(static_cast<int64_t>(hidden), El<DT>::kSize);
-      switch (units_per_thread(n, VEC ? 4 : 2)) {
-        case 1: return launch_grad<norm_grad_kernel<DT, VEC, 1>>(st, dev, threads_for(n, 1, kThreads), 0, stream, p, bytes, &scratch);
-        case 2: return launch_grad<norm_grad_kernel<DT, VEC, 2>>(st, dev, threads_for(n, 2, kThreads), 0, stream, p, bytes, &scratch);
-        case 4:
-          if constexpr (VEC)
-            return launch_grad<norm_grad_kernel<DT, VEC, 4>>(st, dev, threads_for(n, 4, kThreads), 0, stream, p, bytes, &scratch);
+      if (n <= grad_threads(1))
+        return launch_grad<norm_grad_kernel<DT, VEC, 1>>(st, dev, threads_for(n, 1, grad_threads(1)), 0, stream, p, bytes, &scratch);
+      if (n <= 2 * grad_threads(2))
+        return launch_grad<norm_grad_kernel<DT, VEC, 2>>(st, dev, threads_for(n, 2, grad_threads(2)), 0, stream, p, bytes, &scratch);
+      if constexpr (VEC) {
+        if (n <= 4 * grad_threads(4))
+          return launch_grad<norm_grad_kernel<DT, VEC, 4>>(st, dev, threads_for(n, 4, grad_threads(4)), 0, stream, p, bytes, &scratch);
       }
       return VC_ERR_UNSUPPORTED;
     };
@@ -620,7 +659,9 @@ vc_status_t norm_grad(const void* const* dout, const void* const* dres_out, cons
     w.per = p.per;
     w.chunks = static_cast<uint32_t>((hidden + 31) / 32);
     w.hidden = p.hidden;
-    rc = launch<norm_weight_kernel>(dev, Shape{w.chunks * static_cast<unsigned>(nranks), kSumThreads}, stream, w, kNormWeight, 1,
+    // warps enough to have every part in flight at once
+    const unsigned warps = std::min<unsigned>(kSumWarps, (p.per + kSumAhead - 1) / kSumAhead);
+    rc = launch<norm_weight_kernel>(dev, Shape{w.chunks * static_cast<unsigned>(nranks), warps * 32}, stream, w, kNormWeight, 1,
                                     static_cast<int64_t>(hidden) * nranks * 4 * (1 + static_cast<int64_t>(p.per)));
   }
   if (scratch) {

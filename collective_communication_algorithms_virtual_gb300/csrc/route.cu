@@ -12,7 +12,7 @@ namespace vc {
 namespace layer {
 namespace {
 
-constexpr int kWarps = 8;  // tokens of a block
+constexpr int kWarps = 4;  // tokens of a block
 constexpr unsigned kAll = 0xffffffffu;
 
 struct RouteParams {
@@ -180,10 +180,10 @@ __device__ __forceinline__ int choose(float* c, int topk, int lane, Candidate* l
     bound = top;
   }
   if constexpr (V == 1) return found;
-  if (found < topk) bound = kNone;
+  bound = found < topk ? -3.402823466e38f : fmaxf(bound, -3.402823466e38f);  // above -inf
   int mine = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) mine += c[i] >= bound && c[i] > kNone;
+  for (int i = 0; i < V; ++i) mine += c[i] >= bound;
   int upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -195,7 +195,7 @@ __device__ __forceinline__ int choose(float* c, int topk, int lane, Candidate* l
     int at = upto - mine;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (c[i] >= bound && c[i] > kNone) list[at++] = Candidate{c[i], lane * V + i};
+      if (c[i] >= bound) list[at++] = Candidate{c[i], lane * V + i};
     __syncwarp();
     Candidate x{kNone, -1};
     if (lane < n) x = list[lane];
@@ -237,7 +237,7 @@ __device__ __forceinline__ int choose(float* c, int topk, int lane, Candidate* l
 }
 
 template <int DT, int V>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 16 : 4) route_kernel(const __grid_constant__ RouteParams p) {
   __shared__ float table[kWarps][V * 32];  // a token's c, where a group's experts are not whole lanes
   __shared__ Candidate list[kWarps][32];
   stream_order();
@@ -275,8 +275,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     load_row<VC_FLOAT32, V, true>(p.bias[r], lane, p.experts, p.vec_bias, b);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float x = __fadd_rn(c[i], b[i]);
-      c[i] = c[i] > kNone && x > kNone ? x : kNone;  // a NaN is not chosen either
+      c[i] = fmaxf(__fadd_rn(c[i], b[i]), kNone);  // a NaN is not chosen either
     }
   }
   if (p.groups > 1) {
@@ -289,14 +288,20 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         two.take(a);
         two.take(b);
       }
-      const float mine = two.worth(p.group_top);
-      int better = 0;
-#pragma unroll 4
-      for (int from = 0; from < p.groups * p.group_lanes; from += p.group_lanes) {
-        const float w = __shfl_sync(kAll, mine, from);
-        better += from + p.group_lanes <= lane ? w >= mine : w > mine;  // of groups before this lane's, a tie too
+      // the best groups one by one, the lowest of equal ones first
+      float rest = two.worth(p.group_top);
+      bool kept = false;
+      const int group = lane & -p.group_lanes;
+      for (int g = 0; g < p.keep_groups; ++g) {
+        const float top = warp_max(rest);
+        if (!(top > kNone)) break;
+        const int best = (__ffs(__ballot_sync(kAll, rest == top)) - 1) & -p.group_lanes;
+        if (group == best) {
+          kept = true;
+          rest = kNone;
+        }
       }
-      if (better >= p.keep_groups) {
+      if (!kept) {
 #pragma unroll
         for (int i = 0; i < V; ++i) c[i] = kNone;
       }

@@ -2165,8 +2165,11 @@ VC_EXPORT vc_status_t vc_device_errors(vc_stream_t stream, uint32_t* flags) {
     const uint32_t zero = 0;
     cudaError_t e = cudaMemcpyFromSymbolAsync(flags, dev::g_device_error, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(dev::g_device_error, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, s);
+    uint32_t exchange = 0;
+    if (e == cudaSuccess) e = layer::take_exchange_errors(s, &exchange);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device error word");
+    *flags |= exchange;
     return VC_SUCCESS;
   });
 }
@@ -2285,4 +2288,4 @@ VC_EXPORT vc_status_t vc_get_copy_pipeline(size_t* min_bytes) {
   return VC_SUCCESS;
 }
 
-VC_EXPORT int vc_version(void) { return 100; }
+VC_EXPORT int vc_version(void) { return 200; }

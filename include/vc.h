@@ -558,7 +558,8 @@ vc_status_t vc_get_reuse_order(size_t* min_step_bytes);
  * Device error word.  Waits for `stream` (after the work enqueued so far),
  * then reads and clears the word: bit 1 set when a bulk-copy pipeline's wait
  * for a tile's load gave up (the launch then stopped issuing copies and
- * returned; its outputs are incomplete).  Never set in correct operation;
+ * returned; its outputs are incomplete).  A large vc_dispatch moves its rows by
+ * such a pipeline and reports here too.  Never set in correct operation;
  * the waits are bounded so that a fault elsewhere cannot hang a launch.
  */
 vc_status_t vc_device_errors(vc_stream_t stream, uint32_t* flags);
