@@ -17,7 +17,6 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
-import sys
 from typing import Sequence
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -349,9 +348,19 @@ def vc_reduce(send, recv_root, root=0, algo="fused", op="sum", stream=None) -> N
 
 # Pointer arrays go to the library as packed bytes, and the checks compare
 # attributes in place: the smallest calls spend most of their time here, and a
-# ctypes array per argument took twice as long.
+# ctypes array per argument took twice as long.  N pointers p, p + s, ... are
+# one whole number, p * ones + s * steps in 64-bit digits (lowest first, as the
+# machine stores them).
 
-_PACK: dict = {}
+_DIGITS: dict = {}
+_SEQUENCES = (list, tuple)
+
+
+def _digits(N: int):
+    d = _DIGITS.get(N)
+    if d is None:
+        d = _DIGITS[N] = sum(1 << 64 * i for i in range(N)), sum(i << 64 * i for i in range(N))
+    return d
 
 
 def _invalid(msg: str):
@@ -369,7 +378,7 @@ def _bad(x, shape, dtype, dev) -> bool:
 
 def _shape(a, n: int, what: str) -> tuple:
     """(ranks, the n dimensions of each rank's tensor) of a per-rank argument."""
-    shape = (len(a), *a[0].shape) if a.__class__ in (list, tuple) else a.shape
+    shape = (len(a), *a[0].shape) if a.__class__ in _SEQUENCES else a.shape
     if len(shape) != n + 1:
         raise _invalid(f"{what}: want {n} dimensions for each rank, not {tuple(shape[1:])}")
     return shape
@@ -378,7 +387,7 @@ def _shape(a, n: int, what: str) -> tuple:
 def _start(a):
     """What a call's checks go by: a tensor of the per-rank argument, its
     dtype, element size and CUDA device."""
-    x = a[0] if a.__class__ in (list, tuple) else a
+    x = a[0] if a.__class__ in _SEQUENCES else a
     dev = x.get_device()
     if dev < 0:
         raise _invalid(f"tensors must be on a CUDA device, not {x.device}")
@@ -392,30 +401,27 @@ def _ptrs(a, what: str, full: tuple, size: int, dtype, dev: int):
     if a is None:
         return None
     N = full[0]
-    pack = _PACK.get(N)
-    if pack is None:
-        pack = _PACK[N] = struct.Struct(f"={N}Q").pack
-    if a.__class__ in (list, tuple):
+    if a.__class__ in _SEQUENCES:
         if len(a) != N:
             raise _invalid(f"{what}: {len(a)} tensors for {N} ranks")
         if CHECK_TENSORS:
             for x in a:
                 if _bad(x, full[1:], dtype, dev):
                     _refuse(x, what, full[1:], dtype, dev)
-        return pack(*[x.data_ptr() for x in a])
+        return struct.pack(f"={N}Q", *[x.data_ptr() for x in a])
     if CHECK_TENSORS and (a.shape != full or a.dtype is not dtype or a.get_device() != dev or not a.is_contiguous()):
         _refuse(a, what, full, dtype, dev)
-    p = a.data_ptr()
-    return pack(*range(p, p + N * size, size)) if size else bytes(8 * N)
+    ones, steps = _DIGITS.get(N) or _digits(N)
+    return (a.data_ptr() * ones + size * steps).to_bytes(8 * N, "little")
 
 
 def _shared(a, what: str, full: tuple, size: int, dtype, dev: int):
     """As _ptrs, or one tensor that stands for every rank."""
-    if a is None or a.__class__ in (list, tuple) or len(a.shape) == len(full):
+    if a is None or a.__class__ in _SEQUENCES or len(a.shape) == len(full):
         return _ptrs(a, what, full, size, dtype, dev)
     if CHECK_TENSORS and _bad(a, full[1:], dtype, dev):
         _refuse(a, what, full[1:], dtype, dev)
-    return a.data_ptr().to_bytes(8, sys.byteorder) * full[0]
+    return a.data_ptr().to_bytes(8, "little") * full[0]
 
 
 _torch_module = None
@@ -444,8 +450,8 @@ def vc_reduce_scatter_norm(send, weight, out, residual=None, residual_out=None, 
     (rows,) fp32."""
     torch = _torch()
     x, dt, es, dev = _start(send)
-    N, rows, hidden = row = tuple(_shape(out, 2, "out"))
-    odt = (out[0] if out.__class__ in (list, tuple) else out).dtype
+    N, rows, hidden = row = _shape(out, 2, "out")
+    odt = (out[0] if out.__class__ in _SEQUENCES else out).dtype
     code, i8, f32 = _dtype_code(x), odt is torch.int8, torch.float32
     if i8 and scale is None:
         raise _invalid("an int8 output wants a scale")
@@ -470,7 +476,7 @@ def vc_reduce_scatter_norm_backward(dout, h, weight, rstd, dsend=None, dresidual
     ``dresidual_out`` is the gradient that reaches the sum itself."""
     x, dt, es, dev = _start(dout)
     f32 = _torch().float32
-    N, rows, hidden = row = tuple(_shape(dout, 2, "dout"))
+    N, rows, hidden = row = _shape(dout, 2, "dout")
     size = rows * hidden * es
     check(lib().vc_reduce_scatter_norm_backward(
         _ptrs(dout, "dout", row, size, dt, dev),
@@ -492,7 +498,7 @@ def vc_route(logits, ids, weights, bias=None, score="softmax", ngroups: int = 1,
     ``bias`` is (experts,) fp32 for each rank or one for all."""
     torch = _torch()
     x, dt, es, dev = _start(logits)
-    N, rows, experts = every = tuple(_shape(logits, 2, "logits"))
+    N, rows, experts = every = _shape(logits, 2, "logits")
     topk = _shape(ids, 2, "ids")[2]
     chosen, size = (N, rows, topk), rows * topk * 4
     how = _pack_how(_code(SCORES, score), topk, ngroups, topk_groups, group_top, bool(renormalize), scale)
@@ -510,7 +516,7 @@ def vc_route_backward(dweights, logits, ids, dlogits, score="softmax", renormali
     with vc_route's logits and ids."""
     torch = _torch()
     x, dt, es, dev = _start(logits)
-    N, rows, experts = every = tuple(_shape(logits, 2, "logits"))
+    N, rows, experts = every = _shape(logits, 2, "logits")
     topk = _shape(ids, 2, "ids")[2]
     chosen, size = (N, rows, topk), rows * topk * 4
     how = _pack_how(_code(SCORES, score), topk, 1, 1, 1, bool(renormalize), scale)
@@ -529,7 +535,7 @@ def vc_dispatch_plan(ids, slots, offsets, capacity: int, stream=None) -> None:
     at most."""
     i32 = _torch().int32
     x, _, _, dev = _start(ids)
-    N, rows, topk = chosen = tuple(_shape(ids, 2, "ids"))
+    N, rows, topk = chosen = _shape(ids, 2, "ids")
     ends = _shape(offsets, 1, "offsets")[1]
     if capacity < 1 or ends < 1:
         raise _invalid("capacity and the offsets' length must be at least 1")
@@ -546,7 +552,7 @@ def vc_dispatch(send, slots, recv, scale=None, recv_scale=None, stream=None) -> 
     (capacity,) where given.  fp32, bf16, fp16 or int8 rows."""
     torch = _torch()
     x, dt, es, dev = _start(send)
-    N, rows, hidden = row = tuple(_shape(send, 2, "send"))
+    N, rows, hidden = row = _shape(send, 2, "send")
     topk, cap = _shape(slots, 2, "slots")[2], _shape(recv, 2, "recv")[1]
     check(lib().vc_dispatch(
         _ptrs(send, "send", row, rows * hidden * es, dt, dev),
@@ -563,7 +569,7 @@ def vc_combine(recv, slots, out, weights=None, stream=None) -> None:
     summed.  With the gradient of recv and no weights: dispatch's gradient."""
     torch = _torch()
     x, dt, es, dev = _start(out)
-    N, rows, hidden = row = tuple(_shape(out, 2, "out"))
+    N, rows, hidden = row = _shape(out, 2, "out")
     topk, cap = _shape(slots, 2, "slots")[2], _shape(recv, 2, "recv")[1]
     chosen, size = (N, rows, topk), rows * topk * 4
     check(lib().vc_combine(
@@ -580,7 +586,7 @@ def vc_combine_backward(dout, recv, slots, weights=None, drecv=None, dweights=No
     without dweights."""
     torch = _torch()
     x, dt, es, dev = _start(dout)
-    N, rows, hidden = row = tuple(_shape(dout, 2, "dout"))
+    N, rows, hidden = row = _shape(dout, 2, "dout")
     if recv is None and drecv is None:
         raise _invalid("no gradient is asked for")
     topk, cap = _shape(slots, 2, "slots")[2], _shape(recv if recv is not None else drecv, 2, "recv")[1]

@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kMoveThreads, VEC ? 4 : 2) combine_kernel(cons
         recv[b] = d >= 0 ? static_cast<const char*>(p.recv[d]) : nullptr;
         s[b] = recv[b] + __shfl_sync(kAll, row, j) * width;
         w[b] = __shfl_sync(kAll, weight, j);
-        const R from(s[b], Bytes{recv[b], recv[b] + p.s.capacity * width});
+        const R from(s[b], count, Bytes{recv[b], recv[b] + p.s.capacity * width});
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           v[b][u] = R::zero();
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kMoveThreads, VEC ? 4 : 2) combine_kernel(cons
 #pragma unroll
       for (int b = 0; b < kCombineBatch; ++b) {
         if (!recv[b]) continue;
-        const R from(s[b], Bytes{recv[b], recv[b] + p.s.capacity * width});
+        const R from(s[b], count, Bytes{recv[b], recv[b] + p.s.capacity * width});
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           if (at + u * 32 >= count) continue;
@@ -463,8 +463,8 @@ __global__ void __launch_bounds__(kMoveThreads, VEC ? 6 : 4) combine_grad_kernel
   }
   __syncthreads();
   const char* gradient = static_cast<const char*>(p.dout[r]);
-  const R dout(gradient + t * width, Bytes{gradient, gradient + p.s.rows * width});
-  const auto answer = [&](int j) { return R(from[j], Bytes{base[j], base[j] + p.s.capacity * width}); };
+  const R dout(gradient + t * width, count, Bytes{gradient, gradient + p.s.rows * width});
+  const auto answer = [&](int j) { return R(from[j], count, Bytes{base[j], base[j] + p.s.capacity * width}); };
   for (int j0 = 0; j0 < k; j0 += kGradBatch) {
     float dot[kGradBatch];
 #pragma unroll

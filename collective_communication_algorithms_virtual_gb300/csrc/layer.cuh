@@ -328,14 +328,18 @@ struct Row {
   uint32_t m;        // bytes from there to unit 0
   int lo, hi;        // the units whose vectors are all the buffer's
 
-  __device__ __forceinline__ Row(const void* row, Bytes in) {
+  // A row of `units` units.
+  __device__ __forceinline__ Row(const void* row, int units, Bytes in) {
     base = static_cast<const char*>(row);
     if constexpr (!VEC) {
       m = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(base)) & 15;
       base -= m;
-      lo = base < in.lo;
-      const int64_t vectors = (in.hi - base) / 16;
-      hi = static_cast<int>(vectors < 0x7fffffff ? vectors : 0x7fffffff) - (m != 0);
+      lo = 0;
+      hi = units;
+      if (base < in.lo || base + (static_cast<int64_t>(units) + 1) * 16 > in.hi) {  // the buffer's first or last row
+        lo = base < in.lo;
+        hi = min(static_cast<int64_t>(units), (in.hi - base) / 16 - (m != 0));
+      }
     }
   }
   static __device__ __forceinline__ Raw zero() { return Raw{}; }

@@ -47,7 +47,7 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
 
 // One block per row; VPT units of the row in each thread.
 template <int DT, bool VEC, int VPT, bool I8>
-__global__ void __launch_bounds__(kThreads, VPT <= (VEC ? 2 : 1) ? 2 : 1) norm_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kThreads, VPT <= 2 ? 2 : 1) norm_kernel(const __grid_constant__ NormParams p) {
   using E = El<DT>;
   constexpr int kN = E::kVec;
   constexpr int kBatch = (VEC ? 8 : 4) / VPT > 0 ? (VEC ? 8 : 4) / VPT : 1;  // ranks whose loads are in flight together
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreads, VPT <= (VEC ? 2 : 1) ? 2 : 1) norm_k
   const int64_t sent = static_cast<int64_t>(p.nranks) * p.rows;
   const auto row_of = [&](const void* buffer, int64_t at_byte, int64_t rows) {
     const char* b = static_cast<const char*>(buffer);
-    return Row<E::kSize, VEC>(b + at_byte, Bytes{b, b + rows * width});
+    return Row<E::kSize, VEC>(b + at_byte, nu, Bytes{b, b + rows * width});
   };
   const auto residual = row_of(p.has_residual ? p.residual[r] : p.out[r], own, p.rows);
   const auto weights = row_of(p.weight[r], 0, 1);
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(grad_threads(VPT)) norm_grad_kernel(const __gr
   const int64_t width = static_cast<int64_t>(p.hidden) * E::kSize;
   const auto row_of = [&](const void* buffer, int64_t at_byte, int64_t rows) {
     const char* b = static_cast<const char*>(buffer);
-    return R(b + at_byte, Bytes{b, b + rows * width});
+    return R(b + at_byte, nu, Bytes{b, b + rows * width});
   };
   const R weights = row_of(p.weight[r], 0, 1);
   float dw[VPT][kN];
