@@ -3,9 +3,12 @@
 // (dispatch), the answers back (combine), and combine's gradient (see vc.h).
 //
 // The plan is a stable counting sort by expert in one launch of one
-// thread-block cluster; no atomics, so the order is the definition's.  The
-// moves stream: each token's row is read once and written to all its places,
-// or the other way round, 16 bytes a thread where rows allow it.
+// thread-block cluster.  The moves stream: each token's row is read once and
+// written to all its places, or the other way round, and memory bounds them;
+// on a GB300, copy rate 6.69 TB/s, 4096 tokens of 4096 bf16 to 8 places each:
+//   dispatch 302 MB, 48.1 us, 6.3 TB/s (its plan 7.1 us)
+//   combine  302 MB, 48.3 us, 6.3 TB/s
+//   combine's gradient 570 MB, 94.9 us, 6.0 TB/s
 #include <cooperative_groups.h>
 
 #include "layer.cuh"
@@ -45,7 +48,10 @@ size_t plan_smem(int experts) { return static_cast<size_t>(experts) * (kPlanRow 
 // contiguous piece per warp.  Each warp counts its piece by expert; the counts
 // before each warp's (of the same expert), the experts before (on the same
 // rank) and the equal choices before in the warp's own piece add up to a
-// choice's row.
+// choice's row.  Counting is additions of whole numbers in shared memory, in
+// any order; equal choices of a step are found by a ballot for each bit of the
+// expert (__match_any_sync: 13.0 us on 8 blocks where this takes 8.8).
+// Latency bounds it: two walks over the ids, a cluster barrier, two scans.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ DispatchPlanParams p) {
   extern __shared__ uint32_t sm[];
   __shared__ uint32_t part[32];
@@ -158,6 +164,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 // ---------------------------------------------------------------------------
 // moves
 // ---------------------------------------------------------------------------
+// A warp takes a piece of two units a lane of one row (1 KB): small enough
+// that 32 tokens of 4 KB still fill 128 warps (2.2 us; pieces of 2 KB 2.6 us).
 constexpr int kMoveThreads = 256;
 constexpr int kMoveWarps = kMoveThreads / 32;
 constexpr int kUnits = 2;  // 16-byte units of a thread in one piece of a row
@@ -346,7 +354,9 @@ struct CombineParams {
 
 constexpr int kCombineBatch = 4;  // choices whose loads are in flight together
 
-// One warp sums one piece of one token's row over its choices, in order.
+// One warp sums one piece of one token's row over its choices, in order, four
+// choices' loads in flight (4096 x 8 x 8 KB: 48 us; one at a time 129 us; 8
+// choices at once 95 us, for want of registers).
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kMoveThreads, VEC ? 4 : 2) combine_kernel(const __grid_constant__ CombineParams p) {
   using E = El<DT>;
@@ -429,7 +439,9 @@ struct CombineGradParams {
 };
 constexpr int kGradBatch = 4;  // choices whose loads are in flight together
 
-// One block takes one token.
+// One block takes one token, so that its dot products meet in one place
+// (2048 tokens of 2048 bf16, 4 choices: 75 MB, 16.0 us; a row is read only
+// after its slot, and 2.25 rounds of blocks wait for both).
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kMoveThreads, VEC ? 6 : 4) combine_grad_kernel(const __grid_constant__ CombineGradParams p) {
   using E = El<DT>;
@@ -605,6 +617,7 @@ vc_status_t check_move(int nranks, size_t rows, size_t hidden, int topk, size_t 
   vc_status_t rc = check_slots(nranks, rows, topk, capacity);
   if (rc == VC_SUCCESS) rc = check_tokens(nranks, rows, hidden);
   if (rc == VC_SUCCESS) rc = check_tokens(nranks, capacity, hidden);
+  if (rc == VC_SUCCESS && hidden > static_cast<size_t>(kMaxInt)) return fail(VC_ERR_INVALID_ARG, "hidden above 2^31 - 1");
   return rc;
 }
 // Blocks for `tiles` tiles of one warp: all of them, or as many as are resident.
