@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       if (b < cluster.block_rank()) before += n;
       all += n;
     }
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // the others' counts are read
   uint32_t upto = all;  // inclusive scan over the experts
 #pragma unroll

@@ -278,7 +278,9 @@ struct El {
 // (only the bytes before the first boundary and after the last one are stored
 // by element).  A last unit that the row does not fill ends in elements that
 // are not the row's: whoever sums over it masks them.  No access passes the
-// ends of a buffer.  (A combine of 4096 tokens, 8 choices and 4099 bf16: 166
+// ends of a buffer.  A load may bring bytes of the neighbouring rows along,
+// which are dropped (in an in-place call another block may be writing them);
+// a store never touches them.  (A combine of 4096 tokens, 8 choices and 4099 bf16: 166
 // us with an access per element, 94 us so, against 48 us for 4096 elements; an
 // 8-rank norm of 2048 x 8191: 107 us, against 54 us for 8192.)
 //

@@ -4,6 +4,7 @@ library.  Buffers are made-up addresses that nothing reads."""
 import ctypes
 import math
 import struct
+import subprocess
 
 import pytest
 import torch
@@ -253,3 +254,10 @@ def test_mismatched_tensors_never_reach_the_library(rec, bad):
         bad()
     assert e.value.status == b.VC_ERR_INVALID_ARG
     assert rec.calls == []
+
+
+def test_header_and_checks_from_c(tmp_path):
+    from .test_c_abi import _build_c_program
+
+    out = subprocess.run([str(_build_c_program(tmp_path, "abi_layer"))], capture_output=True, text=True)
+    assert out.returncode == 0 and out.stdout.startswith("ok"), (out.returncode, out.stderr)
