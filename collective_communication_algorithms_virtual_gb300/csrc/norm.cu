@@ -14,7 +14,12 @@ namespace vc {
 namespace layer {
 namespace {
 
-constexpr int kThreads = 512;  // most threads of a block that holds a row in registers
+// Most threads of a block that holds a row in registers, `vpt` units a thread.
+__host__ __device__ constexpr int norm_threads(bool vec, int vpt) { return vec && vpt == 2 ? 1024 : 512; }
+// Blocks of that size per SM that its registers are kept low enough for.
+__host__ __device__ constexpr int norm_blocks(bool vec, bool few, int vpt) {
+  return vec && !few && vpt == 1 ? 3 : vec && vpt == 2 ? 1 : vpt <= 3 ? 2 : 1;
+}
 
 struct NormParams {
   const void* send[VC_MAX_RANKS];
@@ -48,51 +53,74 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
   return (a & 255) | (b & 255) << 8 | (c & 255) << 16 | static_cast<uint32_t>(d) << 24;
 }
 
-// One block per row; VPT units of the row in each thread, as few as keep the
-// block within kThreads, since more warps hide more latency (8 ranks, 2048 x
-// 8192 bf16: 512 threads of 2 units 62.4 us, 256 of 4 63.3, 1024 of 1 63.3,
-// 512 of 2 on three blocks per SM 73.7).  The sum over the ranks is in rank
-// order in fp32; a thread asks for several ranks' units, the residual and the
-// weight before it uses the first (91 us before it did).
-template <int DT, bool VEC, int VPT, bool I8>
-__global__ void __launch_bounds__(kThreads, VPT <= 2 ? 2 : 1) norm_kernel(const __grid_constant__ NormParams p) {
+// A block works a row, VPT units of it in each thread.  The sum over the ranks
+// is in rank order in fp32.
+//   FEW (one or two ranks): so little is read for a row that its loads alone
+// do not keep memory busy; a block takes rows blockIdx.x, + gridDim.x, ... and
+// asks for the next row's units while it works one (4096 tokens of 4096 bf16,
+// one rank: 36.4 us with a block per row, 23.7 so).
+//   Otherwise a block per row, and a thread asks for several ranks' units, the
+// residual and the weight before it uses the first (8 ranks, 2048 x 8192 bf16
+// to 8 bits: 91 us before it did, 58.6 so): up to 512 units one of them a
+// thread, four ranks at a time and three blocks of 512 per SM (8 ranks, 4096 x
+// 4096: 57.3 us; eight at a time and two blocks 60.9), then two units a
+// thread (1024 threads of one: 63.3 against 62.4), to 1536 three (8 ranks,
+// 1024 x 10240: 43.4 us, with four 52.9), to 2048 two in blocks of 1024.
+template <int DT, bool VEC, bool FEW, int VPT, bool I8>
+__global__ void __launch_bounds__(norm_threads(VEC, VPT), norm_blocks(VEC, FEW, VPT))
+    norm_kernel(const __grid_constant__ NormParams p) {
   using E = El<DT>;
-  constexpr int kN = E::kVec;
-  constexpr int kBatch = (VEC ? 8 : 4) / VPT > 0 ? (VEC ? 8 : 4) / VPT : 1;  // ranks whose loads are in flight together
+  using R = Row<E::kSize, VEC>;
   using Out = Span<E::kSize, 16, VEC>;
+  constexpr int kN = E::kVec;
   using Quants = Span<1, kN, VEC>;
-  __shared__ float part[32];
-  __shared__ uint32_t most[32];
-  __shared__ __align__(16) unsigned char room[kThreads / 32][Out::kRoom];
-  stream_order();
-  const uint32_t r = blockIdx.y, t = blockIdx.x;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t row = static_cast<int64_t>(r) * p.rows + t;
-  const int64_t width = static_cast<int64_t>(p.hidden) * E::kSize;
-  const int64_t at = row * width;                    // the row's place in each send buffer
-  const int64_t own = static_cast<int64_t>(t) * width;  // and in rank r's own buffers
-  char* sums = p.has_residual_out ? static_cast<char*>(p.residual_out[r]) + own : nullptr;
-  const int nu = (p.hidden + kN - 1) / kN;
-  const int64_t sent = static_cast<int64_t>(p.nranks) * p.rows;
-  const auto row_of = [&](const void* buffer, int64_t at_byte, int64_t rows) {
-    const char* b = static_cast<const char*>(buffer);
-    return Row<E::kSize, VEC>(b + at_byte, nu, Bytes{b, b + rows * width});
-  };
-  const auto residual = row_of(p.has_residual ? p.residual[r] : p.out[r], own, p.rows);
-  const auto weights = row_of(p.weight[r], 0, 1);
+  // ranks whose loads are in flight together
+  constexpr int kBatch = FEW ? 2 : VPT == 1 ? 4 : (VEC ? 8 : 4) / VPT > 0 ? (VEC ? 8 : 4) / VPT : 1;
   // the residual and the weight are asked for well before they are used,
   // where registers allow it
   constexpr bool kAhead = VPT <= (VEC ? 4 : 2);
-  using R = Row<E::kSize, VEC>;
-  typename R::Raw res[VPT], weight[VPT];
-  const auto load_res = [&] {
+  __shared__ float part[2][32];
+  __shared__ uint32_t most[2][32];
+  __shared__ __align__(16) unsigned char room[norm_threads(VEC, VPT) / 32][Out::kRoom];
+  stream_order();
+  const uint32_t r = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t width = static_cast<int64_t>(p.hidden) * E::kSize;
+  const int nu = (p.hidden + kN - 1) / kN;
+  const int64_t sent = static_cast<int64_t>(p.nranks) * p.rows;
+  // a row from its place in a buffer of `rows` rows
+  const auto row_of = [&](const void* buffer, int64_t at, int64_t rows) {
+    const char* b = static_cast<const char*>(buffer);
+    return R(b + at, nu, Bytes{b, b + rows * width});
+  };
+  const int64_t block = static_cast<int64_t>(r) * p.rows * width;  // where rank r's rows begin in each send buffer
+  const R weights = row_of(p.weight[r], 0, 1);
+  struct Loaded {
+    typename R::Raw res[VPT], v[kBatch][VPT];
+  };
+  const auto load_res = [&](int64_t own, Loaded& l) {
+    const R residual = row_of(p.has_residual ? p.residual[r] : p.out[r], own, p.rows);
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       const int c = threadIdx.x + u * blockDim.x;
-      res[u] = R::zero();
-      if (p.has_residual && c < nu) res[u] = residual.load_plain(c);
+      l.res[u] = R::zero();
+      if (p.has_residual && c < nu) l.res[u] = residual.load_plain(c);
     }
   };
+  const auto load_ranks = [&](int q0, int64_t at, Loaded& l) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (q0 + b >= p.nranks) break;
+      const R from = row_of(p.send[q0 + b], at, sent);
+#pragma unroll
+      for (int u = 0; u < VPT; ++u) {
+        const int c = threadIdx.x + u * blockDim.x;
+        l.v[b][u] = R::zero();
+        if (c < nu) l.v[b][u] = from.load(c);
+      }
+    }
+  };
+  typename R::Raw weight[VPT];
   const auto load_weight = [&] {
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
@@ -101,95 +129,110 @@ __global__ void __launch_bounds__(kThreads, VPT <= 2 ? 2 : 1) norm_kernel(const 
       if (c < nu) weight[u] = weights.load_kept(c);
     }
   };
-  if (kAhead) load_res();
-  float h[VPT][kN];
+  // One row, of which the residual (kAhead or FEW) and the ranks' units (FEW) are there.
+  const auto work = [&](uint32_t t, int flip, Loaded& now) {
+    const int64_t own = t * width, at = block + own;  // the row's place in rank r's buffers, and in the send buffers
+    const R residual = row_of(p.has_residual ? p.residual[r] : p.out[r], own, p.rows);
+    float h[VPT][kN];
 #pragma unroll
-  for (int u = 0; u < VPT; ++u)
+    for (int u = 0; u < VPT; ++u)
 #pragma unroll
-    for (int i = 0; i < kN; ++i) h[u][i] = 0.f;
-  for (int q0 = 0; q0 < p.nranks; q0 += kBatch) {
-    typename R::Raw v[kBatch][VPT];
+      for (int i = 0; i < kN; ++i) h[u][i] = 0.f;
+    for (int q0 = 0; q0 < p.nranks; q0 += kBatch) {
+      if (!FEW) load_ranks(q0, at, now);
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (q0 + b >= p.nranks) break;
-      const R from = row_of(p.send[q0 + b], at, sent);
+      for (int b = 0; b < kBatch; ++b) {
+        if (q0 + b >= p.nranks) break;
+        const R from = row_of(p.send[q0 + b], at, sent);
 #pragma unroll
-      for (int u = 0; u < VPT; ++u) {
-        const int c = threadIdx.x + u * blockDim.x;
-        v[b][u] = R::zero();
-        if (c < nu) v[b][u] = from.load(c);
-      }
-    }
+        for (int u = 0; u < VPT; ++u) {
+          const int c = threadIdx.x + u * blockDim.x;
+          if (c < nu) {
+            float f[kN];
+            E::widen(from.finish(now.v[b][u], c, p.hidden), f);
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (q0 + b >= p.nranks) break;
-      const R from = row_of(p.send[q0 + b], at, sent);
-#pragma unroll
-      for (int u = 0; u < VPT; ++u) {
-        const int c = threadIdx.x + u * blockDim.x;
-        if (c < nu) {
-          float f[kN];
-          E::widen(from.finish(v[b][u], c, p.hidden), f);
-#pragma unroll
-          for (int i = 0; i < kN; ++i) h[u][i] += f[i];
+            for (int i = 0; i < kN; ++i) h[u][i] += f[i];
+          }
         }
       }
+      if (FEW) break;
     }
-  }
-  if (!kAhead) load_res();
-  if (kAhead) load_weight();
-  float ss = 0.f;
-#pragma unroll
-  for (int u = 0; u < VPT; ++u) {
-    const int c = threadIdx.x + u * blockDim.x;
-    if (p.has_residual && c < nu) {
-      float f[kN];
-      E::widen(residual.finish(res[u], c, p.hidden), f);
-#pragma unroll
-      for (int i = 0; i < kN; ++i) h[u][i] += f[i];
-    }
-    mask_unit<E::kSize, VEC>(c, p.hidden, h[u]);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) ss += h[u][i] * h[u][i];
-    if (sums) Out(room[warp], E::narrow(h[u])).write(sums, c - lane, p.hidden);
-  }
-  const float rs = 1.f / sqrtf(block_sum(ss, part) / static_cast<float>(p.hidden) + p.eps);
-  if (p.has_rstd && threadIdx.x == 0) p.rstd[r][t] = rs;
-  if (!kAhead) load_weight();
-  uint32_t top = 0;
-#pragma unroll
-  for (int u = 0; u < VPT; ++u) {
-    const int c = threadIdx.x + u * blockDim.x;
-    float w[kN];
-#pragma unroll
-    for (int i = 0; i < kN; ++i) w[i] = 0.f;
-    if (c < nu) E::widen(weights.finish(weight[u], c, p.hidden), w);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) h[u][i] = h[u][i] * rs * w[i];
-    if (I8) {
-      mask_unit<E::kSize, VEC>(c, p.hidden, h[u]);
-      if (c < nu) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) top = max(top, __float_as_uint(fabsf(h[u][i])));
-      }
-    } else {
-      Out(room[warp], E::narrow(h[u])).write(static_cast<char*>(p.out[r]) + own, c - lane, p.hidden);
-    }
-  }
-  if (I8) {
-    const Quant quant(block_max_bits(top, most));
-    if (threadIdx.x == 0) p.scale[r][t] = quant.scale;
-    int8_t* to = static_cast<int8_t*>(p.out[r]) + static_cast<int64_t>(t) * p.hidden;
+    if (!FEW && !kAhead) load_res(own, now);
+    if (!FEW && kAhead) load_weight();
+    char* sums = p.has_residual_out ? static_cast<char*>(p.residual_out[r]) + own : nullptr;
+    float ss = 0.f;
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       const int c = threadIdx.x + u * blockDim.x;
-      uint32_t w[2];
+      if (p.has_residual && c < nu) {
+        float f[kN];
+        E::widen(residual.finish(now.res[u], c, p.hidden), f);
 #pragma unroll
-      for (int i = 0; i < kN / 4; ++i)
-        w[i] = pack4(quant(h[u][4 * i]), quant(h[u][4 * i + 1]), quant(h[u][4 * i + 2]), quant(h[u][4 * i + 3]));
-      if constexpr (kN == 8) Quants(room[warp], make_uint2(w[0], w[1])).write(to, c - lane, p.hidden);
-      else Quants(room[warp], w[0]).write(to, c - lane, p.hidden);
+        for (int i = 0; i < kN; ++i) h[u][i] += f[i];
+      }
+      mask_unit<E::kSize, VEC>(c, p.hidden, h[u]);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) ss += h[u][i] * h[u][i];
+      if (sums) Out(room[warp], E::narrow(h[u])).write(sums, c - lane, p.hidden);
     }
+    const float rs = 1.f / sqrtf(block_sum(ss, part[flip]) / static_cast<float>(p.hidden) + p.eps);
+    if (p.has_rstd && threadIdx.x == 0) p.rstd[r][t] = rs;
+    if (!FEW && !kAhead) load_weight();
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < VPT; ++u) {
+      const int c = threadIdx.x + u * blockDim.x;
+      float w[kN];
+#pragma unroll
+      for (int i = 0; i < kN; ++i) w[i] = 0.f;
+      if (c < nu) E::widen(weights.finish(weight[u], c, p.hidden), w);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) h[u][i] = h[u][i] * rs * w[i];
+      if (I8) {
+        mask_unit<E::kSize, VEC>(c, p.hidden, h[u]);
+        if (c < nu) {
+#pragma unroll
+          for (int i = 0; i < kN; ++i) top = max(top, __float_as_uint(fabsf(h[u][i])));
+        }
+      } else {
+        Out(room[warp], E::narrow(h[u])).write(static_cast<char*>(p.out[r]) + own, c - lane, p.hidden);
+      }
+    }
+    if (I8) {
+      const Quant quant(block_max_bits(top, most[flip]));
+      if (threadIdx.x == 0) p.scale[r][t] = quant.scale;
+      int8_t* to = static_cast<int8_t*>(p.out[r]) + static_cast<int64_t>(t) * p.hidden;
+#pragma unroll
+      for (int u = 0; u < VPT; ++u) {
+        const int c = threadIdx.x + u * blockDim.x;
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < kN / 4; ++i)
+          w[i] = pack4(quant(h[u][4 * i]), quant(h[u][4 * i + 1]), quant(h[u][4 * i + 2]), quant(h[u][4 * i + 3]));
+        if constexpr (kN == 8) Quants(room[warp], make_uint2(w[0], w[1])).write(to, c - lane, p.hidden);
+        else Quants(room[warp], w[0]).write(to, c - lane, p.hidden);
+      }
+    }
+  };
+  if constexpr (FEW) {
+    load_weight();
+    Loaded next;
+    load_res(blockIdx.x * width, next);
+    load_ranks(0, block + blockIdx.x * width, next);
+    int flip = 0;
+    for (uint32_t t = blockIdx.x; t < p.rows; t += gridDim.x, flip ^= 1) {
+      Loaded now = next;
+      if (t + gridDim.x < p.rows) {
+        const int64_t own = (t + gridDim.x) * width;
+        load_res(own, next);
+        load_ranks(0, block + own, next);
+      }
+      work(t, flip, now);
+    }
+  } else {
+    Loaded now;
+    if (kAhead) load_res(blockIdx.x * width, now);
+    work(blockIdx.x, 0, now);
   }
 }
 
@@ -260,7 +303,7 @@ __host__ __device__ constexpr int grad_threads(int vpt) { return 128 * vpt; }
 // one array with atomics would make the last bits depend on the order).
 // Without the weight's gradient the call takes 46.6 us.
 template <int DT, bool VEC, int VPT>
-__global__ void __launch_bounds__(grad_threads(VPT)) norm_grad_kernel(const __grid_constant__ GradParams p) {
+__global__ void __launch_bounds__(grad_threads(VPT), VEC ? 1 : VPT == 1 ? 6 : 2) norm_grad_kernel(const __grid_constant__ GradParams p) {
   using E = El<DT>;
   constexpr int kN = E::kVec;
   using R = Row<E::kSize, VEC>;
@@ -363,7 +406,7 @@ __global__ void __launch_bounds__(grad_threads(VPT)) norm_grad_kernel(const __gr
       }
       if (p.has_dres || p.has_dsend) {
         const Out v(room[warp], E::narrow(d));
-        if (p.has_dres) v.write(static_cast<char*>(p.dres[r]) + own, c - lane, p.hidden);
+        if (p.has_dres) v.template write<true>(static_cast<char*>(p.dres[r]) + own, c - lane, p.hidden);
         if (p.has_dsend) {
           const int64_t at = (static_cast<int64_t>(r) * p.rows + t) * width;
           for (int q = 0; q < p.nranks; ++q) v.template write<true>(static_cast<char*>(p.dsend[q]) + at, c - lane, p.hidden);
@@ -465,13 +508,6 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_weight_kernel(const __gri
   }
 }
 
-// Units a thread holds for a row of n units: the fewest that keep the block
-// within kThreads; 0 where that is more than `most`.
-int units_per_thread(int64_t n, int most) {
-  for (int v = 1; v <= most; v *= 2)
-    if (n <= static_cast<int64_t>(v) * kThreads) return v;
-  return 0;
-}
 unsigned threads_for(int64_t n, int per_thread, int most) {
   const int64_t t = (n + per_thread - 1) / per_thread;
   return static_cast<unsigned>(std::min<int64_t>(most, (t + 31) / 32 * 32));
@@ -479,11 +515,21 @@ unsigned threads_for(int64_t n, int per_thread, int most) {
 // Threads of a block that takes a row element by element.
 unsigned any_threads(int64_t hidden) { return threads_for(hidden, 4, 1024); }
 
-template <int DT, bool VEC, int VPT>
-vc_status_t launch_norm(int dev, int64_t n, bool i8, cudaStream_t s, const NormParams& p, int64_t bytes) {
-  const Shape shape{p.rows, threads_for(n, VPT, kThreads), 0, 1, static_cast<unsigned>(p.nranks)};
-  return i8 ? launch<norm_kernel<DT, VEC, VPT, true>>(dev, shape, s, p, kNorm, 0, bytes)
-            : launch<norm_kernel<DT, VEC, VPT, false>>(dev, shape, s, p, kNorm, 0, bytes);
+// Blocks of each rank: enough to fill the GPU, at most one per row.
+uint32_t blocks_per_rank(int64_t resident, int nranks, uint32_t rows) {
+  return static_cast<uint32_t>(std::max<int64_t>(1, std::min<int64_t>(rows, resident / nranks)));
+}
+
+template <int DT, bool VEC, bool FEW, int VPT, bool I8>
+vc_status_t launch_norm(DeviceState* st, int dev, int64_t n, cudaStream_t s, const NormParams& p, int64_t bytes) {
+  constexpr auto kKernel = norm_kernel<DT, VEC, FEW, VPT, I8>;
+  Shape shape{p.rows, threads_for(n, VPT, norm_threads(VEC, VPT)), 0, 1, static_cast<unsigned>(p.nranks)};
+  if (FEW) shape.grid = blocks_per_rank(int64_t(st->nsm) * resident_blocks<kKernel>(dev, static_cast<int>(shape.block), 0), p.nranks, p.rows);
+  return launch<kKernel>(dev, shape, s, p, kNorm, 0, bytes);
+}
+template <int DT, bool VEC, bool FEW, int VPT>
+vc_status_t launch_norm(DeviceState* st, int dev, int64_t n, bool i8, cudaStream_t s, const NormParams& p, int64_t bytes) {
+  return i8 ? launch_norm<DT, VEC, FEW, VPT, true>(st, dev, n, s, p, bytes) : launch_norm<DT, VEC, FEW, VPT, false>(st, dev, n, s, p, bytes);
 }
 
 vc_status_t norm(const void* const* send, const void* const* residual, const void* const* weight,
@@ -539,30 +585,31 @@ vc_status_t norm(const void* const* send, const void* const* residual, const voi
                         static_cast<int64_t>(hidden) * es * nranks + tokens * 4 * (p.has_rstd + i8);
   return for_dtype(dtype, [&](auto code) {
     constexpr int DT = code();
-    const auto go = [&](auto vec) {  // VC_ERR_UNSUPPORTED: too long for registers
-      constexpr bool VEC = vec();
+    // VC_ERR_UNSUPPORTED: too long for registers
+    const auto go = [&](auto vec, auto few) -> vc_status_t {
+      constexpr bool VEC = vec(), FEW = few();
       const int64_t n = units_of(static_cast<int64_t>(hidden), El<DT>::kSize);
-      switch (units_per_thread(n, VEC ? 8 : 4)) {
-        case 1: return launch_norm<DT, VEC, 1>(dev, n, i8, stream, p, bytes);
-        case 2: return launch_norm<DT, VEC, 2>(dev, n, i8, stream, p, bytes);
-        case 4: return launch_norm<DT, VEC, 4>(dev, n, i8, stream, p, bytes);
-        case 8:
-          if constexpr (VEC) return launch_norm<DT, VEC, 8>(dev, n, i8, stream, p, bytes);
+      if (n <= 512) return launch_norm<DT, VEC, FEW, 1>(st, dev, n, i8, stream, p, bytes);
+      if (n <= 1024) return launch_norm<DT, VEC, FEW, 2>(st, dev, n, i8, stream, p, bytes);
+      if constexpr (VEC) {
+        if (n <= 1536) return launch_norm<DT, VEC, false, 3>(st, dev, n, i8, stream, p, bytes);
+        if (n <= 2048) return launch_norm<DT, VEC, false, 2>(st, dev, n, i8, stream, p, bytes);
+        if (n <= 4096) return launch_norm<DT, VEC, false, 8>(st, dev, n, i8, stream, p, bytes);
+      } else {
+        if (n <= 2048) return launch_norm<DT, VEC, false, 4>(st, dev, n, i8, stream, p, bytes);
       }
       return VC_ERR_UNSUPPORTED;
     };
-    const vc_status_t rc = aligned && hidden % El<DT>::kVec == 0 ? go(std::true_type{}) : go(std::false_type{});
+    const bool whole = aligned && hidden % El<DT>::kVec == 0;
+    const vc_status_t rc = !whole        ? go(std::false_type{}, std::false_type{})
+                           : nranks <= 2 ? go(std::true_type{}, std::true_type{})
+                                         : go(std::true_type{}, std::false_type{});
     if (rc != VC_ERR_UNSUPPORTED) return rc;
     const Shape shape{p.rows, any_threads(static_cast<int64_t>(hidden)), hidden * sizeof(float), 1,
                       static_cast<unsigned>(nranks)};
     return i8 ? launch<norm_any_kernel<DT, true>>(dev, shape, stream, p, kNorm, 0, bytes)
               : launch<norm_any_kernel<DT, false>>(dev, shape, stream, p, kNorm, 0, bytes);
   });
-}
-
-// Blocks of each rank: enough to fill the GPU, at most one per row.
-uint32_t blocks_per_rank(int64_t resident, int nranks, uint32_t rows) {
-  return static_cast<uint32_t>(std::max<int64_t>(1, std::min<int64_t>(rows, resident / nranks)));
 }
 
 template <auto K>

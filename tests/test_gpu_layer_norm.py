@@ -38,9 +38,11 @@ def within(got, want, bound, what):
     assert np.all(off <= bound), (what, float((off - bound).max()), np.unravel_index((off - bound).argmax(), off.shape))
 
 
-SIZES = [  # N, rows, H: one element, odd, a vector, more than one vector a thread, the longest rows
+SIZES = [  # N, rows, H: one element, odd, a vector, more than one vector a thread, the longest rows, more rows than
+    # blocks fit the GPU
     (1, 1, 1), (1, 3, 7), (2, 1, 8), (3, 2, 40), (8, 1, 4096), (2, 5, 1000), (4, 3, 2045), (1, 2, 8200),
-    (2, 1, 16384), (1, 1, 32768), (2, 1, 40001), (1, 2, 12288), (1, 1, 12287), (3, 2, 16387), (1, 1, 49152), (64, 1, 64),
+    (2, 1, 16384), (1, 1, 32768), (2, 1, 40001), (1, 2, 12288), (1, 1, 12287), (3, 2, 16387),
+    (3, 2, 10240), (3, 2, 5120), (1, 3000, 64), (2, 1500, 512), (2, 700, 5128), (1, 1, 49152), (64, 1, 64),
 ]
 
 
