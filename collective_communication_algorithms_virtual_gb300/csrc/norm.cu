@@ -6,8 +6,9 @@
 // block (rows too long for them: in shared memory, in fp32).  Memory bounds
 // them; on a GB300, copy rate 6.69 TB/s:
 //   forward, 8 ranks, 2048 tokens of 8192 bf16 to 8 bits: 352 MB, 58.6 us, 6.0 TB/s
-//   backward, 4 ranks, 4096 tokens of 4096 bf16: 268 MB, 51.2 us, 5.2 TB/s
-//   forward, 8 ranks, one token of 4096 each: 2.8 us, launch and latency
+//   backward, 4 ranks, 4096 tokens of 4096 bf16: 268 MB, 50.1 us, 5.4 TB/s
+//   forward, 1 rank, 4096 tokens of 4096 bf16: 134 MB, 23.7 us, 5.7 TB/s
+//   forward, 8 ranks, one token of 4096 each: 3.0 us, launch and latency
 #include "layer.cuh"
 
 namespace vc {
@@ -292,16 +293,16 @@ struct GradParams {
 };
 
 // Most threads of a block of the gradient whose threads hold `vpt` units (4
-// ranks x 1024 x 4096 bf16, 512 units: 256 threads of 2 51.2 us, 512 of 1
-// 51.7, 128 of 4 59).
+// ranks x 1024 x 4096 bf16, 512 units: 256 threads of 2 50.1 us, 512 of 1
+// 50.2, 128 of 4 59).
 __host__ __device__ constexpr int grad_threads(int vpt) { return 128 * vpt; }
 
 // Block b of rank r takes the rank's rows b, b + per, ...; each thread keeps
 // the weight's gradient of its columns over them, so that it leaves the chip
-// once a block instead of once a row: 304 blocks, 5 MB for 4096 columns,
-// summed by norm_weight_kernel in a fixed order (4.5 us of the 51.2; adding to
+// once a block instead of once a row: 152 blocks, 2.5 MB for 4096 columns,
+// summed by norm_weight_kernel in a fixed order (3.3 us of the 50.1; adding to
 // one array with atomics would make the last bits depend on the order).
-// Without the weight's gradient the call takes 46.6 us.
+// Without the weight's gradient the call takes 46.8 us.
 template <int DT, bool VEC, int VPT>
 __global__ void __launch_bounds__(grad_threads(VPT), VEC ? 1 : VPT == 1 ? 6 : 2) norm_grad_kernel(const __grid_constant__ GradParams p) {
   using E = El<DT>;
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(grad_threads(VPT), VEC ? 1 : VPT == 1 ? 6 : 2)
     if (c < nu) wraw[u] = weights.load_kept(c);
   }
   // A row's loads are asked for while the row before is worked, where
-  // registers allow it (4 ranks x 1024 x 4096 bf16: 53.2 us without, 51.7 with).
+  // registers allow it (4 ranks x 1024 x 4096 bf16: 51.7 with, 53.2 us without).
   constexpr bool kAhead = VEC && VPT <= 2;
   struct Loaded {
     typename R::Raw g[VPT], h[VPT], d[VPT];
