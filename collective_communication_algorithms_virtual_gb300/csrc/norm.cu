@@ -5,9 +5,9 @@
 // the norm's mean is taken while the row is on chip, in the registers of one
 // block (rows too long for them: in shared memory, in fp32).  Memory bounds
 // them; on a GB300, copy rate 6.69 TB/s:
-//   forward, 8 ranks, 2048 tokens of 8192 bf16 to 8 bits: 352 MB, 58.6 us, 6.0 TB/s
+//   forward, 8 ranks, 2048 tokens of 8192 bf16 to 8 bits: 352 MB, 57.7 us, 6.1 TB/s
 //   backward, 4 ranks, 4096 tokens of 4096 bf16: 268 MB, 50.1 us, 5.4 TB/s
-//   forward, 1 rank, 4096 tokens of 4096 bf16: 134 MB, 23.7 us, 5.7 TB/s
+//   forward, 1 rank, 4096 tokens of 4096 bf16: 134 MB, 24.0 us, 5.6 TB/s
 //   forward, 8 ranks, one token of 4096 each: 3.0 us, launch and latency
 #include "layer.cuh"
 
@@ -36,37 +36,50 @@ struct NormParams {
   float eps;
 };
 
-// Quantiser of a row whose largest magnitude has the bits `top`: a factor in
-// two steps, since 127 / max overflows for the smallest rows.
+// The larger magnitude; a NaN stays one.
+__device__ __forceinline__ float max_magnitude(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(fabsf(b)));
+  return m;
+}
+// Quantiser of a row whose largest magnitude has the bits `top`.  Added to
+// 1.5 * 2^23, whose neighbours are whole numbers, a number's nearest whole one
+// (ties to even) is left in the low bits of the sum: one operation for the
+// product, the rounding and the conversion, and no clamping, since no |y| is
+// above the largest (one rank, 4096 x 4096 bf16 to 8 bits: 25.1 us; with two
+// products, a conversion and a clamp 27.4).
 struct Quant {
-  float pre, inv, scale;
+  float inv, scale;
+  bool none, tiny;  // none: zeros, or an infinity or NaN, whose row is zeros too; tiny: 127 / max would overflow
   __device__ __forceinline__ explicit Quant(uint32_t top) {
     const float most = __uint_as_float(top);
-    pre = most < 1e-30f ? 0x1p64f : 1.f;
-    inv = most > 0.f ? 127.f / (most * pre) : 0.f;
+    none = top == 0 || top >= 0x7f800000u;
+    tiny = most < 1e-30f;
+    inv = none ? 0.f : 127.f / (tiny ? most * 0x1p64f : most);
     scale = most / 127.f;
   }
-  __device__ __forceinline__ int operator()(float y) const {  // a NaN becomes 0 (its row's scale is NaN)
-    return max(-127, min(127, __float2int_rn(y * pre * inv)));
+  __device__ __forceinline__ uint32_t byte(float y) const {  // in the low byte
+    return __float_as_uint(__fmaf_rn(tiny ? y * 0x1p64f : y, inv, 12582912.f));
+  }
+  __device__ __forceinline__ uint32_t four(const float* y) const {
+    const uint32_t lo = __byte_perm(byte(y[0]), byte(y[1]), 0x0040), hi = __byte_perm(byte(y[2]), byte(y[3]), 0x0040);
+    return none ? 0 : __byte_perm(lo, hi, 0x5410);
   }
 };
-__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
-  return (a & 255) | (b & 255) << 8 | (c & 255) << 16 | static_cast<uint32_t>(d) << 24;
-}
 
 // A block works a row, VPT units of it in each thread.  The sum over the ranks
 // is in rank order in fp32.
 //   FEW (one or two ranks): so little is read for a row that its loads alone
 // do not keep memory busy; a block takes rows blockIdx.x, + gridDim.x, ... and
 // asks for the next row's units while it works one (4096 tokens of 4096 bf16,
-// one rank: 36.4 us with a block per row, 23.7 so).
+// one rank: 36.4 us with a block per row, 24.0 so).
 //   Otherwise a block per row, and a thread asks for several ranks' units, the
 // residual and the weight before it uses the first (8 ranks, 2048 x 8192 bf16
-// to 8 bits: 91 us before it did, 58.6 so): up to 512 units one of them a
+// to 8 bits: 91 us before it did, 57.7 so): up to 512 units one of them a
 // thread, four ranks at a time and three blocks of 512 per SM (8 ranks, 4096 x
-// 4096: 57.3 us; eight at a time and two blocks 60.9), then two units a
+// 4096: 56.8 us; eight at a time and two blocks 60.9), then two units a
 // thread (1024 threads of one: 63.3 against 62.4), to 1536 three (8 ranks,
-// 1024 x 10240: 43.4 us, with four 52.9), to 2048 two in blocks of 1024.
+// 1024 x 10240: 42.1 us, with four 52.9), to 2048 two in blocks of 1024.
 template <int DT, bool VEC, bool FEW, int VPT, bool I8>
 __global__ void __launch_bounds__(norm_threads(VEC, VPT), norm_blocks(VEC, FEW, VPT))
     norm_kernel(const __grid_constant__ NormParams p) {
@@ -179,7 +192,7 @@ __global__ void __launch_bounds__(norm_threads(VEC, VPT), norm_blocks(VEC, FEW, 
     const float rs = 1.f / sqrtf(block_sum(ss, part[flip]) / static_cast<float>(p.hidden) + p.eps);
     if (p.has_rstd && threadIdx.x == 0) p.rstd[r][t] = rs;
     if (!FEW && !kAhead) load_weight();
-    uint32_t top = 0;
+    float top = 0.f;
 #pragma unroll
     for (int u = 0; u < VPT; ++u) {
       const int c = threadIdx.x + u * blockDim.x;
@@ -193,14 +206,14 @@ __global__ void __launch_bounds__(norm_threads(VEC, VPT), norm_blocks(VEC, FEW, 
         mask_unit<E::kSize, VEC>(c, p.hidden, h[u]);
         if (c < nu) {
 #pragma unroll
-          for (int i = 0; i < kN; ++i) top = max(top, __float_as_uint(fabsf(h[u][i])));
+          for (int i = 0; i < kN; ++i) top = max_magnitude(top, h[u][i]);
         }
       } else {
         Out(room[warp], E::narrow(h[u])).write(static_cast<char*>(p.out[r]) + own, c - lane, p.hidden);
       }
     }
     if (I8) {
-      const Quant quant(block_max_bits(top, most[flip]));
+      const Quant quant(block_max_bits(__float_as_uint(top), most[flip]));
       if (threadIdx.x == 0) p.scale[r][t] = quant.scale;
       int8_t* to = static_cast<int8_t*>(p.out[r]) + static_cast<int64_t>(t) * p.hidden;
 #pragma unroll
@@ -208,8 +221,7 @@ __global__ void __launch_bounds__(norm_threads(VEC, VPT), norm_blocks(VEC, FEW, 
         const int c = threadIdx.x + u * blockDim.x;
         uint32_t w[2];
 #pragma unroll
-        for (int i = 0; i < kN / 4; ++i)
-          w[i] = pack4(quant(h[u][4 * i]), quant(h[u][4 * i + 1]), quant(h[u][4 * i + 2]), quant(h[u][4 * i + 3]));
+        for (int i = 0; i < kN / 4; ++i) w[i] = quant.four(h[u] + 4 * i);
         if constexpr (kN == 8) Quants(room[warp], make_uint2(w[0], w[1])).write(to, c - lane, p.hidden);
         else Quants(room[warp], w[0]).write(to, c - lane, p.hidden);
       }
@@ -260,21 +272,21 @@ __global__ void __launch_bounds__(1024) norm_any_kernel(const __grid_constant__ 
   }
   const float rs = 1.f / sqrtf(block_sum(ss, part) / static_cast<float>(p.hidden) + p.eps);
   if (p.has_rstd && threadIdx.x == 0) p.rstd[r][t] = rs;
-  uint32_t top = 0;
+  float top = 0.f;
   for (int c = threadIdx.x; c < p.hidden; c += blockDim.x) {  // each thread reads back what it wrote
     const float y = h[c] * rs * E::load(p.weight[r], c);
     if (I8) {
       h[c] = y;
-      top = max(top, __float_as_uint(fabsf(y)));
+      top = max_magnitude(top, y);
     } else {
       E::store(p.out[r], own + c, y);
     }
   }
   if (I8) {
-    const Quant quant(block_max_bits(top, most));
+    const Quant quant(block_max_bits(__float_as_uint(top), most));
     if (threadIdx.x == 0) p.scale[r][t] = quant.scale;
     for (int c = threadIdx.x; c < p.hidden; c += blockDim.x)
-      static_cast<int8_t*>(p.out[r])[own + c] = static_cast<int8_t>(quant(h[c]));
+      static_cast<int8_t*>(p.out[r])[own + c] = static_cast<int8_t>(quant.none ? 0 : quant.byte(h[c]));
   }
 }
 
