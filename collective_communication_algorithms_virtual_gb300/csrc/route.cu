@@ -358,9 +358,9 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 16 : 4) route_kernel(con
   }
 }
 
-// The gradient: with renormalised weights or sigmoid scores only the chosen
-// logits are read.  350 instructions a token: 16384 tokens, 128 fp32 logits,
-// softmax not renormalised 8.2 us (17.6 MB, 2.6 us).
+// The gradient: with sigmoid scores only the chosen logits are read.  350
+// instructions a token: 16384 tokens, 128 fp32 logits, softmax not
+// renormalised 8.2 us (17.6 MB, 2.6 us).
 template <int DT, int V>
 __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_constant__ RouteGradParams p) {
   stream_order();
@@ -369,6 +369,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
   if (t >= p.rows) return;
   const int64_t at = static_cast<int64_t>(t) * p.experts * El<DT>::kSize;
   const char* row = static_cast<const char*>(p.logits[r]) + at;
+  float all[V];
+  if (!p.sigmoid) load_row<DT, V>(row, lane, p.experts, p.vec, all);
   // lane j: choice j's expert, its logit and the gradient of scale * (its share or score)
   int id = -1;
   float l = kNone, d = 0.f;
@@ -391,7 +393,20 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
     // logits alone, and the gradient stays among them
     const float most = warp_max(l);
     const float e = !there(l) ? 0.f : p.sigmoid ? sigmoid(l) : soft(l, most);
-    const float total = warp_sum(e);
+    float total = warp_sum(e);
+    if (!p.sigmoid) {
+      // `total` counts from the best chosen score.  The scores themselves sum
+      // to less than 2^-126 only where that one is more than 80 below the
+      // row's largest logit (exp(-80) / 1024 experts is above it).
+      const float top = row_max<V>(all);
+      if (!(most == top || most - top >= -80.f)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) all[i] = soft(all[i], top);
+        const float sum = pair_sum<V>(all);
+        const float s = warp_sum(there(l) ? __fdiv_rn(soft(l, top), sum) : 0.f);
+        if (!(s >= 0x1p-126f)) total = 0.f;
+      }
+    }
     if (total >= 0x1p-126f) {
       const float share = e / total;
       give = share * (d - warp_sum(d * share));
@@ -400,8 +415,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
   } else if (p.sigmoid) {
     give = there(l) ? d * sigmoid(l) / (1.f + expf(l)) : 0.f;
   } else {
-    float all[V];
-    load_row<DT, V>(row, lane, p.experts, p.vec, all);
     const float most = row_max<V>(all);
 #pragma unroll
     for (int i = 0; i < V; ++i) all[i] = soft(all[i], most);
@@ -538,8 +551,7 @@ vc_status_t route_grad(const float* const* dweights, const void* const* logits, 
   p.sigmoid = how->score == VC_SCORE_SIGMOID;
   p.renormalize = how->renormalize != 0;
   p.scale = how->scale;
-  const bool dense = !p.sigmoid && !p.renormalize;
-  const int64_t bytes = n * nranks * ((int64_t(nexperts) + (dense ? nexperts : k)) * es + k * 8);
+  const int64_t bytes = n * nranks * ((int64_t(nexperts) + (p.sigmoid ? k : nexperts)) * es + k * 8);
   const Shape shape{(p.rows + kWarps - 1) / kWarps, kWarps * 32, 0, 1, static_cast<unsigned>(nranks)};
   return for_dtype(dtype, [&](auto code) {
     return for_width(nexperts, [&](auto width) {
