@@ -45,6 +45,7 @@ struct RouteGradParams {
 };
 
 constexpr float kNone = -INFINITY;
+constexpr float kLowest = -3.402823466e38f;  // of the finite numbers
 
 // Lane's V logits of a row; -inf past the last expert.
 // KEPT: through L1, for what is read again: the bias by every warp (16384
@@ -147,7 +148,8 @@ struct Two {
     b = fmaxf(b, fminf(a, x));
     a = fmaxf(a, x);
   }
-  __device__ __forceinline__ float worth(int top) const { return top == 2 && b > kNone ? __fadd_rn(a, b) : a; }
+  // Of a group that has experts above kNone, whatever their sum.
+  __device__ __forceinline__ float worth(int top) const { return top == 2 && b > kNone ? fmaxf(__fadd_rn(a, b), kLowest) : a; }
 };
 
 // An expert that may be among the chosen.
@@ -192,7 +194,7 @@ __device__ __forceinline__ int choose(float* c, int topk, int lane, Candidate* l
     bound = warp_max(rest);
     if (rest == bound) rest = kNone;
   }
-  bound = fmaxf(bound, -3.402823466e38f);  // above -inf
+  bound = fmaxf(bound, kLowest);  // above -inf
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) mine += c[i] >= bound;
@@ -306,11 +308,11 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 16 : 4) route_kernel(con
       bool kept = false;
       const int group = lane & -p.group_lanes;
       for (int g = 0; g < p.keep_groups; ++g) {
-        const float top = warp_max(rest);  // -inf: a group without experts, kept or not
+        const float top = warp_max(rest);
         const int best = (__ffs(__ballot_sync(kAll, rest == top)) - 1) & -p.group_lanes;
         if (group == best) {
           kept = true;
-          rest = kNone;
+          rest = NAN;  // passed over from now on
         }
       }
       if (!kept) {

@@ -689,9 +689,10 @@ vc_status_t vc_reduce_scatter_norm_backward(const void* const* dout, const void*
  *   one whose c is -inf or NaN is not chosen either.
  * With ngroups > 1 the experts are ngroups groups of nexperts / ngroups
  * neighbours.  A group is worth its largest c (group_top 1) or the sum of its
- * two largest (group_top 2; of one, where it has one), and experts are chosen
- * from the topk_groups best groups.  Ties go to the lower index, of groups
- * and of experts.  For choice j, best first:
+ * two largest (group_top 2; of one, where it has one; a sum below every finite
+ * number counts as the lowest of them, above a group without experts), and
+ * experts are chosen from the topk_groups best groups.  Ties go to the lower
+ * index, of groups and of experts.  For choice j, best first:
  *   ids[r][t*topk + j] = the expert,
  *   weights[r][t*topk + j] = scale * s, or with renormalize
  *     scale * s / max(sum of the chosen s, 2^-126).

@@ -7,6 +7,7 @@ import torch
 import collective_communication_algorithms_virtual_gb300 as vc
 
 from . import layer_ref as ref
+from .test_gpu_route import check
 
 pytestmark = pytest.mark.gpu
 
@@ -102,3 +103,29 @@ def test_backward_beside_infinite_and_absent_logits(dt):
     p = 1 / (1 + np.exp(1.0))  # the share of logit 1 against 2
     want = 2 * p * (1 - p)
     assert np.allclose(got[2], [0, want, 0, -want], rtol=2e-6 if dt == "f32" else 2.0 ** -8, atol=0)
+
+
+LOWEST = torch.finfo(torch.float32).min
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G", [(8, 4), (24, 4), (64, 16), (128, 32), (256, 16), (160, 5), (1024, 32)])
+def test_groups_biased_to_the_lowest_number(score, E, G):
+    """A mask by the lowest finite bias: two such scores add up to less than
+    any fp32 number, and yet their group has experts.  Kept groups, more than
+    hold an ordinary expert, are then the lowest of the masked ones, which
+    come before groups that a bias of -inf empties."""
+    each = E // G
+    logits = torch.randn(1, 4, E, generator=torch.Generator().manual_seed(E)).cuda()
+    topk = min(32, 2 * each + 1)
+    masked = torch.full((E,), LOWEST, device="cuda")
+    for ordinary in ([], [1], [G - 1]):
+        for empty in ([], [0], [0, 2]):
+            bias = masked.clone()
+            for g in empty:
+                bias[g * each:(g + 1) * each] = -float("inf")
+            for g in ordinary:
+                bias[g * each:(g + 1) * each] = 0
+            for keep in (1, 2, 3, G):
+                for top in (1, 2):
+                    check(logits, bias, score, topk, G, keep, top, margin=False)
