@@ -125,22 +125,28 @@ inline vc_status_t check_tokens(int nranks, size_t rows, size_t width) {
 // host: launches
 // ---------------------------------------------------------------------------
 
-// Lets kernel K take `smem` dynamic bytes (from 32 KB on: with its static
-// ones they may pass the 48 KB that need no leave) and, where asked, a cluster
-// above the portable 8 blocks; once per device and size reached.
+// Lets kernel K take all the dynamic shared memory that a block can have,
+// where a call wants more than 32 KB (with its static bytes that may pass the
+// 48 KB that need no leave), and, where asked, a cluster above the portable 8
+// blocks; once per device.  Every thread sets the same values, so first calls
+// that race agree whatever sizes they are for.
 template <auto K>
 vc_status_t allow(int dev, size_t smem, bool big_cluster) {
-  static std::atomic<size_t> most[64];
-  static std::atomic<bool> wide[64];
-  if (smem > (32u << 10) && smem > most[dev].load(std::memory_order_relaxed)) {
-    cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static std::atomic<bool> raised[64], wide[64];
+  if (smem > (32u << 10) && !raised[dev].load(std::memory_order_acquire)) {
+    int block = 0;
+    cudaFuncAttributes own;
+    cudaError_t e = cudaDeviceGetAttribute(&block, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&own, K);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, block - static_cast<int>(own.sharedSizeBytes));
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-    most[dev].store(smem, std::memory_order_relaxed);
+    raised[dev].store(true, std::memory_order_release);
   }
-  if (big_cluster && !wide[dev].load(std::memory_order_relaxed)) {
+  if (big_cluster && !wide[dev].load(std::memory_order_acquire)) {
     cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-    wide[dev].store(true, std::memory_order_relaxed);
+    wide[dev].store(true, std::memory_order_release);
   }
   return VC_SUCCESS;
 }
