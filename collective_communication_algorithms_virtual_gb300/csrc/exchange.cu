@@ -551,13 +551,39 @@ const void* const* untyped(T* const* a) {
   return reinterpret_cast<const void* const*>(const_cast<const std::remove_const_t<T>* const*>(a));
 }
 
+// Most blocks of a cluster of the plan: 16, above the portable size, where the
+// device can place such a one with the shared memory of the most experts, else
+// 8.  Asked once per device.
+unsigned plan_cluster(int dev) {
+  static std::atomic<unsigned> most[64];
+  unsigned n = most[dev].load(std::memory_order_relaxed);
+  if (n) return n;
+  n = 8;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = plan_smem(VC_ROUTE_MAX_EXPERTS);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {16, 1, 1};
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (allow<plan_kernel>(dev, cfg.dynamicSmemBytes, true) == VC_SUCCESS &&
+      cudaOccupancyMaxActiveClusters(&clusters, plan_kernel, &cfg) == cudaSuccess && clusters >= 1)
+    n = 16;
+  cudaGetLastError();
+  clear_error();
+  most[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
 // Blocks of the cluster that sorts `total` choices: a choice per thread up to
 // 16 (32768 choices: 1 block 66 us, 8 blocks 8.8 us, 16 blocks 7.1 us; 128
-// choices: 1 block 3.8 us, 16 blocks 4.4 us).
-unsigned plan_blocks(int64_t total) {
+// choices: 1 block 3.8 us, 16 blocks 4.4 us).  The plan is the same for any.
+unsigned plan_blocks(int dev, int64_t total) {
   unsigned b = 1;
-  while (b < 16 && total > static_cast<int64_t>(b) * kPlanThreads) b *= 2;
-  return b;
+  while (b < 8 && total > static_cast<int64_t>(b) * kPlanThreads) b *= 2;
+  return total > 8 * kPlanThreads ? plan_cluster(dev) : b;
 }
 
 vc_status_t dispatch_plan(const int32_t* const* ids, int32_t* const* slots, int32_t* const* offsets, int nranks,
@@ -591,7 +617,7 @@ vc_status_t dispatch_plan(const int32_t* const* ids, int32_t* const* slots, int3
     p.offsets[r] = offsets[r];
   }
   const int64_t total = per * nranks;
-  const unsigned blocks = plan_blocks(total);
+  const unsigned blocks = plan_blocks(dev, total);
   const int64_t warps = static_cast<int64_t>(blocks) * kPlanWarps;
   p.per = static_cast<uint32_t>(per);
   p.total = static_cast<uint32_t>(total);

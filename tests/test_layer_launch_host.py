@@ -88,3 +88,16 @@ def test_first_calls_of_two_sizes_may_race(L, what):
     assert status == {"first": OK, "second": OK}, L.vc_last_error()
     assert large(L) == OK and small(L) == OK, L.vc_last_error()
     assert all(five[-1] == 0 for five in launches(L))
+
+
+@pytest.mark.parametrize("largest", [16, 8])
+def test_plan_takes_a_cluster_that_the_device_can_place(L, largest):
+    """16 blocks where a cluster of them fits the device, else the portable 8."""
+    L.fake_largest_cluster(largest)
+    for rows in (2000, 40000):
+        assert host.plan(L, rows=rows, topk=4, E=1024, cap=1 << 20,
+                         **{k: host.ptrs(host.area(i), 2, 1 << 28) for i, k in enumerate(("ids", "slots", "offsets"))}) == OK
+    assert host.plan(L, rows=4) == OK, L.vc_last_error()
+    got = launches(L)
+    assert [(grid, cluster) for grid, _, _, cluster, _ in got] == [(largest, largest)] * 2 + [(1, 1)]
+    assert all(five[-1] == 0 for five in got)
