@@ -658,7 +658,7 @@ template <class U>
 vc_status_t launch_dispatch(DeviceState* st, int dev, DispatchParams& p, int64_t row, int64_t bytes, cudaStream_t s) {
   constexpr int64_t kPiece = 32 * kUnitsOf<U>;
   p.n = row / static_cast<int64_t>(sizeof(U));
-  p.pieces = static_cast<uint32_t>((p.n + kPiece - 1) / kPiece);
+  p.pieces = static_cast<uint32_t>(std::max<int64_t>(1, (p.n + kPiece - 1) / kPiece));  // one of no units moves its token's scale
   p.tiles *= p.pieces;
   return launch<dispatch_kernel<U>>(dev, Shape{move_blocks<dispatch_kernel<U>>(st, dev, p.tiles), kMoveThreads}, s, p, kDispatch, 0,
                                     bytes);
@@ -681,7 +681,7 @@ vc_status_t dispatch(const void* const* send, const float* const* scale, const i
   if (rc == VC_SUCCESS && scale) rc = b.add(untyped(scale), nranks, n * 4, 4, false, "scale");
   if (rc == VC_SUCCESS && scale) rc = b.add(untyped(recv_scale), nranks, cap * 4, 4, true, "recv_scale");
   if (rc == VC_SUCCESS) rc = b.disjoint();
-  if (rc != VC_SUCCESS || rows == 0 || hidden == 0) return rc;
+  if (rc != VC_SUCCESS || rows == 0 || (hidden == 0 && !scale)) return rc;
   DeviceState* st = nullptr;
   int dev = 0;
   rc = device_state(&st, &dev);

@@ -101,3 +101,12 @@ def test_plan_takes_a_cluster_that_the_device_can_place(L, largest):
     got = launches(L)
     assert [(grid, cluster) for grid, _, _, cluster, _ in got] == [(largest, largest)] * 2 + [(1, 1)]
     assert all(five[-1] == 0 for five in got)
+
+
+def test_dispatch_of_no_elements_moves_scales(L):
+    """Rows of no elements have nothing to move but their scales."""
+    assert host.dispatch(L, H=0) == OK and launches(L) == []
+    scales = dict(scale=host.ptrs(host.area(3)), recv_scale=host.ptrs(host.area(4)))
+    assert host.dispatch(L, H=0, **scales) == OK
+    assert [five[0] for five in launches(L)] == [1]
+    assert host.dispatch(L, H=0, rows=0, **scales) == OK and len(launches(L)) == 1
