@@ -1,4 +1,5 @@
-"""Layer operators at the edges of their definitions: rows without elements."""
+"""Layer operators at the edges of their definitions: rows without elements,
+and calls in a row that work in place on rows off 16-byte boundaries."""
 import pytest
 import torch
 
@@ -30,3 +31,32 @@ def test_scales_move_without_rows(dt):
     vc.vc_dispatch(send, slots.cuda(), recv)
     vc.vc_dispatch(send, slots.cuda(), recv, scale=scale, recv_scale=got)
     assert torch.equal(got.cpu().view(-1), want)
+
+
+@pytest.mark.parametrize("H", [1003, 1024])
+def test_calls_in_place_one_after_another(H):
+    """Each call reads what the one before wrote in place, rows of other blocks
+    beside its own: enqueued at once, with the waits of one launch for the
+    next on the GPU alone, the bits are those of calls that the host waits for."""
+    N, rows, steps = 2, 1500, 12
+    g = torch.Generator().manual_seed(H)
+    send = (torch.randn(N, N * rows, H, generator=g) * 0.5).to(torch.bfloat16).cuda()
+    start = torch.randn(N, rows, H, generator=g).to(torch.bfloat16).cuda()
+    grad = torch.randn(N, rows, H, generator=g).to(torch.bfloat16).cuda()
+    w = (1 + 0.1 * torch.randn(H, generator=g)).to(torch.bfloat16).cuda()
+    found = []
+    for wait in (True, False, False):
+        h, d, out = start.clone(), grad.clone(), torch.empty_like(start)
+        rs = torch.empty(N, rows, device="cuda")
+        dsend = torch.empty_like(send)
+        torch.cuda.synchronize()
+        for _ in range(steps):
+            vc.vc_reduce_scatter_norm(send, w, out, residual=h, residual_out=h, rstd=rs)
+            if wait:
+                torch.cuda.synchronize()
+            vc.vc_reduce_scatter_norm_backward(out, h, w, rs, dsend=dsend, dresidual=d, dresidual_out=d)
+            if wait:
+                torch.cuda.synchronize()
+        found.append((h, d, out, dsend))
+    for other in found[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(found[0], other))
