@@ -376,9 +376,15 @@ def _bad(x, shape, dtype, dev) -> bool:
     return x.shape != shape or x.dtype is not dtype or x.get_device() != dev or not x.is_contiguous()
 
 
+def _first(a, what: str):
+    if not a:
+        raise _invalid(f"{what}: none, want one for each rank")
+    return a[0]
+
+
 def _shape(a, n: int, what: str) -> tuple:
     """(ranks, the n dimensions of each rank's tensor) of a per-rank argument."""
-    shape = (len(a), *a[0].shape) if a.__class__ in _SEQUENCES else a.shape
+    shape = (len(a), *_first(a, what).shape) if a.__class__ in _SEQUENCES else a.shape
     if len(shape) != n + 1:
         raise _invalid(f"{what}: want {n} dimensions for each rank, not {tuple(shape[1:])}")
     return shape
@@ -387,7 +393,7 @@ def _shape(a, n: int, what: str) -> tuple:
 def _start(a):
     """What a call's checks go by: a tensor of the per-rank argument, its
     dtype, element size and CUDA device."""
-    x = a[0] if a.__class__ in _SEQUENCES else a
+    x = _first(a, "tensors") if a.__class__ in _SEQUENCES else a
     dev = x.get_device()
     if dev < 0:
         raise _invalid(f"tensors must be on a CUDA device, not {x.device}")
