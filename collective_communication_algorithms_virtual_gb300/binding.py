@@ -445,6 +445,13 @@ def _torch():
 _pack_how = struct.Struct("=6if").pack  # vc_route_t: score, topk, ngroups, topk_groups, group_top, renormalize, scale
 
 
+def _how(*fields) -> bytes:
+    try:
+        return _pack_how(*fields)
+    except (struct.error, OverflowError) as e:
+        raise _invalid(f"route description {fields}: {e}") from None
+
+
 def vc_reduce_scatter_norm(send, weight, out, residual=None, residual_out=None, scale=None, rstd=None,
                            eps: float = 1e-6, stream=None) -> None:
     """ReduceScatter of the ranks' partial sums, residual and RMS norm in one pass.
@@ -507,7 +514,7 @@ def vc_route(logits, ids, weights, bias=None, score="softmax", ngroups: int = 1,
     N, rows, experts = every = _shape(logits, 2, "logits")
     topk = _shape(ids, 2, "ids")[2]
     chosen, size = (N, rows, topk), rows * topk * 4
-    how = _pack_how(_code(SCORES, score), topk, ngroups, topk_groups, group_top, bool(renormalize), scale)
+    how = _how(_code(SCORES, score), topk, ngroups, topk_groups, group_top, bool(renormalize), scale)
     check(lib().vc_route(
         _ptrs(logits, "logits", every, rows * experts * es, dt, dev),
         _shared(bias, "bias", (N, experts), experts * 4, torch.float32, dev),
@@ -525,7 +532,7 @@ def vc_route_backward(dweights, logits, ids, dlogits, score="softmax", renormali
     N, rows, experts = every = _shape(logits, 2, "logits")
     topk = _shape(ids, 2, "ids")[2]
     chosen, size = (N, rows, topk), rows * topk * 4
-    how = _pack_how(_code(SCORES, score), topk, 1, 1, 1, bool(renormalize), scale)
+    how = _how(_code(SCORES, score), topk, 1, 1, 1, bool(renormalize), scale)
     check(lib().vc_route_backward(
         _ptrs(dweights, "dweights", chosen, size, torch.float32, dev),
         _ptrs(logits, "logits", every, rows * experts * es, dt, dev),

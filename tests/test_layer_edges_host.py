@@ -43,3 +43,15 @@ def refused(rec, call):
 ])
 def test_no_tensors_are_refused(rec, call, none):
     refused(rec, lambda: call(none))
+
+
+@pytest.mark.parametrize("over", [dict(scale=1e39), dict(scale=-1e300), dict(ngroups=1 << 31), dict(group_top=-1 << 40),
+                                  dict(topk_groups=1.5), dict(score=1 << 32)])
+def test_route_numbers_that_the_library_cannot_hold_are_refused(rec, over):
+    """A scale that is finite here and infinite in fp32, numbers past int32, a
+    count that is not whole."""
+    refused(rec, lambda: b.vc_route(Fake(2, 3, 16), Fake(2, 3, 4, dtype=I), Fake(2, 3, 4), stream=1, **over))
+    over = {k: v for k, v in over.items() if k in ("scale", "score")}
+    if over:
+        refused(rec, lambda: b.vc_route_backward(Fake(2, 3, 4), Fake(2, 3, 16), Fake(2, 3, 4, dtype=I), Fake(2, 3, 16),
+                                                 stream=1, **over))
