@@ -650,12 +650,18 @@ vc_status_t vc_reduce_scatter_noalloc(const void* const* send, void* const* recv
  *   residual: NULL adds none.  residual_out: NULL writes none;
  *   residual_out[r] == residual[r] is allowed.
  *   out_dtype: dtype, or VC_INT8 with
- *     scale[r][t] = max |y| / 127,  out = y / scale rounded to nearest even;
- *   a row of zeros has scale 0 and zeros, a row with a NaN has scale NaN.
+ *     scale[r][t] = max |y| / 127,  out = y * (127 / max |y|)
+ *   where both quotients are rounded to fp32 and the product is then rounded
+ *   once, to the nearest whole number (ties to even).  That is y / scale but
+ *   for y within rounding of half a step, and but for rows whose max |y| / 127
+ *   is subnormal or 0 in fp32: their out goes to 127 all the same.  A row of
+ *   zeros has scale 0 and zeros; a row with a NaN has scale NaN and zeros, one
+ *   with an infinity and no NaN has scale infinity and zeros.
  *   scale: required with VC_INT8, else not looked at.  rstd: fp32, NULL
  *   writes none.
- *   eps: finite and >= 0.  hidden above VC_NORM_MAX_HIDDEN is
- *   VC_ERR_UNSUPPORTED.
+ *   eps: finite and >= 0, rounded to fp32.  hidden above VC_NORM_MAX_HIDDEN
+ *   is VC_ERR_UNSUPPORTED.  With hidden = 0 there is no mean, and nothing is
+ *   written.
  */
 vc_status_t vc_reduce_scatter_norm(const void* const* send, const void* const* residual, const void* const* weight,
                                    void* const* residual_out, void* const* out, float* const* scale,

@@ -1,5 +1,6 @@
 """Layer operators at the edges of their definitions: rows without elements,
-and calls in a row that work in place on rows off 16-byte boundaries."""
+8-bit rounding at half steps and of the smallest numbers, and calls in a row that work in place on rows off 16-byte boundaries."""
+import numpy as np
 import pytest
 import torch
 
@@ -60,3 +61,61 @@ def test_calls_in_place_one_after_another(H):
         found.append((h, d, out, dsend))
     for other in found[1:]:
         assert all(torch.equal(a, b) for a, b in zip(found[0], other))
+
+
+@pytest.mark.parametrize("H", [256, 1001])
+def test_eight_bits_are_the_documented_product(H):
+    """out = y times fp32's 127 / max |y|, rounded once to the nearest even
+    whole number, with y as the same call in fp32 gives it: the product of two
+    fp32 numbers is exact in 64 bits.  Rows on a grid of half steps (127 / max
+    = 1), ordinary ones, subnormal ones, one with an infinity and one with a
+    NaN (eps = 1 and a weight of 1 leave small rows as they are; on the grid
+    the weight makes up for rms)."""
+    rows = 64
+    g = torch.Generator().manual_seed(H)
+    x = torch.randn(1, rows, H, generator=g)
+    x[0, 8:16] *= 1e-30
+    x[0, 16:24] *= 1e-38
+    x[0, 24:32] *= 1e-41
+    x[0, 32:40] = torch.randint(-254, 255, (8, H), generator=g).float() / 2
+    x[0, 32:40, 3] = 127
+    x[0, 40, 5], x[0, 41, 5] = float("inf"), float("nan")
+    x = x.cuda()
+    w = torch.ones(1, H, device="cuda")
+    y = torch.empty(1, rows, H, device="cuda")
+    q, scale = torch.empty(1, rows, H, dtype=torch.int8, device="cuda"), torch.empty(1, rows, device="cuda")
+    vc.vc_reduce_scatter_norm(x, w, y, eps=1.0)
+    vc.vc_reduce_scatter_norm(x, w, q, scale=scale, eps=1.0)
+    y, q, scale = y.cpu().numpy()[0], q.cpu().numpy()[0], scale.cpu().numpy()[0]
+    top = np.abs(y).max(-1)
+    assert np.array_equal(scale, top / np.float32(127), equal_nan=True)
+    for t in range(rows):
+        if not np.isfinite(top[t]):
+            assert t in (40, 41) and not q[t].any()
+        elif top[t] > 1e-30:
+            inv = np.float32(127) / top[t]
+            assert np.array_equal(q[t], np.rint(y[t].astype(np.float64) * np.float64(inv))), t
+        else:  # 127 / max would overflow for the smallest: both are taken 2^64 times as large
+            inv = np.float32(127) / (top[t] * np.float32(2.0 ** 64))
+            assert np.array_equal(q[t], np.rint(y[t].astype(np.float64) * 2.0 ** 64 * np.float64(inv))), t
+            assert np.abs(q[t].astype(int)).max() == 127
+    assert (scale[24:32] < 2.0 ** -126).all()
+    # a row whose y are whole and half numbers up to 127: the ties go to even numbers
+    w = (x[:, 32].square().mean(-1) + 1.0).sqrt()
+    one = x[:, 32:33].clone()
+    vc.vc_reduce_scatter_norm(one, w.expand(H).contiguous(), y32 := torch.empty_like(one), eps=1.0)
+    vc.vc_reduce_scatter_norm(one, w.expand(H).contiguous(), q8 := torch.empty(1, 1, H, dtype=torch.int8, device="cuda"),
+                              scale=torch.empty(1, 1, device="cuda"), eps=1.0)
+    v = y32.cpu().numpy()[0, 0]
+    inv = np.float32(127) / np.abs(v).max()
+    assert np.array_equal(q8.cpu().numpy()[0, 0], np.rint(v.astype(np.float64) * np.float64(inv)))
+
+
+def test_infinite_values_without_a_nan():
+    """An infinite weight, on values that are not 0: scale infinity and zeros."""
+    H = 64
+    x, w = torch.randn(1, 2, H).abs().add(0.5).cuda(), torch.ones(1, H, device="cuda")
+    w[0, 7] = float("inf")
+    q, scale = torch.empty(1, 2, H, dtype=torch.int8, device="cuda"), torch.empty(1, 2, device="cuda")
+    vc.vc_reduce_scatter_norm(x, w, q, scale=scale)
+    assert torch.isinf(scale).all() and not q.any()
