@@ -1,5 +1,5 @@
 """vc_route and its backward at the ends of the number range, against the
-definition in 64 bits."""
+definition in 64 bits, and its choices bit for bit."""
 import numpy as np
 import pytest
 import torch
@@ -129,3 +129,42 @@ def test_groups_biased_to_the_lowest_number(score, E, G):
             for keep in (1, 2, 3, G):
                 for top in (1, 2):
                     check(logits, bias, score, topk, G, keep, top, margin=False)
+
+
+def pairs(x):
+    """The sum over the last dimension, neighbours first."""
+    return x if x.shape[-1] == 1 else pairs(x[..., 0::2] + x[..., 1::2])
+
+
+def scores32(l, score):
+    """Scores as single fp32 operations in the documented order."""
+    if score == "sigmoid":
+        return 1 / (1 + torch.exp(-l))
+    e = torch.exp(l - l.amax(-1, keepdim=True))
+    pad = 2 ** (l.shape[-1] - 1).bit_length() - l.shape[-1]
+    return e / pairs(torch.nn.functional.pad(e, (0, pad)))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,keep", [(48, 1, 1), (60, 4, 2), (64, 8, 3), (200, 5, 2), (256, 8, 4), (1000, 1, 1), (1024, 32, 5)])
+def test_choices_bit_for_bit(score, E, G, keep):
+    """The order of experts and groups is that of the documented fp32
+    operations, bit for bit: bf16 logits give many equal scores, and biases of
+    a few roundings decide among them.  No token is left out."""
+    rows, topk = 2048, 8
+    g = torch.Generator().manual_seed(E + G)
+    logits = torch.randn(1, rows, E, generator=g).to(torch.bfloat16).cuda()
+    s = scores32(logits.float(), score)
+    tiny = (torch.randn(E, generator=g) * 1e-6).cuda() * float(s.mean())
+    for bias in (tiny, None) if G > 1 else (tiny,):
+        ids = torch.empty(1, rows, topk, dtype=torch.int32, device="cuda")
+        w = torch.empty(1, rows, topk, device="cuda")
+        vc.vc_route(logits, ids, w, bias=bias, score=score, ngroups=G, topk_groups=keep, group_top=2)
+        c = s if bias is None else s + bias
+        if G > 1:
+            best = torch.sort(c.view(1, rows, G, E // G), dim=-1, descending=True)[0]
+            kept = torch.sort(best[..., 0] + best[..., 1], dim=-1, descending=True, stable=True)[1][..., :keep]
+            on = torch.zeros(1, rows, G, dtype=torch.bool, device="cuda").scatter(-1, kept, True)
+            c = torch.where(on.repeat_interleave(E // G, -1), c, -float("inf"))
+        want = torch.sort(c, dim=-1, descending=True, stable=True)[1][..., :topk]
+        assert torch.equal(ids.long(), want)
