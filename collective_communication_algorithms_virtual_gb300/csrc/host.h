@@ -39,8 +39,6 @@ struct DeviceState {
 vc_status_t device_state(DeviceState** out, int* dev_out);
 vc_status_t scratch_pool(DeviceState* st, int dev, cudaMemPool_t* pool);
 
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb);
-
 // One launch on `stream`, bracketed by events and recorded while the trace
 // is on (`rec` without its time).
 vc_status_t launch_traced(cudaStream_t stream, const vc_trace_record_t& rec, cudaError_t (*launch)(void*), void* arg);

@@ -554,14 +554,10 @@ struct Call {
   cudaStream_t stream = nullptr;
 };
 
-}  // namespace
-
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
 }
-
-namespace {
 
 vc_status_t plan_status(PlanStatus ps, const std::string& why) {
   if (ps == PlanStatus::Invalid) return fail(VC_ERR_INVALID_ARG, why);
