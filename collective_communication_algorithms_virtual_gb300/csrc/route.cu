@@ -9,10 +9,12 @@
 //
 // Instruction issue bounds it: 16384 tokens of 256 bf16 logits, sigmoid scores
 // with a bias, 4 of 8 groups, 8 experts chosen, take 14.7 us for 870
-// instructions a token (250 of them scores and bias, 120 groups, 230 the
-// choice), 82% of the issue slots; the 9.4 MB would take 1.4 us.  8 tokens, 64
-// experts: 2.1 us, a launch.  Four tokens a block and 32 registers keep 64
-// warps per SM (8 tokens and 48 registers: 16.8 us).
+// instructions a token, 82% of the issue slots (the 9.4 MB would take 1.4 us):
+// 490 for the row, the choice of 8 by logits and their weights (of one expert
+// 370), 245 for the scores and biases, 135 for the groups.  Softmax without
+// them, 505 instructions, 9.4 us.  8 tokens, 64 experts: 2.0 us, a launch.  Four
+// tokens a block and 32 registers keep 64 warps per SM (8 tokens and 48
+// registers: 16.8 us).
 #include "layer.cuh"
 
 namespace vc {
@@ -40,7 +42,7 @@ struct RouteGradParams {
   const int32_t* ids[VC_MAX_RANKS];
   void* dlogits[VC_MAX_RANKS];
   uint32_t rows;
-  int experts, topk, sigmoid, renormalize, vec;
+  int experts, topk, renormalize, vec;
   float scale;
 };
 
@@ -360,10 +362,15 @@ __global__ void __launch_bounds__(kWarps * 32, V <= 8 ? 16 : 4) route_kernel(con
   }
 }
 
-// The gradient: with sigmoid scores only the chosen logits are read.  350
-// instructions a token: 16384 tokens, 128 fp32 logits, softmax not
-// renormalised 8.2 us (17.6 MB, 2.6 us).
-template <int DT, int V>
+// The gradient.  With sigmoid scores only the chosen logits are read; with
+// renormalised softmax scores the row is read for its largest logit (16384
+// tokens, 256 bf16 logits, 8 chosen: 10.2 us, 9.1 us without).  The kind of
+// score is a compile-time constant: in one kernel the row's registers cost the
+// sigmoid forms 3% (the same sizes, not renormalised: 8.65 us, 8.3 us so).
+// 16384 tokens, 128 fp32 logits, 6 chosen: softmax 7.4 us for 350 instructions
+// a token (17.6 MB, 2.6 us), renormalised 6.9 us for 300; sigmoid 6.2 us for
+// 240, renormalised 7.1 us for 310.
+template <int DT, int V, bool SIGMOID>
 __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_constant__ RouteGradParams p) {
   stream_order();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -372,7 +379,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
   const int64_t at = static_cast<int64_t>(t) * p.experts * El<DT>::kSize;
   const char* row = static_cast<const char*>(p.logits[r]) + at;
   float all[V];
-  if (!p.sigmoid) load_row<DT, V>(row, lane, p.experts, p.vec, all);
+  if (!SIGMOID) load_row<DT, V>(row, lane, p.experts, p.vec, all);
   // lane j: choice j's expert, its logit and the gradient of scale * (its share or score)
   int id = -1;
   float l = kNone, d = 0.f;
@@ -394,9 +401,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
     // shares of the chosen scores; of a softmax they depend on the chosen
     // logits alone, and the gradient stays among them
     const float most = warp_max(l);
-    const float e = !there(l) ? 0.f : p.sigmoid ? sigmoid(l) : soft(l, most);
+    const float e = !there(l) ? 0.f : SIGMOID ? sigmoid(l) : soft(l, most);
     float total = warp_sum(e);
-    if (!p.sigmoid) {
+    if (!SIGMOID) {
       // `total` counts from the best chosen score.  The scores themselves sum
       // to less than 2^-126 only where that one is more than 80 below the
       // row's largest logit (exp(-80) / 1024 experts is above it).
@@ -412,9 +419,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_grad_kernel(const __grid_co
     if (total >= 0x1p-126f) {
       const float share = e / total;
       give = share * (d - warp_sum(d * share));
-      if (p.sigmoid) give *= 1.f / (1.f + expf(l));
+      if (SIGMOID) give *= 1.f / (1.f + expf(l));
     }
-  } else if (p.sigmoid) {
+  } else if (SIGMOID) {
     give = there(l) ? d * sigmoid(l) / (1.f + expf(l)) : 0.f;
   } else {
     const float most = row_max<V>(all);
@@ -550,15 +557,16 @@ vc_status_t route_grad(const float* const* dweights, const void* const* logits, 
   p.rows = static_cast<uint32_t>(rows);
   p.experts = nexperts;
   p.topk = how->topk;
-  p.sigmoid = how->score == VC_SCORE_SIGMOID;
   p.renormalize = how->renormalize != 0;
   p.scale = how->scale;
-  const int64_t bytes = n * nranks * ((int64_t(nexperts) + (p.sigmoid ? k : nexperts)) * es + k * 8);
+  const bool sigmoid = how->score == VC_SCORE_SIGMOID;
+  const int64_t bytes = n * nranks * ((int64_t(nexperts) + (sigmoid ? k : nexperts)) * es + k * 8);
   const Shape shape{(p.rows + kWarps - 1) / kWarps, kWarps * 32, 0, 1, static_cast<unsigned>(nranks)};
   return for_dtype(dtype, [&](auto code) {
     return for_width(nexperts, [&](auto width) {
       p.vec = whole_lanes(aligned, nexperts, width());
-      return launch<route_grad_kernel<code(), width()>>(dev, shape, stream, p, kRouteBackward, 0, bytes);
+      return sigmoid ? launch<route_grad_kernel<code(), width(), true>>(dev, shape, stream, p, kRouteBackward, 0, bytes)
+                     : launch<route_grad_kernel<code(), width(), false>>(dev, shape, stream, p, kRouteBackward, 0, bytes);
     });
   });
 }
