@@ -5,8 +5,8 @@
 // the norm's mean is taken while the row is on chip, in the registers of one
 // block (rows too long for them: in shared memory, in fp32).  Memory bounds
 // them; on a GB300, copy rate 6.69 TB/s:
-//   forward, 8 ranks, 2048 tokens of 8192 bf16 to 8 bits: 352 MB, 57.7 us, 6.1 TB/s
-//   backward, 4 ranks, 4096 tokens of 4096 bf16: 268 MB, 50.1 us, 5.4 TB/s
+//   forward, 8 ranks, 2048 tokens of 8192 bf16 to 8 bits: 352 MB, 57.9 us, 6.1 TB/s
+//   backward, 4 ranks, 4096 tokens of 4096 bf16: 268 MB, 50.6 us, 5.3 TB/s
 //   forward, 1 rank, 4096 tokens of 4096 bf16: 134 MB, 24.0 us, 5.6 TB/s
 //   forward, 8 ranks, one token of 4096 each: 3.0 us, launch and latency
 #include "layer.cuh"

@@ -688,7 +688,8 @@ vc_status_t vc_reduce_scatter_norm_backward(const void* const* dout, const void*
 
 /*
  * Choice of `topk` of `nexperts` experts for each token.
- *   s = softmax of the token's logits, or 1 / (1 + exp(-logit)) for each;
+ *   s = softmax of the token's logits, or 1 / (1 + exp(-logit)) for each (in
+ *       fp32: 0 below about -88.7, where the exponential overflows);
  *   c = s + bias, what the experts are compared by; without a bias (and
  *       without sums of two, below) the logits themselves, which s follows;
  *   an expert whose logit is -inf or NaN is not there: s = 0, never chosen;
