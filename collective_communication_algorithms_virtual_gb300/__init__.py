@@ -38,6 +38,8 @@ from .binding import (  # noqa: F401
     vc_dispatch,
     vc_combine,
     vc_combine_backward,
+    vc_expert_product,
+    vc_expert_product_backward,
     vc_scatter,
     vc_select_algo,
     vc_set_cost_model,

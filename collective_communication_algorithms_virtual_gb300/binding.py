@@ -51,7 +51,8 @@ KERNEL_OPS = {0: "sum", 1: "max", 2: "min"}
 
 
 LAYER_KERNELS = ("norm", "norm_backward", "norm_weight", "route", "route_backward", "dispatch_plan", "dispatch",
-                 "combine", "combine_backward")
+                 "combine", "combine_backward", "expert_product", "expert_weight", "expert_product_fp8", "quantize",
+                 "grad_norm", "clip", "pad")
 
 
 def kernel_name(code: int) -> str:
@@ -106,6 +107,8 @@ def lib() -> ctypes.CDLL:
             "vc_dispatch": [V, V, V, V, V, I, Z, Z, I, Z, I, V],
             "vc_combine": [V, V, V, V, I, Z, Z, I, Z, I, V],
             "vc_combine_backward": [V, V, V, V, V, V, I, Z, Z, I, Z, I, V],
+            "vc_expert_product": [V, V, V, V, I, I, Z, Z, Z, I, I, V],
+            "vc_expert_product_backward": [V, V, V, V, V, V, I, I, Z, Z, Z, I, I, I, V],
         }.items():
             f = getattr(L, name)
             f.argtypes = args
@@ -613,6 +616,63 @@ def vc_combine_backward(dout, recv, slots, weights=None, drecv=None, dweights=No
         _ptrs(drecv, "drecv", there, bulk, dt, dev),
         _ptrs(dweights, "dweights", chosen, size, torch.float32, dev),
         N, rows, hidden, topk, cap, _dtype_code(x), _stream_handle(stream, x)))
+
+
+def _experts(offsets, N: int, what) -> int:
+    """Experts of each rank, from the offsets (experts + 1,) of each."""
+    ends = _shape(offsets, 1, "offsets")[1]
+    if ends < 2:
+        raise _invalid(f"offsets: want {what} + 1 for each rank, not {ends}")
+    return ends - 1
+
+
+def vc_expert_product(rows, weight, offsets, out, transposed: bool = False, stream=None) -> None:
+    """Each expert's product with the rows that its rank has received.
+
+    ``rows[d]`` (capacity, in) and ``offsets[d]`` (experts of a rank + 1,)
+    int32, as vc_dispatch and vc_dispatch_plan write them; ``weight[d]``
+    (experts of a rank, in, out), or (experts of a rank, out, in) with
+    ``transposed``; ``out[d]`` (capacity, out).  Rows of no expert keep what
+    out holds."""
+    i32 = _torch().int32
+    x, dt, es, dev = _start(rows)
+    N, cap, win = row = _shape(rows, 2, "rows")
+    width, each = _shape(out, 2, "out")[2], _experts(offsets, N, "experts")
+    check(lib().vc_expert_product(
+        _ptrs(rows, "rows", row, cap * win * es, dt, dev),
+        _ptrs(weight, "weight", (N, each, width, win) if transposed else (N, each, win, width), each * win * width * es, dt, dev),
+        _ptrs(offsets, "offsets", (N, each + 1), (each + 1) * 4, i32, dev),
+        _ptrs(out, "out", (N, cap, width), cap * width * es, dt, dev),
+        N, each * N, cap, win, width, bool(transposed), _dtype_code(x), _stream_handle(stream, x)))
+
+
+def vc_expert_product_backward(dout, rows, weight, offsets, drows=None, dweight=None, transposed: bool = False,
+                               stream=None) -> None:
+    """Gradients of vc_expert_product: ``drows[d]`` (capacity, in) and
+    ``dweight[d]``, shaped as the weights, in their type or fp32, where given.
+    ``weight`` may be None without drows, ``rows`` without dweight."""
+    torch = _torch()
+    x, dt, es, dev = _start(dout)
+    N, cap, width = row = _shape(dout, 2, "dout")
+    if drows is None and dweight is None:
+        raise _invalid("no gradient is asked for")
+    if rows is None and (drows is None or dweight is not None):
+        raise _invalid("dweight wants rows")
+    win = _shape(rows if rows is not None else drows, 2, "rows")[2]
+    each = _experts(offsets, N, "experts")
+    every, n = (N, each, width, win) if transposed else (N, each, win, width), each * win * width
+    wdt = dt
+    if dweight is not None and (dweight[0] if dweight.__class__ in _SEQUENCES else dweight).dtype is torch.float32:
+        wdt = torch.float32
+    check(lib().vc_expert_product_backward(
+        _ptrs(dout, "dout", row, cap * width * es, dt, dev),
+        _ptrs(rows, "rows", (N, cap, win), cap * win * es, dt, dev),
+        _ptrs(weight, "weight", every, n * es, dt, dev),
+        _ptrs(offsets, "offsets", (N, each + 1), (each + 1) * 4, torch.int32, dev),
+        _ptrs(drows, "drows", (N, cap, win), cap * win * es, dt, dev),
+        _ptrs(dweight, "dweight", every, n * wdt.itemsize, wdt, dev),
+        N, each * N, cap, win, width, bool(transposed), _dtype_code(x),
+        DTYPES["f32"] if wdt is torch.float32 else _dtype_code(x), _stream_handle(stream, x)))
 
 
 def vc_busbw_factor(coll, nranks: int) -> float:

@@ -1,5 +1,5 @@
 // What the layer operators' translation units (norm.cu, route.cu,
-// exchange.cu) share: argument checks and launches on the host, element
+// exchange.cu, expert.cu, quantize.cu, clip.cu) share: argument checks and launches on the host, element
 // formats and small reductions on the device.
 #pragma once
 
@@ -22,7 +22,8 @@ namespace layer {
 // Kernel index of the launch trace (vc.h).
 enum Kernel : int {
   kNorm = 0, kNormBackward = 1, kNormWeight = 2, kRoute = 3, kRouteBackward = 4, kPlan = 5, kDispatch = 6,
-  kCombine = 7, kCombineBackward = 8
+  kCombine = 7, kCombineBackward = 8, kExpertProduct = 9, kExpertWeight = 10, kExpertProduct8 = 11, kQuantize = 12,
+  kGradNorm = 13, kClip = 14, kPad = 15
 };
 constexpr int kTraceLayer = 1 << 9;
 

@@ -792,6 +792,44 @@ vc_status_t vc_combine_backward(const void* const* dout, const void* const* recv
                                 size_t rows, size_t hidden, int topk, size_t capacity, vc_dtype_t dtype,
                                 vc_stream_t stream);
 
+/* Largest width of an expert's rows. */
+#define VC_EXPERT_MAX_WIDTH (1 << 20)
+
+/*
+ * The experts' products on the rows that each rank has received (vc_dispatch's
+ * recv, vc_dispatch_plan's offsets).  Expert i of rank d has weights W, block i
+ * of weight[d]; for row p in [offsets[d][i], offsets[d][i+1]):
+ *   out[d][p] = rows[d][p] W     W in_width by out_width, or
+ *   out[d][p] = rows[d][p] W^T   W out_width by in_width, with `transposed`.
+ * Rows of no expert keep what out holds; their inputs, whatever they are, do
+ * not matter.  in_width = 0 gives rows of 0.
+ *   rows[d]: capacity*in_width; weight[d]: (nexperts/nranks)*in_width*out_width;
+ *   offsets[d]: nexperts/nranks + 1, not descending; they are taken as
+ *   max(0, min(offset, capacity)).  out[d]: capacity*out_width.
+ *   nranks divides nexperts <= VC_ROUTE_MAX_EXPERTS; a width above
+ *   VC_EXPERT_MAX_WIDTH is VC_ERR_UNSUPPORTED.
+ * Sums are fp32.
+ */
+vc_status_t vc_expert_product(const void* const* rows, const void* const* weight, const int32_t* const* offsets,
+                              void* const* out, int nranks, int nexperts, size_t capacity, size_t in_width,
+                              size_t out_width, int transposed, vc_dtype_t dtype, vc_stream_t stream);
+
+/*
+ * Its gradients, with the forward call's rows, weight, offsets and sizes:
+ *   drows[d][p] = dout[d][p] W^T (W with `transposed`); rows of no expert keep
+ *   what drows holds;
+ *   dweight[d] block i = sum over the expert's rows p of rows[d][p]^T
+ *   dout[d][p] (dout[d][p]^T rows[d][p] with `transposed`), every element
+ *   written: 0 for an expert without rows.  dweight_dtype: dtype or VC_FLOAT32.
+ *   drows, dweight: NULL is not written, one at least is wanted; weight may be
+ *   NULL without drows, rows without dweight.
+ */
+vc_status_t vc_expert_product_backward(const void* const* dout, const void* const* rows, const void* const* weight,
+                                       const int32_t* const* offsets, void* const* drows, void* const* dweight,
+                                       int nranks, int nexperts, size_t capacity, size_t in_width, size_t out_width,
+                                       int transposed, vc_dtype_t dtype, vc_dtype_t dweight_dtype,
+                                       vc_stream_t stream);
+
 /* Library version, major*10000 + minor*100 + patch. */
 int vc_version(void);
 

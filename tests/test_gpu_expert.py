@@ -1,0 +1,185 @@
+"""The experts' products and their gradients against 64-bit products, within
+bounds derived in tests/expert_ref.py: types, both layouts of the weights, odd
+and whole widths, buffers at any element, and what the rows behind the last
+expert's hold before and after."""
+import numpy as np
+import pytest
+import torch
+
+import collective_communication_algorithms_virtual_gb300 as vc
+
+from . import expert_ref as ref
+from .layer_ref import DT, f64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def made(*shape, dt, g, by=1.0, shift=0):
+    """Normal numbers, each rank's buffer `shift` elements off a boundary."""
+    n = int(np.prod(shape[1:], dtype=np.int64))
+    out = []
+    for _ in range(shape[0]):
+        room = torch.zeros(n + shift + 64, dtype=DT[dt], device="cuda")
+        t = room[shift:shift + n].view(shape[1:])
+        t.copy_(torch.randn(*shape[1:], generator=g, device="cuda") * by)
+        out.append(t)
+    return out
+
+
+def host(ts):
+    return np.stack([f64(t) for t in ts])
+
+
+def offsets_of(rows):
+    ends = np.concatenate([np.zeros((len(rows), 1), np.int64), np.cumsum(rows, 1)], 1).astype(np.int32)
+    return torch.from_numpy(ends).cuda()
+
+
+def inputs(dt, rows, cap, win, width, transposed, shift=0, seed=0):
+    N, each = np.asarray(rows).shape
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = made(N, cap, win, dt=dt, g=g, shift=shift)
+    w = made(N, each, *((width, win) if transposed else (win, width)), dt=dt, g=g, by=max(win, 1) ** -0.5, shift=shift)
+    dy = made(N, cap, width, dt=dt, g=g, shift=shift)
+    return x, w, dy, offsets_of(rows)
+
+
+def check(got, want, bound, what):
+    assert np.isfinite(want).all()
+    off = np.abs(got - want)
+    bad = ~(off <= bound)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, first at {np.argwhere(bad)[0]}: {got[bad][0]} want {want[bad][0]} +- {bound[bad][0]}"
+
+
+def run(dt, rows, cap, win, width, transposed, shift=0, wide=False):
+    x, w, dy, off = inputs(dt, rows, cap, win, width, transposed, shift)
+    last = [int(e) for e in off[:, -1]]
+    for d, n in enumerate(last):  # no expert's rows must not matter
+        x[d][n:], dy[d][n:] = float("nan"), float("inf")
+    out, dx = (made(len(x), cap, n, dt=dt, g=torch.Generator(device="cuda").manual_seed(9), shift=shift) for n in (width, win))
+    dw = [torch.full(t.shape, float("nan"), dtype=torch.float32 if wide else t.dtype, device="cuda") for t in w]
+    kept = host(out), host(dx)
+    vc.vc_expert_product(x, w, off, out, transposed=transposed)
+    vc.vc_expert_product_backward(dy, x, w, off, drows=dx, dweight=dw, transposed=transposed)
+    torch.cuda.synchronize()
+    X, W, dY = (host(t) for t in (x, w, dy))
+    check(host(out), *ref.product(X, W, off.cpu(), kept[0], transposed, dt), "out")
+    check(host(dx), *ref.product(dY, W, off.cpu(), kept[1], not transposed, dt), "drows")
+    check(host(dw), *ref.weight_grad(dY, X, off.cpu(), W.shape, transposed, "f32" if wide else dt), "dweight")
+
+
+ROWS = {
+    "one": ([[1]], 1),
+    "none": ([[0, 0], [0, 0]], 3),
+    "few": ([[3, 0, 1, 2], [0, 0, 0, 5]], 9),
+    "full": ([[64, 64]], 128),
+    "ragged": ([[17, 130, 0], [1, 257, 33], [0, 0, 300]], 301),
+    "long": ([[0, 1100], [513, 15]], 1100),
+}
+WIDTHS = [(64, 128), (512, 256), (8, 8), (128, 640), (200, 72), (1003, 515), (1, 1), (7, 300), (300, 7), (65, 129)]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("rows", ROWS)
+def test_rows(dt, transposed, rows):
+    run(dt, *ROWS[rows], 136, 200, transposed)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("win,width", WIDTHS)
+def test_widths(dt, transposed, win, width):
+    run(dt, *ROWS["ragged"], win, width, transposed, wide=win % 2 == 1)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("shift", [1, 2, 4])
+def test_buffers_at_any_element(dt, shift):
+    run(dt, *ROWS["ragged"], 136, 72, False, shift=shift)
+    run(dt, *ROWS["few"], 64, 66, True, shift=shift, wide=True)
+
+
+def test_many_ranks_and_experts():
+    rng = np.random.RandomState(0)
+    run("bf16", rng.randint(0, 9, (64, 16)), 130, 72, 40, True)
+    run("f16", rng.randint(0, 3, (1, 1024)), 2048, 64, 136, False, wide=True)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_widths_of_nothing(dt):
+    """A sum over nothing is 0; a gradient over no rows too."""
+    x, w, dy, off = inputs(dt, [[2, 3]], 8, 0, 16, False)
+    out = torch.full((1, 8, 16), 7.0, dtype=DT[dt], device="cuda")
+    vc.vc_expert_product(x, w, off, out)
+    assert (out[0, :5] == 0).all() and (out[0, 5:] == 7).all()
+    dw = torch.full((1, 2, 8, 16), 7.0, dtype=DT[dt], device="cuda")
+    none = torch.empty(1, 0, 16, dtype=DT[dt], device="cuda"), torch.empty(1, 0, 8, dtype=DT[dt], device="cuda")
+    vc.vc_expert_product_backward(*none, None, torch.zeros(1, 3, dtype=torch.int32, device="cuda"), dweight=dw)
+    assert (dw == 0).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16"])
+@pytest.mark.parametrize("ends", [[[-5, 4, 400]], [[3, 2, 6]], [[0, 300, 300]], [[2 ** 31 - 1, -2 ** 31, 5]]])
+def test_offsets_outside_the_buffer(dt, ends):
+    """Taken into [0, capacity], and an end before its beginning as none."""
+    x, w, dy, _ = inputs(dt, [[4, 4]], 70, 64, 72, True)
+    off = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    out = torch.zeros(1, 70, 72, dtype=DT[dt], device="cuda")
+    dx, dw = torch.zeros(1, 70, 64, dtype=DT[dt], device="cuda"), torch.empty(1, 2, 72, 64, dtype=DT[dt], device="cuda")
+    vc.vc_expert_product(x, w, off, out, transposed=True)
+    vc.vc_expert_product_backward(dy, x, w, off, drows=dx, dweight=dw, transposed=True)
+    X, W, dY = (host(t) for t in (x, w, dy))
+    if ends != [[3, 2, 6]]:
+        check(f64(out), *ref.product(X, W, off.cpu(), np.zeros(out.shape), True, dt), "out")
+        check(f64(dx), *ref.product(dY, W, off.cpu(), np.zeros(dx.shape), False, dt), "drows")
+    check(f64(dw), *ref.weight_grad(dY, X, off.cpu(), W.shape, True, dt), "dweight")
+
+
+def test_infinities_and_nan_stay_in_their_rows():
+    for dt in ("f32", "bf16"):
+        x, w, dy, off = inputs(dt, [[40, 30]], 80, 72, 64, False)
+        clean, out = (torch.zeros(1, 80, 64, dtype=DT[dt], device="cuda") for _ in range(2))
+        vc.vc_expert_product(x, w, off, clean)
+        x[0][3, 5], x[0][45, 0] = float("inf"), float("nan")
+        vc.vc_expert_product(x, w, off, out)
+        bad = ~torch.isfinite(out[0]).all(1)
+        assert bad.nonzero()[:, 0].tolist() == [3, 45]
+        keep = ~bad
+        assert torch.equal(out[0][keep], clean[0][keep])
+
+
+def test_same_bits_again_and_on_another_stream_and_replayed():
+    x, w, dy, off = inputs("bf16", [[100, 300], [0, 77]], 400, 256, 384, True)
+    out, dx, dw = torch.zeros(2, 400, 384, dtype=DT["bf16"], device="cuda"), torch.zeros(2, 400, 256, dtype=DT["bf16"], device="cuda"), \
+        torch.zeros(2, 2, 384, 256, dtype=DT["bf16"], device="cuda")
+
+    def go(stream=None):
+        vc.vc_expert_product(x, w, off, out, transposed=True, stream=stream)
+        vc.vc_expert_product_backward(dy, x, w, off, drows=dx, dweight=dw, transposed=True, stream=stream)
+    go()
+    want = [t.clone() for t in (out, dx, dw)]
+
+    def same():
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((out, dx, dw), want))
+        for t in (out, dx, dw):
+            t.zero_()
+        torch.cuda.synchronize()
+    same()
+    side = torch.cuda.Stream()
+    go(side)
+    same()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go()
+    for _ in range(3):
+        graph.replay()
+        same()
+    assert vc.vc_device_errors() == 0
