@@ -13,6 +13,7 @@ namespace {
 using tc::Rows;
 
 constexpr int kMaxExperts = VC_ROUTE_MAX_EXPERTS;
+constexpr size_t kMaxCapacity = 0x7fff0000;  // a tile past the last row still has int32 rows
 
 // ---------------------------------------------------------------------------
 // products in fp32
@@ -142,6 +143,305 @@ __global__ void __launch_bounds__(kSimpleThreads, 2) product_simple_kernel(const
 }
 
 // ---------------------------------------------------------------------------
+// products on the tensor cores
+// ---------------------------------------------------------------------------
+// A tile is 128 of m (the weights' side, or the contiguous side of a weights'
+// gradient) by up to 256 of n (rows of one expert, or the other side), fp32
+// sums in tensor memory.  The rows stand on the n side because n may be any
+// multiple of 16: an expert's last rows cost what they are, where the m side
+// would fill up to 128.  64 of k a step.
+//   warp 0: one thread loads each step's tiles by tensor maps
+//   warp 1: one thread issues the products
+//   warps 2 to 5: tensor memory to global memory, while the next tile's
+//     products go to the other half of tensor memory
+constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
+constexpr int kTcThreads = 192, kMaxStages = 12;
+constexpr int kTileBytesA = kTileM * kTileK * 2;
+constexpr uint32_t kColumns = 512;  // two accumulators
+constexpr size_t kTcSmem = 220 << 10;
+
+template <int R>
+struct ProductParams {
+  CUtensorMap a[R], b[R];
+  void* out[R];
+  const int32_t* offsets[R];
+  int32_t capacity;
+  int M, N, K;  // as SimpleParams
+  int experts, each;
+  uint32_t type;  // of the operands (tc::instruction)
+  int out_dtype;
+  bool pairs;     // out's rows start on 4-byte boundaries
+};
+
+struct Tile {
+  int d, i;        // rank, its expert
+  int32_t first;   // its first row (of weights' gradients: of k)
+  int64_t row;     // of out
+  int n0, n, m0;
+  int k;           // elements
+};
+template <bool WEIGHT, class P>
+__device__ __forceinline__ Tile tile_at(const P& p, const uint32_t* ends, uint32_t t, int& e) {
+  Tile x;
+  const uint32_t across = (p.M + kTileM - 1) / kTileM;
+  uint32_t at = t;
+  if constexpr (WEIGHT) {
+    const uint32_t every = across * tc::pieces(p.N, kTileN);
+    e = t / every;
+    at -= e * every;
+  } else {
+    while (ends[e] <= t) ++e;
+    if (e) at -= ends[e - 1];
+  }
+  x.d = e / p.each;
+  x.i = e % p.each;
+  const Rows r = tc::rows_of(p.offsets[x.d], x.i, p.capacity);
+  const int count = WEIGHT ? p.N : r.count, piece = tc::piece_of(count, kTileN, 16);
+  x.n0 = static_cast<int>(at / across) * piece;
+  x.n = min(piece, count - x.n0);
+  x.m0 = static_cast<int>(at % across) * kTileM;
+  x.first = WEIGHT ? r.first : r.first + x.n0;
+  x.row = WEIGHT ? static_cast<int64_t>(x.i) * p.N + x.n0 : x.first;
+  x.k = WEIGHT ? r.count : p.K;
+  return x;
+}
+
+// 32 accumulated columns of a warp (lane: m) to `columns` rows of out, lane 0's
+// first element at `at`.  PAIRS: neighbouring lanes trade halves, so that each
+// store is two elements of one row.
+template <int OUT, bool PAIRS>
+__device__ __forceinline__ void store_columns(const uint32_t (&v)[32], char* at, int64_t pitch, int columns, bool there) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (PAIRS) {
+    const bool odd = lane & 1;
+    char* to = at + (lane & ~1) * 2 + (odd ? pitch : 0);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      if (j >= columns) break;
+      const float mine = __uint_as_float(odd ? v[j + 1] : v[j]);
+      const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1));
+      if (there && j + odd < columns)
+        *reinterpret_cast<uint32_t*>(to) = dev::pack2<OUT == VC_FLOAT16>(odd ? other : mine, odd ? mine : other);
+      to += 2 * pitch;
+    }
+  } else {
+    char* to = at + lane * El<OUT>::kSize;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (j >= columns) break;
+      if (there) El<OUT>::store(to, 0, __uint_as_float(v[j]));
+      to += pitch;
+    }
+  }
+}
+
+// A: M runs along the rows of a's tiles (weights in by out; weights' gradients).
+template <bool AMN, bool WEIGHT, int R>
+__global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_constant__ ProductParams<R> p) {
+  extern __shared__ unsigned char dynamic[];
+  __shared__ uint32_t ends[WEIGHT ? 1 : kMaxExperts];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
+  __shared__ uint32_t columns, gone;
+  __shared__ int longest;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kMaxStages, sums_full = empty + 8 * kMaxStages,
+                 sums_empty = sums_full + 16, done = sums_empty + 16;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) tc::bar_init(full + 8 * s, 1), tc::bar_init(empty + 8 * s, 1);
+    for (int s = 0; s < 2; ++s) tc::bar_init(sums_full + 8 * s, 1), tc::bar_init(sums_empty + 8 * s, 4);
+    tc::bar_init(done, 1);
+    gone = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tc::take_columns(tc::smem_addr(&columns), kColumns);
+  tc::before_sync();
+  stream_order();
+  const uint32_t across = (p.M + kTileM - 1) / kTileM;
+  if constexpr (!WEIGHT) {
+    if (warp == 0) tc::list_tiles(p.offsets, p.experts, p.each, p.capacity, kTileN, across, ends, &longest);
+  }
+  __syncthreads();
+  tc::after_sync();
+  const uint32_t total = WEIGHT ? p.experts * across * tc::pieces(p.N, kTileN) : ends[p.experts - 1];
+  // Stages as small as the longest piece of n allows: few rows, many stages.
+  const int widest = tc::piece_of(WEIGHT ? p.N : longest, kTileN, 16);
+  const uint32_t stage_bytes = kTileBytesA + (WEIGHT ? (widest + 63) / 64 * 8192 : (widest + 31) / 32 * 4096);
+  const uint32_t tiles = (tc::smem_addr(dynamic) + 1023) & ~1023u;
+  const int stages = min(kMaxStages, static_cast<int>((kTcSmem - 1024) / stage_bytes));
+  const uint32_t sums = columns;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int e = 0, s = 0;
+      uint32_t phase = 0, issued = 0;
+      bool ok = true;
+      for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
+        const Tile x = tile_at<WEIGHT>(p, ends, t, e);
+        const int boxes = WEIGHT ? (x.n + 63) / 64 : (x.n + 31) / 32;
+        const uint32_t bytes = kTileBytesA + boxes * (WEIGHT ? 8192 : 4096);
+        const CUtensorMap *a = p.a + x.d, *b = p.b + x.d;
+        for (int k = 0; k < x.k; k += kTileK) {
+          if (!tc::bar_wait(empty + 8 * s, phase ^ 1, &gone)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = full + 8 * s, to = tiles + s * stage_bytes;
+          tc::bar_expect(bar, bytes);
+          if constexpr (WEIGHT) {
+            tc::load2d(to, a, bar, x.m0, x.first + k);
+            tc::load2d(to + 8192, a, bar, x.m0 + 64, x.first + k);
+            for (int j = 0; j < boxes; ++j) tc::load2d(to + kTileBytesA + j * 8192, b, bar, x.n0 + j * 64, x.first + k);
+          } else {
+            if constexpr (AMN) {
+              tc::load3d(to, a, bar, x.m0, k, x.i);
+              tc::load3d(to + 8192, a, bar, x.m0 + 64, k, x.i);
+            } else {
+              tc::load3d(to, a, bar, k, x.m0, x.i);
+            }
+            for (int j = 0; j < boxes; ++j) tc::load2d(to + kTileBytesA + j * 4096, b, bar, k, x.first + j * 32);
+          }
+          ++issued;
+          if (++s == stages) s = 0, phase ^= 1;
+        }
+      }
+      // The block ends after its last loads and products, on whatever path.
+      for (int j = 0; j < stages && issued > static_cast<uint32_t>(j); ++j) {
+        if (s-- == 0) s = stages - 1, phase ^= 1;
+        if (ok) ok = tc::bar_wait(empty + 8 * s, phase, &gone);
+        else tc::bar_wait(full + 8 * s, phase, &gone);
+      }
+    }
+  } else if (warp == 1) {
+    int e = 0, s = 0, half = 0;
+    uint32_t phase = 0, half_phase = 0;
+    bool ok = true;
+    for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      const Tile x = tile_at<WEIGHT>(p, ends, t, e);
+      if (!tc::warp_wait(sums_empty + 8 * half, half_phase ^ 1, &gone)) break;
+      tc::after_sync();
+      const uint32_t to = sums + half * kTileN;
+      const uint32_t how = tc::instruction(p.type, AMN, WEIGHT, (x.n + 15) / 16 * 16, kTileM);
+      for (int k = 0; k < x.k; k += kTileK) {
+        if (!tc::warp_wait(full + 8 * s, phase, &gone)) {
+          ok = false;
+          break;
+        }
+        tc::after_sync();
+        const uint32_t a = tiles + s * stage_bytes, b = a + kTileBytesA;
+        const int left = min(kTileK, x.k - k), parts = (left + 15) / 16;
+        if constexpr (WEIGHT) {
+          if (left % 16 != 0) {  // the rows behind the expert's last are not its own: 0 instead
+            const int n = (parts * 16 - left) * 8, boxes = 2 + (x.n + 63) / 64;
+            for (int j = lane; j < n * boxes; j += 32)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a + j / n * 8192 + left * 128 + j % n * 16), "r"(0) : "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
+        }
+        if (lane == 0) {
+          for (int j = 0; j < parts; ++j)
+            tc::mma16(to, AMN ? tc::desc_mn(a + j * 2048, 8192) : tc::desc_k(a + j * 32),
+                      WEIGHT ? tc::desc_mn(b + j * 2048, 8192) : tc::desc_k(b + j * 32), how, k + j > 0);
+          tc::commit(empty + 8 * s);
+        }
+        __syncwarp();
+        if (++s == stages) s = 0, phase ^= 1;
+      }
+      if (ok && lane == 0) tc::commit(sums_full + 8 * half);
+      __syncwarp();
+      if (half ^= 1; half == 0) half_phase ^= 1;
+    }
+    if (__any_sync(0xffffffffu, gone)) {  // products in flight end before tensor memory is freed
+      if (lane == 0) tc::commit(done);
+      for (uint32_t it = 0; it < tc::kSoon && !tc::bar_test(done, 0); ++it) __nanosleep(64);
+    }
+  } else {
+    int e = 0, half = 0;
+    uint32_t half_phase = 0;
+    const int part = warp & 3;  // the lanes of tensor memory that this warp reaches
+    for (uint32_t t = blockIdx.x; t < total; t += gridDim.x) {
+      const Tile x = tile_at<WEIGHT>(p, ends, t, e);
+      if (!tc::warp_wait(sums_full + 8 * half, half_phase, &gone, tc::kLate)) break;
+      tc::after_sync();
+      const int es = p.out_dtype == VC_FLOAT32 ? 4 : 2, m = x.m0 + part * 32;
+      const int64_t pitch = static_cast<int64_t>(p.M) * es;
+      char* out = static_cast<char*>(p.out[x.d]) + x.row * pitch + static_cast<int64_t>(m) * es;
+      const bool there = m + lane < p.M;
+      for (int c = 0; c < x.n; c += 32) {
+        uint32_t v[32];
+        if (x.k > 0) {
+          tc::load_columns(sums + (part << 21) + half * kTileN + c, v);
+          tc::loaded(v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0;
+        }
+        if (c + 32 >= x.n) {
+          tc::before_sync();
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(sums_empty + 8 * half);
+        }
+        const int columns = min(32, x.n - c);
+        if (WEIGHT && p.out_dtype == VC_FLOAT32) store_columns<VC_FLOAT32, false>(v, out, pitch, columns, there);
+        else if (p.out_dtype == VC_BFLOAT16)
+          p.pairs ? store_columns<VC_BFLOAT16, true>(v, out, pitch, columns, there) : store_columns<VC_BFLOAT16, false>(v, out, pitch, columns, there);
+        else
+          p.pairs ? store_columns<VC_FLOAT16, true>(v, out, pitch, columns, there) : store_columns<VC_FLOAT16, false>(v, out, pitch, columns, there);
+        out += 32 * pitch;
+      }
+      if (half ^= 1; half == 0) half_phase ^= 1;
+    }
+  }
+  tc::before_sync();
+  __syncthreads();
+  tc::after_sync();
+  if (warp == 1) tc::free_columns(sums, kColumns);
+  if (gone && threadIdx.x == 0) atomicOr(&dev::g_device_error, 4u);
+}
+
+// -- operands off 16-byte boundaries --------------------------------------------
+// Tensor maps want them, so such rows are copied to scratch first, a row each
+// 16 bytes' multiple apart: the rows that the experts have, the weights of
+// experts that have rows.
+struct PadParams {
+  const void* from[VC_MAX_RANKS];
+  const int32_t* offsets[VC_MAX_RANKS];
+  char* to;
+  int64_t rows;          // of each rank
+  int64_t width, pitch;  // elements, bytes
+  int64_t group;         // rows of each expert's weights; 0: the experts' rows
+  int32_t capacity;
+  int nranks, each;
+};
+constexpr int kPadThreads = 256;
+
+template <int ES>
+__global__ void __launch_bounds__(kPadThreads) pad_kernel(const __grid_constant__ PadParams p) {
+  stream_order();
+  const int lane = threadIdx.x & 31;
+  const int d = blockIdx.y;
+  const int64_t warps = gridDim.x * (kPadThreads / 32);
+  int64_t last = p.rows;
+  if (p.group == 0) {
+    int32_t most = 0;
+    for (int i = lane; i < p.each; i += 32) {
+      const Rows r = tc::rows_of(p.offsets[d], i, p.capacity);
+      most = max(most, r.first + r.count);
+    }
+    last = __reduce_max_sync(0xffffffffu, most);
+  }
+  const char* from = static_cast<const char*>(p.from[d]);
+  const Bytes ends{from, from + p.rows * p.width * ES};
+  const int units = static_cast<int>(p.pitch / 16);
+  for (int64_t r = blockIdx.x * (kPadThreads / 32) + threadIdx.x / 32; r < last; r += warps) {
+    if (p.group != 0 && tc::rows_of(p.offsets[d], static_cast<int>(r / p.group), p.capacity).count == 0) continue;
+    const Row<ES, false> row(from + r * p.width * ES, units, ends);
+    uint4* to = reinterpret_cast<uint4*>(p.to + (d * p.rows + r) * p.pitch);
+    for (int c = lane; c < units; c += 32) to[c] = row.finish(row.load(c), c, p.width);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
 const void* const* untyped(const int32_t* const* a) { return reinterpret_cast<const void* const*>(a); }
@@ -156,6 +456,7 @@ vc_status_t check_sizes(Sizes* z, int nranks, int nexperts, size_t capacity, siz
   if (rc != VC_SUCCESS) return rc;
   if (nexperts < 1 || nexperts > VC_ROUTE_MAX_EXPERTS || nexperts % nranks != 0)
     return fail(VC_ERR_INVALID_ARG, "nexperts must be in [1, VC_ROUTE_MAX_EXPERTS] and a multiple of nranks");
+  if (capacity > kMaxCapacity) return fail(VC_ERR_INVALID_ARG, "too many rows");
   if (in > VC_EXPERT_MAX_WIDTH || out > VC_EXPERT_MAX_WIDTH) return fail(VC_ERR_UNSUPPORTED, "a width above VC_EXPERT_MAX_WIDTH");
   rc = check_tokens(nranks, capacity, std::max(in, out));
   if (rc != VC_SUCCESS) return rc;
@@ -174,14 +475,156 @@ int64_t row_tiles(const Sizes& z, int most) {
   return z.nranks * (std::min<int64_t>(z.each, z.capacity) + z.capacity / most);
 }
 
-// rows (capacity, in) times weights, in by out or out by in, to out (capacity, out).
-vc_status_t rows_product(DeviceState* st, int dev, const Sizes& z, const void* const* rows, const void* const* weight,
+// Blocks of one kernel that the GPU holds, for `tiles` of them at most.
+unsigned grid_of(DeviceState* st, int64_t tiles) { return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(tiles, st->nsm))); }
+
+// Scratch of one call, from the library's pool.
+class Scratch {
+ public:
+  Scratch(DeviceState* st, int dev, cudaStream_t stream) : st_(st), dev_(dev), stream_(stream) {}
+  ~Scratch() {
+    if (mem_) cudaFreeAsync(mem_, stream_);
+  }
+  vc_status_t take(int64_t bytes) {
+    cudaMemPool_t pool;
+    vc_status_t rc = scratch_pool(st_, dev_, &pool);
+    if (rc != VC_SUCCESS) return rc;
+    cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void**>(&mem_), static_cast<size_t>(bytes), pool, stream_);
+    if (e == cudaErrorMemoryAllocation) {
+      cudaGetLastError();
+      mem_ = nullptr;
+      return fail(VC_ERR_NOMEM, "scratch allocation of " + std::to_string(bytes) + " bytes failed");
+    }
+    return e == cudaSuccess ? VC_SUCCESS : cuda_fail(e, "cudaMallocFromPoolAsync");
+  }
+  char* mem() const { return mem_; }
+
+ private:
+  DeviceState* st_;
+  int dev_;
+  cudaStream_t stream_;
+  char* mem_ = nullptr;
+};
+
+// What a tensor map reads: rows of `width` elements, `pitch` bytes apart.
+struct Operand {
+  const void* p[VC_MAX_RANKS];
+  int64_t rows, width, pitch, group;  // group: as PadParams
+  int es;
+  int64_t padded = -1;  // where its copy is in scratch
+
+  Operand(const void* const* a, const Sizes& z, int64_t rows, int64_t width, int64_t group, int es)
+      : rows(rows), width(width), pitch(width * es), group(group), es(es) {
+    uintptr_t all = static_cast<uintptr_t>(pitch);
+    for (int r = 0; r < z.nranks; ++r) {
+      p[r] = a[r];
+      all |= reinterpret_cast<uintptr_t>(a[r]);
+    }
+    if (rows != 0 && width != 0 && all % 16 != 0) padded = 0;
+  }
+};
+
+// Copies the operands that want it to scratch.
+vc_status_t pad(DeviceState* st, int dev, const Sizes& z, const int32_t* const* offsets, Operand* const* ops, int n, Scratch* scratch,
+                int* step, cudaStream_t stream) {
+  int64_t need = 0;
+  for (int i = 0; i < n; ++i)
+    if (ops[i]->padded >= 0) {
+      Operand& o = *ops[i];
+      o.pitch = (o.width * o.es + 15) / 16 * 16;
+      o.padded = need;
+      need += (z.nranks * o.rows * o.pitch + 255) / 256 * 256;
+    }
+  if (need == 0) return VC_SUCCESS;
+  vc_status_t rc = scratch->take(need);
+  for (int i = 0; i < n && rc == VC_SUCCESS; ++i)
+    if (ops[i]->padded >= 0) {
+      Operand& o = *ops[i];
+      PadParams p = {};
+      for (int r = 0; r < z.nranks; ++r) {
+        p.from[r] = o.p[r];
+        p.offsets[r] = offsets[r];
+      }
+      p.to = scratch->mem() + o.padded;
+      p.rows = o.rows;
+      p.width = o.width;
+      p.pitch = o.pitch;
+      p.group = o.group;
+      p.capacity = static_cast<int32_t>(z.capacity);
+      p.nranks = z.nranks;
+      p.each = z.each;
+      constexpr auto K = pad_kernel<2>;
+      const int64_t fit = (int64_t(st->nsm) * resident_blocks<K>(dev, kPadThreads, 0) + z.nranks - 1) / z.nranks;
+      const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((o.rows + 7) / 8, fit));
+      rc = launch<K>(dev, Shape{blocks, kPadThreads, 0, 1, static_cast<unsigned>(z.nranks)}, stream, p, kPad, (*step)++,
+                     z.nranks * o.rows * (o.width * o.es + o.pitch));
+      for (int r = 0; r < z.nranks; ++r) o.p[r] = p.to + r * o.rows * o.pitch;
+    }
+  return rc;
+}
+
+CUtensorMapDataType map_type(vc_dtype_t d) { return d == VC_BFLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16; }
+
+vc_status_t map_rows(CUtensorMap* map, vc_dtype_t dtype, const Operand& o, int r, uint32_t box) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(o.width), static_cast<uint64_t>(o.rows)}, strides[1] = {static_cast<uint64_t>(o.pitch)};
+  return tc::tensor_map(map, map_type(dtype), 2, o.p[r], dims, strides, 64, box);
+}
+vc_status_t map_weights(CUtensorMap* map, vc_dtype_t dtype, const Operand& o, int r, uint32_t box) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(o.width), static_cast<uint64_t>(o.group), static_cast<uint64_t>(o.rows / o.group)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(o.pitch), static_cast<uint64_t>(o.pitch * o.group)};
+  return tc::tensor_map(map, map_type(dtype), 3, o.p[r], dims, strides, 64, box);
+}
+
+// One launch of the tensor-core kernel.  a: weights or the right side of their
+// gradient; b: rows or the left side.
+template <bool AMN, bool WEIGHT, int R>
+vc_status_t launch_product(DeviceState* st, int dev, const Sizes& z, const Operand& a, const Operand& b, const int32_t* const* offsets,
+                           void* const* out, int64_t M, int64_t N, int64_t K, vc_dtype_t dtype, vc_dtype_t out_dtype, int64_t tiles,
+                           int64_t bytes, int step, cudaStream_t stream) {
+  ProductParams<R> p;
+  p.pairs = M % 2 == 0;
+  for (int r = 0; r < z.nranks; ++r) {
+    vc_status_t rc = VC_SUCCESS;
+    if (a.rows != 0 && a.width != 0 && b.rows != 0 && b.width != 0) {  // else no step loads anything
+      rc = WEIGHT ? map_rows(&p.a[r], dtype, a, r, 64) : map_weights(&p.a[r], dtype, a, r, AMN ? 64 : 128);
+      if (rc == VC_SUCCESS) rc = map_rows(&p.b[r], dtype, b, r, WEIGHT ? 64 : 32);
+    }
+    if (rc != VC_SUCCESS) return rc;
+    p.out[r] = out[r];
+    p.offsets[r] = offsets[r];
+    p.pairs = p.pairs && reinterpret_cast<uintptr_t>(out[r]) % 4 == 0;
+  }
+  p.capacity = static_cast<int32_t>(z.capacity);
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.experts = z.nexperts;
+  p.each = z.each;
+  p.type = dtype == VC_BFLOAT16 ? 1 : 0;
+  p.out_dtype = out_dtype;
+  return launch<product_kernel<AMN, WEIGHT, R>>(dev, Shape{grid_of(st, tiles), kTcThreads, kTcSmem}, stream, p,
+                                                WEIGHT ? kExpertWeight : kExpertProduct, step, bytes);
+}
+
+// rows (capacity, in) times weights, in by width or width by in, to out (capacity, width).
+vc_status_t rows_product(DeviceState* st, int dev, const Sizes& z, const Operand& rows, const Operand& weight,
                          const int32_t* const* offsets, void* const* out, int64_t in, int64_t width, bool transposed,
                          vc_dtype_t dtype, int step, cudaStream_t stream) {
+  const int64_t bytes = (z.nranks * z.capacity * (in + width) + z.nexperts * in * width) * dtype_size(dtype);
+  if (dtype != VC_FLOAT32) {
+    const int64_t tiles = row_tiles(z, kTileN) * ((width + kTileM - 1) / kTileM);
+    const auto go = [&](auto mn, auto ranks) {
+      return launch_product<mn(), false, ranks()>(st, dev, z, weight, rows, offsets, out, width, 0, in, dtype, dtype, tiles, bytes, step, stream);
+    };
+    const auto sized = [&](auto mn) {
+      return z.nranks <= 8 ? go(mn, std::integral_constant<int, 8>{}) : go(mn, std::integral_constant<int, VC_MAX_RANKS>{});
+    };
+    return transposed ? sized(std::false_type{}) : sized(std::true_type{});
+  }
   SimpleParams p = {};
   for (int r = 0; r < z.nranks; ++r) {
-    p.a[r] = weight[r];
-    p.b[r] = rows[r];
+    p.a[r] = weight.p[r];
+    p.b[r] = rows.p[r];
     p.out[r] = out[r];
     p.offsets[r] = offsets[r];
   }
@@ -195,22 +638,27 @@ vc_status_t rows_product(DeviceState* st, int dev, const Sizes& z, const void* c
   p.K = static_cast<int>(in);
   p.experts = z.nexperts;
   p.each = z.each;
-  const int64_t bytes = (z.nranks * z.capacity * (in + width) + z.nexperts * in * width) * dtype_size(dtype);
   const int64_t tiles = row_tiles(z, kSimpleN) * ((width + kSimpleM - 1) / kSimpleM);
-  return for_dtype(dtype, [&](auto code) {
-    constexpr auto K = product_simple_kernel<code(), code(), false>;
-    return launch<K>(dev, Shape{simple_blocks<K>(st, dev, tiles), kSimpleThreads}, stream, p, kExpertProduct, step, bytes);
-  });
+  constexpr auto K = product_simple_kernel<VC_FLOAT32, VC_FLOAT32, false>;
+  return launch<K>(dev, Shape{simple_blocks<K>(st, dev, tiles), kSimpleThreads}, stream, p, kExpertProduct, step, bytes);
 }
 
 // dweight(n, m) = sum over the expert's rows of left(row, n) * right(row, m).
-vc_status_t weights_gradient(DeviceState* st, int dev, const Sizes& z, const void* const* left, const void* const* right,
+vc_status_t weights_gradient(DeviceState* st, int dev, const Sizes& z, const Operand& left, const Operand& right,
                              const int32_t* const* offsets, void* const* dweight, int64_t N, int64_t M, vc_dtype_t dtype,
                              vc_dtype_t out_dtype, int step, cudaStream_t stream) {
+  const int64_t bytes = z.nranks * z.capacity * (N + M) * dtype_size(dtype) + z.nexperts * N * M * dtype_size(out_dtype);
+  if (dtype != VC_FLOAT32) {
+    const int64_t tiles = z.nexperts * ((N + kTileN - 1) / kTileN) * ((M + kTileM - 1) / kTileM);
+    const auto go = [&](auto ranks) {
+      return launch_product<true, true, ranks()>(st, dev, z, right, left, offsets, dweight, M, N, 0, dtype, out_dtype, tiles, bytes, step, stream);
+    };
+    return z.nranks <= 8 ? go(std::integral_constant<int, 8>{}) : go(std::integral_constant<int, VC_MAX_RANKS>{});
+  }
   SimpleParams p = {};
   for (int r = 0; r < z.nranks; ++r) {
-    p.a[r] = right[r];
-    p.b[r] = left[r];
+    p.a[r] = right.p[r];
+    p.b[r] = left.p[r];
     p.out[r] = dweight[r];
     p.offsets[r] = offsets[r];
   }
@@ -222,15 +670,9 @@ vc_status_t weights_gradient(DeviceState* st, int dev, const Sizes& z, const voi
   p.N = static_cast<int>(N);
   p.experts = z.nexperts;
   p.each = z.each;
-  const int64_t bytes = z.nranks * z.capacity * (N + M) * dtype_size(dtype) + z.nexperts * N * M * dtype_size(out_dtype);
   const int64_t tiles = z.nexperts * ((N + kSimpleN - 1) / kSimpleN) * ((M + kSimpleM - 1) / kSimpleM);
-  const auto go = [&](auto code, auto out) {
-    constexpr auto K = product_simple_kernel<code(), out(), true>;
-    return launch<K>(dev, Shape{simple_blocks<K>(st, dev, tiles), kSimpleThreads}, stream, p, kExpertWeight, step, bytes);
-  };
-  return for_dtype(dtype, [&](auto code) {
-    return out_dtype == VC_FLOAT32 ? go(code, std::integral_constant<int, VC_FLOAT32>{}) : go(code, code);
-  });
+  constexpr auto K = product_simple_kernel<VC_FLOAT32, VC_FLOAT32, true>;
+  return launch<K>(dev, Shape{simple_blocks<K>(st, dev, tiles), kSimpleThreads}, stream, p, kExpertWeight, step, bytes);
 }
 
 vc_status_t product(const void* const* rows, const void* const* weight, const int32_t* const* offsets, void* const* out,
@@ -252,7 +694,16 @@ vc_status_t product(const void* const* rows, const void* const* weight, const in
   int dev = 0;
   rc = device_state(&st, &dev);
   if (rc != VC_SUCCESS) return rc;
-  return rows_product(st, dev, z, rows, weight, offsets, out, z.in, z.out, transposed != 0, dtype, 0, stream);
+  Operand x(rows, z, z.capacity, z.in, 0, es);
+  Operand w(weight, z, z.each * (transposed ? z.out : z.in), transposed ? z.in : z.out, transposed ? z.out : z.in, es);
+  Scratch scratch(st, dev, stream);
+  int step = 0;
+  if (dtype != VC_FLOAT32) {
+    Operand* const ops[] = {&x, &w};
+    rc = pad(st, dev, z, offsets, ops, 2, &scratch, &step, stream);
+  }
+  if (rc != VC_SUCCESS) return rc;
+  return rows_product(st, dev, z, x, w, offsets, out, z.in, z.out, transposed != 0, dtype, step, stream);
 }
 
 vc_status_t product_grad(const void* const* dout, const void* const* rows, const void* const* weight,
@@ -276,23 +727,67 @@ vc_status_t product_grad(const void* const* dout, const void* const* rows, const
   if (rc == VC_SUCCESS && dweight) rc = b.add(dweight, nranks, z.each * z.in * z.out * ws, ws, true, "dweight");
   if (rc == VC_SUCCESS) rc = b.disjoint();
   if (rc != VC_SUCCESS) return rc;
+  const bool to_rows = drows && z.capacity != 0 && z.in != 0, to_weight = dweight && z.in != 0 && z.out != 0;
+  if (!to_rows && !to_weight) return VC_SUCCESS;
   DeviceState* st = nullptr;
   int dev = 0;
-  if (drows && z.capacity != 0 && z.in != 0) {
-    rc = device_state(&st, &dev);
-    if (rc == VC_SUCCESS) rc = rows_product(st, dev, z, dout, weight, offsets, drows, z.out, z.in, !transposed, dtype, 0, stream);
-    if (rc != VC_SUCCESS) return rc;
+  rc = device_state(&st, &dev);
+  if (rc != VC_SUCCESS) return rc;
+  const int64_t outer = transposed ? z.out : z.in, inner = transposed ? z.in : z.out;
+  Operand dy(dout, z, z.capacity, z.out, 0, es);
+  Operand x(to_weight ? rows : dout, z, to_weight ? z.capacity : 0, z.in, 0, es);
+  Operand w(to_rows ? weight : dout, z, to_rows ? z.each * outer : 0, inner, outer, es);
+  Scratch scratch(st, dev, stream);
+  int step = 0;
+  if (dtype != VC_FLOAT32) {
+    Operand* const ops[] = {&dy, &x, &w};
+    rc = pad(st, dev, z, offsets, ops, 3, &scratch, &step, stream);
   }
-  if (dweight && z.in != 0 && z.out != 0) {
-    rc = device_state(&st, &dev);
-    if (rc == VC_SUCCESS)
-      rc = transposed ? weights_gradient(st, dev, z, dout, rows, offsets, dweight, z.out, z.in, dtype, dweight_dtype, drows != nullptr, stream)
-                      : weights_gradient(st, dev, z, rows, dout, offsets, dweight, z.in, z.out, dtype, dweight_dtype, drows != nullptr, stream);
-  }
+  if (rc == VC_SUCCESS && to_rows)
+    rc = rows_product(st, dev, z, dy, w, offsets, drows, z.out, z.in, !transposed, dtype, step++, stream);
+  if (rc == VC_SUCCESS && to_weight)
+    rc = transposed ? weights_gradient(st, dev, z, dy, x, offsets, dweight, z.out, z.in, dtype, dweight_dtype, step, stream)
+                    : weights_gradient(st, dev, z, x, dy, offsets, dweight, z.in, z.out, dtype, dweight_dtype, step, stream);
   return rc;
 }
 
 }  // namespace
+
+cudaError_t take_product_errors(cudaStream_t stream, uint32_t* flags) {
+  static const uint32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(flags, dev::g_device_error, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess)
+    e = cudaMemcpyToSymbolAsync(dev::g_device_error, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, stream);
+  return e;
+}
+
+namespace tc {
+vc_status_t tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* data, const uint64_t* dims,
+                       const uint64_t* strides, uint32_t box0, uint32_t box1) {
+  // the driver's call, found once through the runtime: nothing links with the driver
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::atomic<Encode> found{nullptr};
+  Encode encode = found.load(std::memory_order_acquire);
+  if (!encode) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult seen;
+    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &seen);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDriverEntryPointByVersion");
+    if (seen != cudaDriverEntryPointSuccess || !f) return fail(VC_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+    encode = reinterpret_cast<Encode>(f);
+    found.store(encode, std::memory_order_release);
+  }
+  cuuint64_t d[3], s[2];
+  cuuint32_t box[3] = {box0, box1, 1}, one[3] = {1, 1, 1};
+  for (int i = 0; i < rank; ++i) d[i] = dims[i];
+  for (int i = 0; i + 1 < rank; ++i) s[i] = strides[i];
+  const CUresult r = encode(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(data), d, s, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(VC_ERR_CUDA, "cuTensorMapEncodeTiled: error " + std::to_string(static_cast<int>(r)));
+  return VC_SUCCESS;
+}
+}  // namespace tc
 }  // namespace layer
 }  // namespace vc
 

@@ -47,6 +47,8 @@ namespace layer {
 // Copies the exchange kernels' own device error word to *flags and clears it,
 // in stream order (exchange.cu).
 cudaError_t take_exchange_errors(cudaStream_t stream, uint32_t* flags);
+// The same of the experts' products (expert.cu).
+cudaError_t take_product_errors(cudaStream_t stream, uint32_t* flags);
 }  // namespace layer
 
 // No exception leaves a C entry point.

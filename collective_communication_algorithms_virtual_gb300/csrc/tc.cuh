@@ -51,6 +51,11 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
   return false;
 }
 
+// The same of a whole warp, whose lanes go on or give up together.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gone, uint32_t limit = kSoon) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, gone, limit));
+}
+
 // ---------------------------------------------------------------------------
 // device: loads by tensor maps
 // ---------------------------------------------------------------------------

@@ -2161,11 +2161,12 @@ VC_EXPORT vc_status_t vc_device_errors(vc_stream_t stream, uint32_t* flags) {
     const uint32_t zero = 0;
     cudaError_t e = cudaMemcpyFromSymbolAsync(flags, dev::g_device_error, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(dev::g_device_error, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, s);
-    uint32_t exchange = 0;
+    uint32_t exchange = 0, product = 0;
     if (e == cudaSuccess) e = layer::take_exchange_errors(s, &exchange);
+    if (e == cudaSuccess) e = layer::take_product_errors(s, &product);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device error word");
-    *flags |= exchange;
+    *flags |= exchange | product;
     return VC_SUCCESS;
   });
 }
