@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
   tc::after_sync();
   const uint32_t total = WEIGHT ? p.experts * across * tc::pieces(p.N, kTileN) : ends[p.experts - 1];
   // Stages as small as the longest piece of n allows: few rows, many stages.
-  const int widest = tc::piece_of(WEIGHT ? p.N : longest, kTileN, 16);
+  // Above kTileN rows an expert with fewer may have the longer pieces.
+  const int widest = WEIGHT ? tc::piece_of(p.N, kTileN, 16) : min(kTileN, (longest + 15) / 16 * 16);
   const uint32_t stage_bytes = kTileBytesA + (WEIGHT ? (widest + 63) / 64 * 8192 : (widest + 31) / 32 * 4096);
   const uint32_t tiles = (tc::smem_addr(dynamic) + 1023) & ~1023u;
   const int stages = min(kMaxStages, static_cast<int>((kTcSmem - 1024) / stage_bytes));

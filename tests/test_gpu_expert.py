@@ -106,6 +106,14 @@ def test_buffers_at_any_element(dt, shift):
     run(dt, *ROWS["few"], 64, 66, True, shift=shift, wide=True)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_several_tiles_of_a_block(dt, transposed):
+    """More tiles than the GPU has multiprocessors, long sums, and experts
+    whose pieces are longer than those of one with more rows."""
+    run(dt, [[700, 500, 256], [0, 513, 31]], 1500, 648, 4104, transposed)
+
+
 def test_many_ranks_and_experts():
     rng = np.random.RandomState(0)
     run("bf16", rng.randint(0, 9, (64, 16)), 130, 72, 40, True)
