@@ -107,6 +107,9 @@ def lib() -> ctypes.CDLL:
             "vc_dispatch": [V, V, V, V, V, I, Z, Z, I, Z, I, V],
             "vc_combine": [V, V, V, V, I, Z, Z, I, Z, I, V],
             "vc_combine_backward": [V, V, V, V, V, V, I, Z, Z, I, Z, I, V],
+            "vc_expert_product_fp8": [V, V, V, V, V, V, I, I, Z, Z, Z, I, V],
+            "vc_quantize_fp8": [V, V, V, V, I, Z, Z, Z, I, I, V],
+            "vc_clip_grad_norm": [V, V, V, V, I, Z, V, ctypes.c_double, I, V],
             "vc_expert_product": [V, V, V, V, I, I, Z, Z, Z, I, I, V],
             "vc_expert_product_backward": [V, V, V, V, V, V, I, I, Z, Z, Z, I, I, I, V],
         }.items():
@@ -565,7 +568,7 @@ def vc_dispatch_plan(ids, slots, offsets, capacity: int, stream=None) -> None:
 def vc_dispatch(send, slots, recv, scale=None, recv_scale=None, stream=None) -> None:
     """``send[r]``'s rows (rows, hidden) to the slots' rows of ``recv[d]``
     (capacity, hidden), and ``scale[r]`` (rows,) fp32 to ``recv_scale[d]``
-    (capacity,) where given.  fp32, bf16, fp16 or int8 rows."""
+    (capacity,) where given.  fp32, bf16, fp16, int8 or float8_e4m3fn rows."""
     torch = _torch()
     x, dt, es, dev = _start(send)
     N, rows, hidden = row = _shape(send, 2, "send")
@@ -576,7 +579,8 @@ def vc_dispatch(send, slots, recv, scale=None, recv_scale=None, stream=None) -> 
         _ptrs(slots, "slots", (N, rows, topk), rows * topk * 4, torch.int32, dev),
         _ptrs(recv, "recv", (N, cap, hidden), cap * hidden * es, dt, dev),
         _ptrs(recv_scale, "recv_scale", (N, cap), cap * 4, torch.float32, dev),
-        N, rows, hidden, topk, cap, DTYPES["i8"] if dt is torch.int8 else _dtype_code(x), _stream_handle(stream, x)))
+        N, rows, hidden, topk, cap, DTYPES["i8"] if dt in (torch.int8, torch.float8_e4m3fn) else _dtype_code(x),
+        _stream_handle(stream, x)))
 
 
 def vc_combine(recv, slots, out, weights=None, stream=None) -> None:
@@ -673,6 +677,108 @@ def vc_expert_product_backward(dout, rows, weight, offsets, drows=None, dweight=
         _ptrs(dweight, "dweight", every, n * wdt.itemsize, wdt, dev),
         N, each * N, cap, win, width, bool(transposed), _dtype_code(x),
         DTYPES["f32"] if wdt is torch.float32 else _dtype_code(x), _stream_handle(stream, x)))
+
+
+FP8_BLOCK = 128  # VC_FP8_BLOCK
+
+
+def _blocks(n: int) -> int:
+    return -(-n // FP8_BLOCK)
+
+
+def vc_quantize_fp8(x, out, scale, offsets=None, block_rows: int = 1, stream=None) -> None:
+    """Rounds ``x[r]`` (rows, width) or (matrices, rows, width) to
+    ``out[r]``, float8_e4m3fn of the same shape, with ``scale[r]`` fp32: one for
+    each 128 of a row (``block_rows`` 1), shape (.., rows, ceil(width / 128)),
+    or for each 128 rows by 128 (``block_rows`` 128).  ``offsets[d]`` (experts
+    of a rank + 1,) int32: only the rows that the rank's experts have."""
+    torch = _torch()
+    t, dt, es, dev = _start(x)
+    shape = (len(x), *x[0].shape) if x.__class__ in _SEQUENCES else tuple(x.shape)
+    if len(shape) not in (3, 4):
+        raise _invalid(f"x: want (rows, width) or (matrices, rows, width) for each rank, not {tuple(shape[1:])}")
+    N, rows, width = shape[0], shape[-2], shape[-1]
+    mats = shape[1] if len(shape) == 4 else 1
+    if block_rows not in (1, FP8_BLOCK):
+        raise _invalid(f"block_rows is 1 or {FP8_BLOCK}, not {block_rows}")
+    n, down = mats * rows * width, -(-rows // block_rows)
+    count = None
+    if offsets is not None:
+        ends = _experts(offsets, N, "experts") + 1
+        first = _ptrs(offsets, "offsets", (N, ends), ends * 4, torch.int32, dev)
+        count = struct.pack(f"={N}Q", *(a + 4 * (ends - 1) for a in struct.unpack(f"={N}Q", first)))
+    check(lib().vc_quantize_fp8(
+        _ptrs(x, "x", shape, n * es, dt, dev),
+        _ptrs(out, "out", shape, n, torch.float8_e4m3fn, dev),
+        _ptrs(scale, "scale", (*shape[:-2], down, _blocks(width)), mats * down * _blocks(width) * 4, torch.float32, dev),
+        count, N, mats, rows, width, block_rows, _dtype_code(t), _stream_handle(stream, t)))
+
+
+def vc_expert_product_fp8(rows, row_scale, weight, weight_scale, offsets, out, stream=None) -> None:
+    """vc_expert_product of float8_e4m3fn ``rows[d]`` (capacity, in) and
+    ``weight[d]`` (experts of a rank, out, in), with the scales that
+    vc_quantize_fp8 gives them: ``row_scale[d]`` (capacity, ceil(in / 128)) and
+    ``weight_scale[d]`` (experts of a rank, ceil(out / 128), ceil(in / 128)).
+    ``out[d]`` (capacity, out) in fp32, bf16 or fp16."""
+    torch = _torch()
+    x, dt, es, dev = _start(out)
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    N, cap, win = row = _shape(rows, 2, "rows")
+    width, each = _shape(out, 2, "out")[2], _experts(offsets, N, "experts")
+    across, down = _blocks(win), _blocks(width)
+    check(lib().vc_expert_product_fp8(
+        _ptrs(rows, "rows", row, cap * win, f8, dev),
+        _ptrs(row_scale, "row_scale", (N, cap, across), cap * across * 4, f32, dev),
+        _ptrs(weight, "weight", (N, each, width, win), each * win * width, f8, dev),
+        _ptrs(weight_scale, "weight_scale", (N, each, down, across), each * down * across * 4, f32, dev),
+        _ptrs(offsets, "offsets", (N, each + 1), (each + 1) * 4, torch.int32, dev),
+        _ptrs(out, "out", (N, cap, width), cap * width * es, dt, dev),
+        N, each * N, cap, win, width, _dtype_code(x), _stream_handle(stream, x)))
+
+
+def vc_clip_grad_norm(grads, norm, max_norm=None, out=None, across: bool = True, stream=None) -> None:
+    """The norm of the ranks' gradients, and their clipping by it.
+
+    ``grads[r]``: rank r's tensors, the same types in the same order on every
+    rank, any sizes; ``norm`` (ranks,) fp32, or one scalar tensor for each
+    rank.  With ``across`` the norm is over all ranks (each holds shards of one
+    model), without over each rank's own.  ``max_norm`` None: the norm alone;
+    else gradients above it are scaled to it, in place or into ``out[r]``."""
+    torch = _torch()
+    N = len(grads)
+    mine = [t for ts in grads for t in ts]
+    T = len(mine) // N if N else 0
+    if any(len(ts) != T for ts in grads):
+        raise _invalid("the ranks must hold the same number of tensors")
+    like = norm[0] if norm.__class__ in _SEQUENCES else norm
+    dev = like.get_device()
+    if dev < 0:
+        raise _invalid(f"tensors must be on a CUDA device, not {like.device}")
+    types = [t.dtype for t in mine[:T]]
+    sizes = [t.numel() for t in mine]
+    where = None
+    if max_norm is None:
+        if out is not None:
+            raise _invalid("out wants a max_norm")
+    else:
+        where = mine if out is None else [t for ts in out for t in ts]
+        if len(where) != len(mine) or (out is not None and any(len(ts) != T for ts in out)):
+            raise _invalid("out: want a tensor for each gradient")
+    if CHECK_TENSORS:
+        for ts in (mine,) if where is None or where is mine else (mine, where):
+            for t, dt, n in zip(ts, types * N, sizes):
+                if t.dtype is not dt or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+                    raise _invalid(f"gradients: want contiguous {n} of {dt} on cuda:{dev}, not {tuple(t.shape)} {t.dtype} on "
+                                   f"{t.device}" + ("" if t.is_contiguous() else " (not contiguous)"))
+    codes = {dt: _dtype_code(t) for dt, t in zip(types, mine)}
+    M = N * T
+
+    def packed(ts):
+        return struct.pack(f"={M}Q", *[t.data_ptr() for t in ts])
+    check(lib().vc_clip_grad_norm(
+        packed(mine), None if where is None else packed(where), struct.pack(f"={M}Q", *sizes),
+        struct.pack(f"={T}i", *[codes[dt] for dt in types]), N, T, _ptrs(norm, "norm", (N,), 4, torch.float32, dev),
+        0.0 if max_norm is None else max_norm, bool(across), _stream_handle(stream, like)))
 
 
 def vc_busbw_factor(coll, nranks: int) -> float:

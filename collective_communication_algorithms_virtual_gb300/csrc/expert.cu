@@ -400,6 +400,205 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
   if (gone && threadIdx.x == 0) atomicOr(&dev::g_device_error, 4u);
 }
 
+// ---------------------------------------------------------------------------
+// products of 8-bit operands
+// ---------------------------------------------------------------------------
+// out(row, o) = sum over blocks b of 128 k of s(row, b) * w(o / 128, b) * (the
+// block's products, summed in tensor memory).  Each block's sums go to one of
+// two accumulators in turn; eight warps take them from there, scaled, into
+// registers, while the products of the next block go to the other one.  The
+// rows stand on the m side here, so that a thread has one row's scale: with
+// rows on the n side every sum would want its own from shared memory, more
+// reads than products.
+//   warp 0 loads, warp 1 issues the products, warps 4 to 11 scale and store;
+// these hold 128 sums a thread and take the registers that the first four warps
+// give up (launched with 168 each: 4 x 40 + 8 x 232 = 12 x 168).
+constexpr int kTile8N = 256, kTile8K = 128;
+constexpr int kTc8Threads = 384;
+constexpr int kTileBytesB8 = kTile8N * kTile8K;
+
+template <int R>
+struct Product8Params {
+  CUtensorMap rows[R], weight[R];
+  const float* row_scale[R];
+  const float* weight_scale[R];
+  void* out[R];
+  const int32_t* offsets[R];
+  int32_t capacity;
+  int M, K;       // outputs, inputs
+  int experts, each;
+  bool whole;     // out's rows are whole 16 bytes on 16-byte boundaries
+};
+
+struct Tile8 {
+  int d, i;
+  int32_t first;  // row
+  int n, m0;      // rows, first output
+};
+template <class P>
+__device__ __forceinline__ Tile8 tile8_at(const P& p, const uint32_t* ends, uint32_t t, int& e) {
+  Tile8 x;
+  while (ends[e] <= t) ++e;
+  const uint32_t at = e ? t - ends[e - 1] : t, across = (p.M + kTile8N - 1) / kTile8N;
+  x.d = e / p.each;
+  x.i = e % p.each;
+  const Rows r = tc::rows_of(p.offsets[x.d], x.i, p.capacity);
+  const int n0 = static_cast<int>(at / across) * kTileM;
+  x.n = min(kTileM, r.count - n0);
+  x.first = r.first + n0;
+  x.m0 = static_cast<int>(at % across) * kTile8N;
+  return x;
+}
+
+template <int OUT, int R>
+__global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_constant__ Product8Params<R> p) {
+  extern __shared__ unsigned char dynamic[];
+  __shared__ uint32_t ends[kMaxExperts];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
+  __shared__ uint32_t columns, gone;
+  __shared__ int longest;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kMaxStages, sums_full = empty + 8 * kMaxStages,
+                 sums_empty = sums_full + 16, done = sums_empty + 16;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) tc::bar_init(full + 8 * s, 1), tc::bar_init(empty + 8 * s, 1);
+    for (int s = 0; s < 2; ++s) tc::bar_init(sums_full + 8 * s, 1), tc::bar_init(sums_empty + 8 * s, 8);
+    tc::bar_init(done, 1);
+    gone = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tc::take_columns(tc::smem_addr(&columns), kColumns);
+  tc::before_sync();
+  stream_order();
+  if (warp == 0)
+    tc::list_tiles(p.offsets, p.experts, p.each, p.capacity, kTileM, (p.M + kTile8N - 1) / kTile8N, ends, &longest);
+  __syncthreads();
+  tc::after_sync();
+  const uint32_t total = ends[p.experts - 1];
+  const uint32_t row_bytes = (min(kTileM, longest) + 31) / 32 * 4096, stage_bytes = kTileBytesB8 + row_bytes;
+  const uint32_t tiles = (tc::smem_addr(dynamic) + 1023) & ~1023u;
+  // The products read 128 rows whatever was loaded: past the last stage's there
+  // is room for them.  What they make of the others is not looked at.
+  const int stages = min(kMaxStages, static_cast<int>((kTcSmem - 1024 - (kTileM * kTile8K - row_bytes)) / stage_bytes));
+  const uint32_t sums = columns;
+  const int blocks = (p.K + kTile8K - 1) / kTile8K;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0) {
+      if (lane == 0) {
+        int e = 0, s = 0;
+        uint32_t phase = 0, issued = 0;
+        bool ok = true;
+        for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
+          const Tile8 x = tile8_at(p, ends, t, e);
+          const int boxes = (x.n + 31) / 32;
+          for (int k = 0; k < blocks; ++k) {
+            if (!tc::bar_wait(empty + 8 * s, phase ^ 1, &gone)) {
+              ok = false;
+              break;
+            }
+            const uint32_t bar = full + 8 * s, to = tiles + s * stage_bytes;
+            tc::bar_expect(bar, kTileBytesB8 + boxes * 4096);
+            tc::load3d(to, p.weight + x.d, bar, k * kTile8K, x.m0, x.i);
+            for (int j = 0; j < boxes; ++j) tc::load2d(to + kTileBytesB8 + j * 4096, p.rows + x.d, bar, k * kTile8K, x.first + j * 32);
+            ++issued;
+            if (++s == stages) s = 0, phase ^= 1;
+          }
+        }
+        for (int j = 0; j < stages && issued > static_cast<uint32_t>(j); ++j) {  // as in product_kernel
+          if (s-- == 0) s = stages - 1, phase ^= 1;
+          if (ok) ok = tc::bar_wait(empty + 8 * s, phase, &gone);
+          else tc::bar_wait(full + 8 * s, phase, &gone);
+        }
+      }
+    } else if (warp == 1) {
+      int e = 0, s = 0, half = 0;
+      uint32_t phase = 0, half_phase = 0;
+      bool ok = true;
+      for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
+        const Tile8 x = tile8_at(p, ends, t, e);
+        const uint32_t how = tc::instruction(0, false, false, (min(kTile8N, p.M - x.m0) + 15) / 16 * 16, kTileM);
+        for (int k = 0; k < blocks; ++k) {
+          ok = tc::warp_wait(sums_empty + 8 * half, half_phase ^ 1, &gone) && tc::warp_wait(full + 8 * s, phase, &gone);
+          if (!ok) break;
+          tc::after_sync();
+          if (lane == 0) {
+            const uint32_t b = tiles + s * stage_bytes, a = b + kTileBytesB8;
+            const int parts = min(4, (p.K - k * kTile8K + 31) / 32);
+            for (int j = 0; j < parts; ++j) tc::mma8(sums + half * kTile8N, tc::desc_k(a + j * 32), tc::desc_k(b + j * 32), how, j > 0);
+            tc::commit(empty + 8 * s);
+            tc::commit(sums_full + 8 * half);
+          }
+          __syncwarp();
+          if (++s == stages) s = 0, phase ^= 1;
+          if (half ^= 1; half == 0) half_phase ^= 1;
+        }
+      }
+      if (__any_sync(0xffffffffu, gone)) {
+        if (lane == 0) tc::commit(done);
+        for (uint32_t it = 0; it < tc::kSoon && !tc::bar_test(done, 0); ++it) __nanosleep(64);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    int e = 0, half = 0;
+    uint32_t half_phase = 0;
+    bool ok = true;
+    const int part = warp & 3, side = (warp - 4) / 4;  // lanes of tensor memory; which 128 of the 256 outputs
+    const int64_t down = (p.M + VC_FP8_BLOCK - 1) / VC_FP8_BLOCK;
+    for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      const Tile8 x = tile8_at(p, ends, t, e);
+      const int m = x.m0 + side * 128, row = part * 32 + lane;
+      const bool busy = m < p.M && part * 32 < x.n, there = row < x.n;
+      const float* rs = p.row_scale[x.d] + (static_cast<int64_t>(x.first) + (there ? row : 0)) * blocks;
+      const float* ws = p.weight_scale[x.d] + (x.i * down + (m < p.M ? m / VC_FP8_BLOCK : 0)) * blocks;
+      float acc[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+      float by = blocks > 0 ? __ldg(rs) * __ldg(ws) : 0.f;
+      for (int k = 0; k < blocks; ++k) {
+        const float next = k + 1 < blocks ? __ldg(rs + k + 1) * __ldg(ws + k + 1) : 0.f;
+        ok = tc::warp_wait(sums_full + 8 * half, half_phase, &gone, tc::kLate);
+        if (!ok) break;
+        if (busy) {
+          tc::after_sync();
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t v[32];
+            tc::load_columns(sums + (part << 21) + half * kTile8N + side * 128 + c, v);
+            tc::loaded(v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(by, __uint_as_float(v[j]), acc[c + j]);
+          }
+          tc::before_sync();
+        }
+        __syncwarp();
+        if (lane == 0) tc::bar_arrive(sums_empty + 8 * half);
+        by = next;
+        if (half ^= 1; half == 0) half_phase ^= 1;
+      }
+      if (!ok || !busy || !there) continue;
+      char* out = static_cast<char*>(p.out[x.d]) + ((static_cast<int64_t>(x.first) + row) * p.M + m) * El<OUT>::kSize;
+      const int left = min(128, p.M - m);
+      if (p.whole) {
+#pragma unroll
+        for (int j = 0; j < 128; j += El<OUT>::kVec)
+          if (j < left) *reinterpret_cast<uint4*>(out + j * El<OUT>::kSize) = El<OUT>::narrow(acc + j);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 128; ++j)
+          if (j < left) El<OUT>::store(out, j, acc[j]);
+      }
+    }
+  }
+  tc::before_sync();
+  __syncthreads();
+  tc::after_sync();
+  if (warp == 1) tc::free_columns(sums, kColumns);
+  if (gone && threadIdx.x == 0) atomicOr(&dev::g_device_error, 4u);
+}
+
 // -- operands off 16-byte boundaries --------------------------------------------
 // Tensor maps want them, so such rows are copied to scratch first, a row each
 // 16 bytes' multiple apart: the rows that the experts have, the weights of
@@ -554,26 +753,31 @@ vc_status_t pad(DeviceState* st, int dev, const Sizes& z, const int32_t* const* 
       p.capacity = static_cast<int32_t>(z.capacity);
       p.nranks = z.nranks;
       p.each = z.each;
-      constexpr auto K = pad_kernel<2>;
-      const int64_t fit = (int64_t(st->nsm) * resident_blocks<K>(dev, kPadThreads, 0) + z.nranks - 1) / z.nranks;
-      const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((o.rows + 7) / 8, fit));
-      rc = launch<K>(dev, Shape{blocks, kPadThreads, 0, 1, static_cast<unsigned>(z.nranks)}, stream, p, kPad, (*step)++,
-                     z.nranks * o.rows * (o.width * o.es + o.pitch));
+      const auto go = [&](auto size) {
+        constexpr auto K = pad_kernel<size()>;
+        const int64_t fit = (int64_t(st->nsm) * resident_blocks<K>(dev, kPadThreads, 0) + z.nranks - 1) / z.nranks;
+        const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((o.rows + 7) / 8, fit));
+        return launch<K>(dev, Shape{blocks, kPadThreads, 0, 1, static_cast<unsigned>(z.nranks)}, stream, p, kPad, (*step)++,
+                         z.nranks * o.rows * (o.width * o.es + o.pitch));
+      };
+      rc = o.es == 2 ? go(std::integral_constant<int, 2>{}) : go(std::integral_constant<int, 1>{});
       for (int r = 0; r < z.nranks; ++r) o.p[r] = p.to + r * o.rows * o.pitch;
     }
   return rc;
 }
 
-CUtensorMapDataType map_type(vc_dtype_t d) { return d == VC_BFLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16; }
+CUtensorMapDataType map_type(vc_dtype_t d) {
+  return d == VC_BFLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : d == VC_FLOAT16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+}
 
 vc_status_t map_rows(CUtensorMap* map, vc_dtype_t dtype, const Operand& o, int r, uint32_t box) {
   const uint64_t dims[2] = {static_cast<uint64_t>(o.width), static_cast<uint64_t>(o.rows)}, strides[1] = {static_cast<uint64_t>(o.pitch)};
-  return tc::tensor_map(map, map_type(dtype), 2, o.p[r], dims, strides, 64, box);
+  return tc::tensor_map(map, map_type(dtype), 2, o.p[r], dims, strides, 128 / o.es, box);
 }
 vc_status_t map_weights(CUtensorMap* map, vc_dtype_t dtype, const Operand& o, int r, uint32_t box) {
   const uint64_t dims[3] = {static_cast<uint64_t>(o.width), static_cast<uint64_t>(o.group), static_cast<uint64_t>(o.rows / o.group)};
   const uint64_t strides[2] = {static_cast<uint64_t>(o.pitch), static_cast<uint64_t>(o.pitch * o.group)};
-  return tc::tensor_map(map, map_type(dtype), 3, o.p[r], dims, strides, 64, box);
+  return tc::tensor_map(map, map_type(dtype), 3, o.p[r], dims, strides, 128 / o.es, box);
 }
 
 // One launch of the tensor-core kernel.  a: weights or the right side of their
@@ -752,6 +956,65 @@ vc_status_t product_grad(const void* const* dout, const void* const* rows, const
   return rc;
 }
 
+vc_status_t product8(const void* const* rows, const float* const* row_scale, const void* const* weight, const float* const* weight_scale,
+                     const int32_t* const* offsets, void* const* out, int nranks, int nexperts, size_t capacity, size_t in,
+                     size_t width, vc_dtype_t out_dtype, cudaStream_t stream) {
+  Sizes z;
+  vc_status_t rc = check_sizes(&z, nranks, nexperts, capacity, in, width);
+  if (rc == VC_SUCCESS) rc = check_float(out_dtype);
+  if (rc != VC_SUCCESS) return rc;
+  const int es = dtype_size(out_dtype);
+  const int64_t blocks = (z.in + VC_FP8_BLOCK - 1) / VC_FP8_BLOCK, down = (z.out + VC_FP8_BLOCK - 1) / VC_FP8_BLOCK;
+  const auto floats = [](const float* const* a) { return reinterpret_cast<const void* const*>(a); };
+  Buffers b;
+  rc = b.add(rows, nranks, z.capacity * z.in, 1, false, "rows");
+  if (rc == VC_SUCCESS) rc = b.add(floats(row_scale), nranks, z.capacity * blocks * 4, 4, false, "row_scale");
+  if (rc == VC_SUCCESS) rc = b.add(weight, nranks, z.each * z.in * z.out, 1, false, "weight");
+  if (rc == VC_SUCCESS) rc = b.add(floats(weight_scale), nranks, z.each * down * blocks * 4, 4, false, "weight_scale");
+  if (rc == VC_SUCCESS) rc = b.add(untyped(offsets), nranks, (z.each + 1) * 4, 4, false, "offsets");
+  if (rc == VC_SUCCESS) rc = b.add(out, nranks, z.capacity * z.out * es, es, true, "out");
+  if (rc == VC_SUCCESS) rc = b.disjoint();
+  if (rc != VC_SUCCESS || z.capacity == 0 || z.out == 0) return rc;
+  DeviceState* st = nullptr;
+  int dev = 0;
+  rc = device_state(&st, &dev);
+  if (rc != VC_SUCCESS) return rc;
+  Operand x(rows, z, z.capacity, z.in, 0, 1), w(weight, z, z.each * z.out, z.in, z.out, 1);
+  Scratch scratch(st, dev, stream);
+  Operand* const ops[] = {&x, &w};
+  int step = 0;
+  rc = pad(st, dev, z, offsets, ops, 2, &scratch, &step, stream);
+  if (rc != VC_SUCCESS) return rc;
+  const int64_t bytes = z.nranks * z.capacity * (z.in + 4 * blocks + z.out * es) + z.nexperts * (z.in * z.out + 4 * down * blocks);
+  const auto go = [&](auto code, auto ranks) {
+    constexpr int R = ranks();
+    Product8Params<R> p;
+    p.whole = z.out * es % 16 == 0;
+    for (int r = 0; r < nranks; ++r) {
+      if (z.in != 0) {
+        vc_status_t rc = map_rows(&p.rows[r], VC_INT8, x, r, 32);
+        if (rc == VC_SUCCESS) rc = map_weights(&p.weight[r], VC_INT8, w, r, kTile8N);
+        if (rc != VC_SUCCESS) return rc;
+      }
+      p.row_scale[r] = row_scale[r];
+      p.weight_scale[r] = weight_scale[r];
+      p.out[r] = out[r];
+      p.offsets[r] = offsets[r];
+      p.whole = p.whole && reinterpret_cast<uintptr_t>(out[r]) % 16 == 0;
+    }
+    p.capacity = static_cast<int32_t>(z.capacity);
+    p.M = static_cast<int>(z.out);
+    p.K = static_cast<int>(z.in);
+    p.experts = z.nexperts;
+    p.each = z.each;
+    const int64_t tiles = row_tiles(z, kTileM) * ((z.out + kTile8N - 1) / kTile8N);
+    return launch<product8_kernel<code(), R>>(dev, Shape{grid_of(st, tiles), kTc8Threads, kTcSmem}, stream, p, kExpertProduct8, step, bytes);
+  };
+  return for_dtype(out_dtype, [&](auto code) {
+    return nranks <= 8 ? go(code, std::integral_constant<int, 8>{}) : go(code, std::integral_constant<int, VC_MAX_RANKS>{});
+  });
+}
+
 }  // namespace
 
 cudaError_t take_product_errors(cudaStream_t stream, uint32_t* flags) {
@@ -812,5 +1075,16 @@ VC_EXPORT vc_status_t vc_expert_product_backward(const void* const* dout, const 
   return entry([&] {
     return layer::product_grad(dout, rows, weight, offsets, drows, dweight, nranks, nexperts, capacity, in_width,
                                out_width, transposed, dtype, dweight_dtype, reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+VC_EXPORT vc_status_t vc_expert_product_fp8(const void* const* rows, const float* const* row_scale,
+                                            const void* const* weight, const float* const* weight_scale,
+                                            const int32_t* const* offsets, void* const* out, int nranks, int nexperts,
+                                            size_t capacity, size_t in_width, size_t out_width, vc_dtype_t out_dtype,
+                                            vc_stream_t stream) {
+  return entry([&] {
+    return layer::product8(rows, row_scale, weight, weight_scale, offsets, out, nranks, nexperts, capacity, in_width,
+                           out_width, out_dtype, reinterpret_cast<cudaStream_t>(stream));
   });
 }

@@ -319,7 +319,8 @@ __device__ __noinline__ uint4 load_elements(const char* at, int64_t n) {
     if (i < n) {
       uint32_t e;
       if constexpr (ES == 4) e = *reinterpret_cast<const uint32_t*>(at + i * 4);
-      else e = *reinterpret_cast<const uint16_t*>(at + i * 2);
+      else if constexpr (ES == 2) e = *reinterpret_cast<const uint16_t*>(at + i * 2);
+      else e = static_cast<uint8_t>(at[i]);
       out[i * ES / 4] |= e << (i * ES % 4 * 8);
     }
   return make_uint4(out[0], out[1], out[2], out[3]);

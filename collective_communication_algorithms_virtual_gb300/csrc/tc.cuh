@@ -98,6 +98,11 @@ __device__ __forceinline__ void mma16(uint32_t d, uint64_t a, uint64_t b, uint32
                "l"(a), "l"(b), "r"(how), "r"(static_cast<uint32_t>(add))
                : "memory");
 }
+__device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t how, bool add) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+               "l"(a), "l"(b), "r"(how), "r"(static_cast<uint32_t>(add))
+               : "memory");
+}
 // The barrier is arrived at once every product issued so far has been done.
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");

@@ -830,6 +830,72 @@ vc_status_t vc_expert_product_backward(const void* const* dout, const void* cons
                                        int transposed, vc_dtype_t dtype, vc_dtype_t dweight_dtype,
                                        vc_stream_t stream);
 
+/* 8-bit floating point below: e4m3 (4 bits of exponent, 3 of mantissa, largest
+ * 448, no infinity), a scale in fp32 for each block of this many elements. */
+#define VC_FP8_BLOCK 128
+
+/*
+ * Rounds matrices to 8 bits, a scale for each VC_FP8_BLOCK of a row
+ * (block_rows 1: rows of tokens) or VC_FP8_BLOCK rows by VC_FP8_BLOCK
+ * (block_rows VC_FP8_BLOCK: weights); blocks at the ends are what is left.
+ * With a block's largest magnitude `most`:
+ *   scale = max(most / 448, 2^-126)  (0 for a block of zeros)
+ *   out   = x * min(448 / most, 2^126)
+ * the quotients and the product rounded to fp32, out then to the nearest e4m3
+ * number, ties to even.  A block with a NaN has scale NaN and zeros, one with an
+ * infinity and no NaN scale infinity and zeros.
+ *   x[r], out[r]: matrices*rows*width (out: bytes);
+ *   scale[r]: matrices * ceil(rows / block_rows) * ceil(width / VC_FP8_BLOCK).
+ *   count: NULL, or for each rank the address of one number on the device: of
+ *   its rows only so many, from the first, are done (the last of
+ *   vc_dispatch_plan's offsets: the rows that were received), and the others
+ *   keep their out and scale.  It wants one matrix and block_rows 1.
+ *   A width above VC_EXPERT_MAX_WIDTH is VC_ERR_UNSUPPORTED.
+ * Rows and their scales are dispatched like other rows: vc_dispatch with
+ * VC_INT8 for the one, VC_FLOAT32 and hidden = ceil(width / 128) for the other.
+ */
+vc_status_t vc_quantize_fp8(const void* const* x, void* const* out, float* const* scale, const int32_t* const* count,
+                            int nranks, size_t matrices, size_t rows, size_t width, int block_rows, vc_dtype_t dtype,
+                            vc_stream_t stream);
+
+/*
+ * vc_expert_product with 8-bit rows and weights (out_width by in_width, as with
+ * `transposed`), scaled by blocks as vc_quantize_fp8 writes them: for o <
+ * out_width and row p of expert i
+ *   out[d][p][o] = sum over blocks b of in_width, in order, of
+ *     row_scale[d][p][b] * weight_scale[d][i][o / 128][b]
+ *     * (sum over the block of rows[d][p] * weight[d][i][o])
+ * in fp32, the inner sums first, rounded once to out_dtype (any float).
+ *   row_scale[d]: capacity * ceil(in_width / 128); weight_scale[d]:
+ *   (nexperts/nranks) * ceil(out_width / 128) * ceil(in_width / 128).
+ * Everything else as vc_expert_product.  There is no gradient: it is a form for
+ * serving.
+ */
+vc_status_t vc_expert_product_fp8(const void* const* rows, const float* const* row_scale, const void* const* weight,
+                                  const float* const* weight_scale, const int32_t* const* offsets, void* const* out,
+                                  int nranks, int nexperts, size_t capacity, size_t in_width, size_t out_width,
+                                  vc_dtype_t out_dtype, vc_stream_t stream);
+
+/*
+ * The gradients' norm, and their clipping by it.  Rank r holds `ntensors`
+ * tensors, any sizes; tensor i of rank r is entry r*ntensors + i of grads, out
+ * and counts (elements), and of type dtypes[i] on every rank.
+ *   norm[r] = sqrt(sum of g^2 over every element of rank r's tensors, or of all
+ *             ranks' with `across`: shards of one model)
+ *   out = g where norm <= max_norm, else g * (max_norm / norm), both factors
+ *         fp32, rounded once to the tensor's type.
+ * Squares and the sums of 64 of them are fp32 (a gradient above 1.8e19 gives an
+ * infinite norm), sums of those 64 bits.  An infinite norm scales by 0, a NaN one
+ * by NaN.
+ *   out: NULL for the norm alone (max_norm is not looked at).  out[j] ==
+ *   grads[j] is allowed; a tensor is then not touched where norm <= max_norm.
+ *   max_norm: >= 0, infinity included, rounded to fp32; else
+ *   VC_ERR_INVALID_ARG.  At most 2^20 tensors.
+ */
+vc_status_t vc_clip_grad_norm(const void* const* grads, void* const* out, const size_t* counts,
+                              const vc_dtype_t* dtypes, int nranks, size_t ntensors, float* const* norm,
+                              double max_norm, int across, vc_stream_t stream);
+
 /* Library version, major*10000 + minor*100 + patch. */
 int vc_version(void);
 
