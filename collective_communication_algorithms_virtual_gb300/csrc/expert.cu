@@ -145,17 +145,22 @@ __global__ void __launch_bounds__(kSimpleThreads, 2) product_simple_kernel(const
 // ---------------------------------------------------------------------------
 // products on the tensor cores
 // ---------------------------------------------------------------------------
-// A tile is 128 of m (the weights' side, or the contiguous side of a weights'
-// gradient) by up to 256 of n (rows of one expert, or the other side), fp32
-// sums in tensor memory.  The rows stand on the n side because n may be any
-// multiple of 16: an expert's last rows cost what they are, where the m side
-// would fill up to 128.  64 of k a step.
+// A pair of blocks works a tile of 256 of m (the weights' side, or the
+// contiguous side of a weights' gradient) by up to 256 of n (rows of one expert,
+// or the other side), each block with 128 of m and the fp32 sums of those in its
+// tensor memory.  The rows stand on the n side because n may be any multiple of
+// 16: an expert's last rows cost what they are, where the m side would fill up.
+// Each block loads its half of m and half of n, 64 of k a step; a pair's
+// products read both halves of n, so that each block's shared memory takes two
+// thirds of what a block by itself would load and read (prefill of 32768 rows,
+// 4096 by 2048: 587 us with single blocks of 128 by 256).
 //   warp 0: one thread loads each step's tiles by tensor maps
-//   warp 1: one thread issues the products
-//   warps 2 to 5: tensor memory to global memory, while the next tile's
+//   warp 1: one thread of the pair's first block issues the products
+//   warp 2: rows behind an expert's last, in the last step of a weights' gradient
+//   warps 4 to 7: tensor memory to global memory, while the next tile's
 //     products go to the other half of tensor memory
 constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
-constexpr int kTcThreads = 192, kMaxStages = 12;
+constexpr int kTcThreads = 256, kMaxStages = 12;
 constexpr int kTileBytesA = kTileM * kTileK * 2;
 constexpr uint32_t kColumns = 512;  // two accumulators
 constexpr size_t kTcSmem = 220 << 10;
@@ -177,13 +182,14 @@ struct Tile {
   int d, i;        // rank, its expert
   int32_t first;   // its first row (of weights' gradients: of k)
   int64_t row;     // of out
-  int n0, n, m0;
+  int n0, n, m0;   // m0: of this block's half
+  int half;        // of n, padded: what each block loads
   int k;           // elements
 };
 template <bool WEIGHT, class P>
-__device__ __forceinline__ Tile tile_at(const P& p, const uint32_t* ends, uint32_t t, int& e) {
+__device__ __forceinline__ Tile tile_at(const P& p, const uint32_t* ends, uint32_t t, int rank, int& e) {
   Tile x;
-  const uint32_t across = (p.M + kTileM - 1) / kTileM;
+  const uint32_t across = (p.M + 2 * kTileM - 1) / (2 * kTileM);
   uint32_t at = t;
   if constexpr (WEIGHT) {
     const uint32_t every = across * tc::pieces(p.N, kTileN);
@@ -199,7 +205,8 @@ __device__ __forceinline__ Tile tile_at(const P& p, const uint32_t* ends, uint32
   const int count = WEIGHT ? p.N : r.count, piece = tc::piece_of(count, kTileN, 16);
   x.n0 = static_cast<int>(at / across) * piece;
   x.n = min(piece, count - x.n0);
-  x.m0 = static_cast<int>(at % across) * kTileM;
+  x.m0 = static_cast<int>(at % across) * (2 * kTileM) + rank * kTileM;
+  x.half = (x.n + 15) / 16 * 8;
   x.first = WEIGHT ? r.first : r.first + x.n0;
   x.row = WEIGHT ? static_cast<int64_t>(x.i) * p.N + x.n0 : x.first;
   x.k = WEIGHT ? r.count : p.K;
@@ -240,45 +247,48 @@ template <bool AMN, bool WEIGHT, int R>
 __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_constant__ ProductParams<R> p) {
   extern __shared__ unsigned char dynamic[];
   __shared__ uint32_t ends[WEIGHT ? 1 : kMaxExperts];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
+  __shared__ __align__(8) uint64_t bars[3 * kMaxStages + 5];
   __shared__ uint32_t columns, gone;
   __shared__ int longest;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kMaxStages, sums_full = empty + 8 * kMaxStages,
-                 sums_empty = sums_full + 16, done = sums_empty + 16;
+  const int rank = static_cast<int>(tc::rank_in_cluster());
+  const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kMaxStages, tail = empty + 8 * kMaxStages,
+                 sums_full = tail + 8 * kMaxStages, sums_empty = sums_full + 16, done = sums_empty + 16;
+  const uint32_t full0 = tc::bar_of(full, 0), sums_empty0 = tc::bar_of(sums_empty, 0);  // the first block's
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kMaxStages; ++s) tc::bar_init(full + 8 * s, 1), tc::bar_init(empty + 8 * s, 1);
-    for (int s = 0; s < 2; ++s) tc::bar_init(sums_full + 8 * s, 1), tc::bar_init(sums_empty + 8 * s, 4);
+    for (int s = 0; s < kMaxStages; ++s) tc::bar_init(full + 8 * s, 2), tc::bar_init(empty + 8 * s, 1), tc::bar_init(tail + 8 * s, 1);
+    for (int s = 0; s < 2; ++s) tc::bar_init(sums_full + 8 * s, 1), tc::bar_init(sums_empty + 8 * s, 8);
     tc::bar_init(done, 1);
     gone = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tc::take_columns(tc::smem_addr(&columns), kColumns);
-  tc::before_sync();
+  if (warp == 1) tc::take_columns<true>(tc::smem_addr(&columns), kColumns);
   stream_order();
-  const uint32_t across = (p.M + kTileM - 1) / kTileM;
+  const uint32_t across = (p.M + 2 * kTileM - 1) / (2 * kTileM);
   if constexpr (!WEIGHT) {
     if (warp == 0) tc::list_tiles(p.offsets, p.experts, p.each, p.capacity, kTileN, across, ends, &longest);
   }
-  __syncthreads();
+  tc::before_sync();
+  __syncwarp();
+  tc::cluster_sync();  // both blocks' barriers are there, and this block's list
   tc::after_sync();
   const uint32_t total = WEIGHT ? p.experts * across * tc::pieces(p.N, kTileN) : ends[p.experts - 1];
   // Stages as small as the longest piece of n allows: few rows, many stages.
   // Above kTileN rows an expert with fewer may have the longer pieces.
   const int widest = WEIGHT ? tc::piece_of(p.N, kTileN, 16) : min(kTileN, (longest + 15) / 16 * 16);
-  const uint32_t stage_bytes = kTileBytesA + (WEIGHT ? (widest + 63) / 64 * 8192 : (widest + 31) / 32 * 4096);
+  const uint32_t stage_bytes = kTileBytesA + (WEIGHT ? (widest / 2 + 63) / 64 * 8192 : (widest / 2 + 31) / 32 * 4096);
   const uint32_t tiles = (tc::smem_addr(dynamic) + 1023) & ~1023u;
   const int stages = min(kMaxStages, static_cast<int>((kTcSmem - 1024) / stage_bytes));
-  const uint32_t sums = columns;
+  const uint32_t sums = columns, pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
   if (warp == 0) {
     if (lane == 0) {
       int e = 0, s = 0;
-      uint32_t phase = 0, issued = 0;
+      uint32_t phase = 0, issued = 0, tails = 0, tail_phases = 0;
       bool ok = true;
-      for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
-        const Tile x = tile_at<WEIGHT>(p, ends, t, e);
-        const int boxes = WEIGHT ? (x.n + 63) / 64 : (x.n + 31) / 32;
+      for (uint32_t t = pair; ok && t < total; t += pairs) {
+        const Tile x = tile_at<WEIGHT>(p, ends, t, rank, e);
+        const int boxes = WEIGHT ? (x.half + 63) / 64 : (x.half + 31) / 32;
         const uint32_t bytes = kTileBytesA + boxes * (WEIGHT ? 8192 : 4096);
         const CUtensorMap *a = p.a + x.d, *b = p.b + x.d;
         for (int k = 0; k < x.k; k += kTileK) {
@@ -286,82 +296,114 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
             ok = false;
             break;
           }
-          const uint32_t bar = full + 8 * s, to = tiles + s * stage_bytes;
-          tc::bar_expect(bar, bytes);
+          const uint32_t to = tiles + s * stage_bytes, bar = full0 + 8 * s;
           if constexpr (WEIGHT) {
-            tc::load2d(to, a, bar, x.m0, x.first + k);
-            tc::load2d(to + 8192, a, bar, x.m0 + 64, x.first + k);
-            for (int j = 0; j < boxes; ++j) tc::load2d(to + kTileBytesA + j * 8192, b, bar, x.n0 + j * 64, x.first + k);
-          } else {
-            if constexpr (AMN) {
-              tc::load3d(to, a, bar, x.m0, k, x.i);
-              tc::load3d(to + 8192, a, bar, x.m0 + 64, k, x.i);
+            const int n0 = x.n0 + rank * x.half;
+            if (x.k - k < kTileK && (x.k - k) % 16 != 0) {  // warp 2 has a word to say first
+              const uint32_t here = tail + 8 * s;
+              tails |= 1u << s;
+              tail_phases ^= 1u << s;
+              tc::bar_expect(here, bytes);
+              tc::load2d(to, a, here, x.m0, x.first + k);
+              tc::load2d(to + 8192, a, here, x.m0 + 64, x.first + k);
+              for (int j = 0; j < boxes; ++j) tc::load2d(to + kTileBytesA + j * 8192, b, here, n0 + j * 64, x.first + k);
             } else {
-              tc::load3d(to, a, bar, k, x.m0, x.i);
+              tails &= ~(1u << s);
+              tc::bar_expect_there(bar, bytes);
+              tc::load2d_pair(to, a, bar, x.m0, x.first + k);
+              tc::load2d_pair(to + 8192, a, bar, x.m0 + 64, x.first + k);
+              for (int j = 0; j < boxes; ++j) tc::load2d_pair(to + kTileBytesA + j * 8192, b, bar, n0 + j * 64, x.first + k);
             }
-            for (int j = 0; j < boxes; ++j) tc::load2d(to + kTileBytesA + j * 4096, b, bar, k, x.first + j * 32);
+          } else {
+            tc::bar_expect_there(bar, bytes);
+            if constexpr (AMN) {
+              tc::load3d_pair(to, a, bar, x.m0, k, x.i);
+              tc::load3d_pair(to + 8192, a, bar, x.m0 + 64, k, x.i);
+            } else {
+              tc::load3d_pair(to, a, bar, k, x.m0, x.i);
+            }
+            for (int j = 0; j < boxes; ++j) tc::load2d_pair(to + kTileBytesA + j * 4096, b, bar, k, x.first + rank * x.half + j * 32);
           }
           ++issued;
           if (++s == stages) s = 0, phase ^= 1;
         }
       }
-      // The block ends after its last loads and products, on whatever path.
+      // The pair ends after its last loads and products, on whatever path: the
+      // first block's barriers know of both blocks' loads.
       for (int j = 0; j < stages && issued > static_cast<uint32_t>(j); ++j) {
         if (s-- == 0) s = stages - 1, phase ^= 1;
+        const bool alone = tails >> s & 1;
         if (ok) ok = tc::bar_wait(empty + 8 * s, phase, &gone);
-        else tc::bar_wait(full + 8 * s, phase, &gone);
+        if (!ok && (rank == 0 || alone)) {
+          const uint32_t bar = alone ? tail + 8 * s : full + 8 * s, parity = alone ? ~tail_phases >> s & 1 : phase;
+          for (uint32_t it = 0; it < tc::kSoon && !tc::bar_test(bar, parity); ++it) __nanosleep(64);
+        }
       }
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 && rank == 0) {
     int e = 0, s = 0, half = 0;
     uint32_t phase = 0, half_phase = 0;
     bool ok = true;
-    for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
-      const Tile x = tile_at<WEIGHT>(p, ends, t, e);
+    for (uint32_t t = pair; ok && t < total; t += pairs) {
+      const Tile x = tile_at<WEIGHT>(p, ends, t, rank, e);
       if (!tc::warp_wait(sums_empty + 8 * half, half_phase ^ 1, &gone)) break;
       tc::after_sync();
       const uint32_t to = sums + half * kTileN;
-      const uint32_t how = tc::instruction(p.type, AMN, WEIGHT, (x.n + 15) / 16 * 16, kTileM);
+      const uint32_t how = tc::instruction(p.type, AMN, WEIGHT, 2 * x.half, 2 * kTileM);
       for (int k = 0; k < x.k; k += kTileK) {
         if (!tc::warp_wait(full + 8 * s, phase, &gone)) {
           ok = false;
           break;
         }
         tc::after_sync();
-        const uint32_t a = tiles + s * stage_bytes, b = a + kTileBytesA;
-        const int left = min(kTileK, x.k - k), parts = (left + 15) / 16;
-        if constexpr (WEIGHT) {
-          if (left % 16 != 0) {  // the rows behind the expert's last are not its own: 0 instead
-            const int n = (parts * 16 - left) * 8, boxes = 2 + (x.n + 63) / 64;
-            for (int j = lane; j < n * boxes; j += 32)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a + j / n * 8192 + left * 128 + j % n * 16), "r"(0) : "memory");
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-          }
-        }
         if (lane == 0) {
+          const uint32_t a = tiles + s * stage_bytes, b = a + kTileBytesA;
+          const int parts = (min(kTileK, x.k - k) + 15) / 16;
           for (int j = 0; j < parts; ++j)
-            tc::mma16(to, AMN ? tc::desc_mn(a + j * 2048, 8192) : tc::desc_k(a + j * 32),
-                      WEIGHT ? tc::desc_mn(b + j * 2048, 8192) : tc::desc_k(b + j * 32), how, k + j > 0);
-          tc::commit(empty + 8 * s);
+            tc::mma16_pair(to, AMN ? tc::desc_mn(a + j * 2048, 8192) : tc::desc_k(a + j * 32),
+                           WEIGHT ? tc::desc_mn(b + j * 2048, 8192) : tc::desc_k(b + j * 32), how, k + j > 0);
+          tc::commit_pair(empty + 8 * s);
         }
         __syncwarp();
         if (++s == stages) s = 0, phase ^= 1;
       }
-      if (ok && lane == 0) tc::commit(sums_full + 8 * half);
+      if (ok && lane == 0) tc::commit_pair(sums_full + 8 * half);
       __syncwarp();
       if (half ^= 1; half == 0) half_phase ^= 1;
     }
     if (__any_sync(0xffffffffu, gone)) {  // products in flight end before tensor memory is freed
-      if (lane == 0) tc::commit(done);
+      if (lane == 0) tc::commit_pair(done);
       for (uint32_t it = 0; it < tc::kSoon && !tc::bar_test(done, 0); ++it) __nanosleep(64);
     }
-  } else {
+  } else if (WEIGHT && warp == 2) {
+    // The last step's rows behind the expert's last, up to 16, are not its own:
+    // 0 instead, on both sides (either may be NaN).
+    int e = 0;
+    uint32_t step = 0, phases = 0;  // of the stages; of each stage's barrier
+    for (uint32_t t = pair; t < total; t += pairs) {
+      const Tile x = tile_at<WEIGHT>(p, ends, t, rank, e);
+      const uint32_t steps = (static_cast<uint32_t>(x.k) + kTileK - 1) / kTileK;
+      const int left = x.k % kTileK;
+      step = (step + steps % stages) % stages;
+      if (left % 16 == 0) continue;
+      const int s = static_cast<int>(step == 0 ? stages - 1 : step - 1);
+      if (!tc::warp_wait(tail + 8 * s, phases >> s & 1, &gone, tc::kLate)) break;
+      phases ^= 1u << s;
+      const int n = (16 - left % 16) * 8, boxes = 2 + (x.half + 63) / 64;
+      for (int j = lane; j < n * boxes; j += 32)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tiles + s * stage_bytes + j / n * 8192 + left * 128 + j % n * 16),
+                     "r"(0)
+                     : "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive_there(full0 + 8 * s);
+    }
+  } else if (warp >= 4) {
     int e = 0, half = 0;
     uint32_t half_phase = 0;
     const int part = warp & 3;  // the lanes of tensor memory that this warp reaches
-    for (uint32_t t = blockIdx.x; t < total; t += gridDim.x) {
-      const Tile x = tile_at<WEIGHT>(p, ends, t, e);
+    for (uint32_t t = pair; t < total; t += pairs) {
+      const Tile x = tile_at<WEIGHT>(p, ends, t, rank, e);
       if (!tc::warp_wait(sums_full + 8 * half, half_phase, &gone, tc::kLate)) break;
       tc::after_sync();
       const int es = p.out_dtype == VC_FLOAT32 ? 4 : 2, m = x.m0 + part * 32;
@@ -380,7 +422,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
         if (c + 32 >= x.n) {
           tc::before_sync();
           __syncwarp();
-          if (lane == 0) tc::bar_arrive(sums_empty + 8 * half);
+          if (lane == 0) tc::bar_arrive_there(sums_empty0 + 8 * half);
         }
         const int columns = min(32, x.n - c);
         if (WEIGHT && p.out_dtype == VC_FLOAT32) store_columns<VC_FLOAT32, false>(v, out, pitch, columns, there);
@@ -394,9 +436,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
     }
   }
   tc::before_sync();
-  __syncthreads();
+  __syncwarp();
+  tc::cluster_sync();  // neither block ends while the other may reach it
   tc::after_sync();
-  if (warp == 1) tc::free_columns(sums, kColumns);
+  if (warp == 1) tc::free_columns<true>(sums, kColumns);
   if (gone && threadIdx.x == 0) atomicOr(&dev::g_device_error, 4u);
 }
 
@@ -467,7 +510,7 @@ __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_c
     gone = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tc::take_columns(tc::smem_addr(&columns), kColumns);
+  if (warp == 1) tc::take_columns<false>(tc::smem_addr(&columns), kColumns);
   tc::before_sync();
   stream_order();
   if (warp == 0)
@@ -595,7 +638,7 @@ __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_c
   tc::before_sync();
   __syncthreads();
   tc::after_sync();
-  if (warp == 1) tc::free_columns(sums, kColumns);
+  if (warp == 1) tc::free_columns<false>(sums, kColumns);
   if (gone && threadIdx.x == 0) atomicOr(&dev::g_device_error, 4u);
 }
 
@@ -675,8 +718,10 @@ int64_t row_tiles(const Sizes& z, int most) {
   return z.nranks * (std::min<int64_t>(z.each, z.capacity) + z.capacity / most);
 }
 
-// Blocks of one kernel that the GPU holds, for `tiles` of them at most.
-unsigned grid_of(DeviceState* st, int64_t tiles) { return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(tiles, st->nsm))); }
+// Groups of `blocks` blocks, one on each multiprocessor, for `tiles` of them at most.
+unsigned grid_of(DeviceState* st, int64_t tiles, int blocks) {
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(tiles, st->nsm / blocks)));
+}
 
 // Scratch of one call, from the library's pool.
 class Scratch {
@@ -807,7 +852,7 @@ vc_status_t launch_product(DeviceState* st, int dev, const Sizes& z, const Opera
   p.each = z.each;
   p.type = dtype == VC_BFLOAT16 ? 1 : 0;
   p.out_dtype = out_dtype;
-  return launch<product_kernel<AMN, WEIGHT, R>>(dev, Shape{grid_of(st, tiles), kTcThreads, kTcSmem}, stream, p,
+  return launch<product_kernel<AMN, WEIGHT, R>>(dev, Shape{2 * grid_of(st, tiles, 2), kTcThreads, kTcSmem, 2}, stream, p,
                                                 WEIGHT ? kExpertWeight : kExpertProduct, step, bytes);
 }
 
@@ -817,7 +862,7 @@ vc_status_t rows_product(DeviceState* st, int dev, const Sizes& z, const Operand
                          vc_dtype_t dtype, int step, cudaStream_t stream) {
   const int64_t bytes = (z.nranks * z.capacity * (in + width) + z.nexperts * in * width) * dtype_size(dtype);
   if (dtype != VC_FLOAT32) {
-    const int64_t tiles = row_tiles(z, kTileN) * ((width + kTileM - 1) / kTileM);
+    const int64_t tiles = row_tiles(z, kTileN) * ((width + 2 * kTileM - 1) / (2 * kTileM));
     const auto go = [&](auto mn, auto ranks) {
       return launch_product<mn(), false, ranks()>(st, dev, z, weight, rows, offsets, out, width, 0, in, dtype, dtype, tiles, bytes, step, stream);
     };
@@ -854,7 +899,7 @@ vc_status_t weights_gradient(DeviceState* st, int dev, const Sizes& z, const Ope
                              vc_dtype_t out_dtype, int step, cudaStream_t stream) {
   const int64_t bytes = z.nranks * z.capacity * (N + M) * dtype_size(dtype) + z.nexperts * N * M * dtype_size(out_dtype);
   if (dtype != VC_FLOAT32) {
-    const int64_t tiles = z.nexperts * ((N + kTileN - 1) / kTileN) * ((M + kTileM - 1) / kTileM);
+    const int64_t tiles = z.nexperts * ((N + kTileN - 1) / kTileN) * ((M + 2 * kTileM - 1) / (2 * kTileM));
     const auto go = [&](auto ranks) {
       return launch_product<true, true, ranks()>(st, dev, z, right, left, offsets, dweight, M, N, 0, dtype, out_dtype, tiles, bytes, step, stream);
     };
@@ -1008,7 +1053,7 @@ vc_status_t product8(const void* const* rows, const float* const* row_scale, con
     p.experts = z.nexperts;
     p.each = z.each;
     const int64_t tiles = row_tiles(z, kTileM) * ((z.out + kTile8N - 1) / kTile8N);
-    return launch<product8_kernel<code(), R>>(dev, Shape{grid_of(st, tiles), kTc8Threads, kTcSmem}, stream, p, kExpertProduct8, step, bytes);
+    return launch<product8_kernel<code(), R>>(dev, Shape{grid_of(st, tiles, 1), kTc8Threads, kTcSmem}, stream, p, kExpertProduct8, step, bytes);
   };
   return for_dtype(out_dtype, [&](auto code) {
     return nranks <= 8 ? go(code, std::integral_constant<int, 8>{}) : go(code, std::integral_constant<int, VC_MAX_RANKS>{});
