@@ -165,6 +165,7 @@ constexpr int kTileBytesA = kTileM * kTileK * 2;
 constexpr uint32_t kColumns = 512;  // two accumulators
 constexpr size_t kTcSmem = 220 << 10;
 
+constexpr int kRowBox = 32;  // rows of one load
 template <int R>
 struct ProductParams {
   CUtensorMap a[R], b[R];
@@ -276,20 +277,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
   // Stages as small as the longest piece of n allows: few rows, many stages.
   // Above kTileN rows an expert with fewer may have the longer pieces.
   const int widest = WEIGHT ? tc::piece_of(p.N, kTileN, 16) : min(kTileN, (longest + 15) / 16 * 16);
-  const uint32_t stage_bytes = kTileBytesA + (WEIGHT ? (widest / 2 + 63) / 64 * 8192 : (widest / 2 + 31) / 32 * 4096);
+  const uint32_t stage_bytes = kTileBytesA + (WEIGHT ? (widest / 2 + 63) / 64 * 8192 : (widest / 2 + kRowBox - 1) / kRowBox * 128 * kRowBox);
   const uint32_t tiles = (tc::smem_addr(dynamic) + 1023) & ~1023u;
   const int stages = min(kMaxStages, static_cast<int>((kTcSmem - 1024) / stage_bytes));
   const uint32_t sums = columns, pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (tc::elect()) {
       int e = 0, s = 0;
       uint32_t phase = 0, issued = 0, tails = 0, tail_phases = 0;
       bool ok = true;
       for (uint32_t t = pair; ok && t < total; t += pairs) {
         const Tile x = tile_at<WEIGHT>(p, ends, t, rank, e);
-        const int boxes = WEIGHT ? (x.half + 63) / 64 : (x.half + 31) / 32;
-        const uint32_t bytes = kTileBytesA + boxes * (WEIGHT ? 8192 : 4096);
+        const int boxes = WEIGHT ? (x.half + 63) / 64 : (x.half + kRowBox - 1) / kRowBox;
+        const uint32_t bytes = kTileBytesA + boxes * (WEIGHT ? 8192 : 128 * kRowBox);
         const CUtensorMap *a = p.a + x.d, *b = p.b + x.d;
         for (int k = 0; k < x.k; k += kTileK) {
           if (!tc::bar_wait(empty + 8 * s, phase ^ 1, &gone)) {
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
             } else {
               tc::load3d_pair(to, a, bar, k, x.m0, x.i);
             }
-            for (int j = 0; j < boxes; ++j) tc::load2d_pair(to + kTileBytesA + j * 4096, b, bar, k, x.first + rank * x.half + j * 32);
+            for (int j = 0; j < boxes; ++j) tc::load2d_pair(to + kTileBytesA + j * (128 * kRowBox), b, bar, k, x.first + rank * x.half + j * kRowBox);
           }
           ++issued;
           if (++s == stages) s = 0, phase ^= 1;
@@ -341,39 +342,40 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
       }
     }
   } else if (warp == 1 && rank == 0) {
-    int e = 0, s = 0, half = 0;
-    uint32_t phase = 0, half_phase = 0;
-    bool ok = true;
-    for (uint32_t t = pair; ok && t < total; t += pairs) {
-      const Tile x = tile_at<WEIGHT>(p, ends, t, rank, e);
-      if (!tc::warp_wait(sums_empty + 8 * half, half_phase ^ 1, &gone)) break;
-      tc::after_sync();
-      const uint32_t to = sums + half * kTileN;
-      const uint32_t how = tc::instruction(p.type, AMN, WEIGHT, 2 * x.half, 2 * kTileM);
-      for (int k = 0; k < x.k; k += kTileK) {
-        if (!tc::warp_wait(full + 8 * s, phase, &gone)) {
-          ok = false;
-          break;
-        }
+    if (tc::elect()) {
+      int e = 0, s = 0, half = 0;
+      uint32_t phase = 0, half_phase = 0;
+      bool ok = true;
+      const uint64_t a0 = AMN ? tc::desc_mn(tiles, 8192) : tc::desc_k(tiles);
+      const uint64_t b0 = WEIGHT ? tc::desc_mn(tiles + kTileBytesA, 8192) : tc::desc_k(tiles + kTileBytesA);
+      constexpr uint32_t kNextA = (AMN ? 2048 : 32) / 16, kNextB = (WEIGHT ? 2048 : 32) / 16;  // 16 of k on
+      for (uint32_t t = pair; ok && t < total; t += pairs) {
+        const Tile x = tile_at<WEIGHT>(p, ends, t, rank, e);
+        if (!tc::bar_wait(sums_empty + 8 * half, half_phase ^ 1, &gone)) break;
         tc::after_sync();
-        if (lane == 0) {
-          const uint32_t a = tiles + s * stage_bytes, b = a + kTileBytesA;
-          const int parts = (min(kTileK, x.k - k) + 15) / 16;
-          for (int j = 0; j < parts; ++j)
-            tc::mma16_pair(to, AMN ? tc::desc_mn(a + j * 2048, 8192) : tc::desc_k(a + j * 32),
-                           WEIGHT ? tc::desc_mn(b + j * 2048, 8192) : tc::desc_k(b + j * 32), how, k + j > 0);
+        const uint32_t to = sums + half * kTileN;
+        const uint32_t how = tc::instruction(p.type, AMN, WEIGHT, 2 * x.half, 2 * kTileM);
+        for (int k = 0; k < x.k; k += kTileK) {
+          if (!tc::bar_wait(full + 8 * s, phase, &gone)) {
+            ok = false;
+            break;
+          }
+          tc::after_sync();
+          const uint64_t a = a0 + (s * stage_bytes >> 4), b = b0 + (s * stage_bytes >> 4);
+          const int left = x.k - k;
+#pragma unroll
+          for (int j = 0; j < kTileK / 16; ++j)
+            if (j * 16 < left) tc::mma16_pair(to, a + j * kNextA, b + j * kNextB, how, k + j > 0);
           tc::commit_pair(empty + 8 * s);
+          if (++s == stages) s = 0, phase ^= 1;
         }
-        __syncwarp();
-        if (++s == stages) s = 0, phase ^= 1;
+        if (ok) tc::commit_pair(sums_full + 8 * half);
+        if (half ^= 1; half == 0) half_phase ^= 1;
       }
-      if (ok && lane == 0) tc::commit_pair(sums_full + 8 * half);
-      __syncwarp();
-      if (half ^= 1; half == 0) half_phase ^= 1;
-    }
-    if (__any_sync(0xffffffffu, gone)) {  // products in flight end before tensor memory is freed
-      if (lane == 0) tc::commit_pair(done);
-      for (uint32_t it = 0; it < tc::kSoon && !tc::bar_test(done, 0); ++it) __nanosleep(64);
+      if (gone) {  // products in flight end before tensor memory is freed
+        tc::commit_pair(done);
+        for (uint32_t it = 0; it < tc::kSoon && !tc::bar_test(done, 0); ++it) __nanosleep(64);
+      }
     }
   } else if (WEIGHT && warp == 2) {
     // The last step's rows behind the expert's last, up to 16, are not its own:
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_c
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
-      if (lane == 0) {
+      if (tc::elect()) {
         int e = 0, s = 0;
         uint32_t phase = 0, issued = 0;
         bool ok = true;
@@ -556,31 +558,33 @@ __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_c
         }
       }
     } else if (warp == 1) {
-      int e = 0, s = 0, half = 0;
-      uint32_t phase = 0, half_phase = 0;
-      bool ok = true;
-      for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
-        const Tile8 x = tile8_at(p, ends, t, e);
-        const uint32_t how = tc::instruction(0, false, false, (min(kTile8N, p.M - x.m0) + 15) / 16 * 16, kTileM);
-        for (int k = 0; k < blocks; ++k) {
-          ok = tc::warp_wait(sums_empty + 8 * half, half_phase ^ 1, &gone) && tc::warp_wait(full + 8 * s, phase, &gone);
-          if (!ok) break;
-          tc::after_sync();
-          if (lane == 0) {
-            const uint32_t b = tiles + s * stage_bytes, a = b + kTileBytesB8;
-            const int parts = min(4, (p.K - k * kTile8K + 31) / 32);
-            for (int j = 0; j < parts; ++j) tc::mma8(sums + half * kTile8N, tc::desc_k(a + j * 32), tc::desc_k(b + j * 32), how, j > 0);
+      if (tc::elect()) {
+        int e = 0, s = 0, half = 0;
+        uint32_t phase = 0, half_phase = 0;
+        bool ok = true;
+        const uint64_t b0 = tc::desc_k(tiles), a0 = tc::desc_k(tiles + kTileBytesB8);
+        for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
+          const Tile8 x = tile8_at(p, ends, t, e);
+          const uint32_t how = tc::instruction(0, false, false, (min(kTile8N, p.M - x.m0) + 15) / 16 * 16, kTileM);
+          for (int k = 0; k < blocks; ++k) {
+            ok = tc::bar_wait(sums_empty + 8 * half, half_phase ^ 1, &gone) && tc::bar_wait(full + 8 * s, phase, &gone);
+            if (!ok) break;
+            tc::after_sync();
+            const uint64_t a = a0 + (s * stage_bytes >> 4), b = b0 + (s * stage_bytes >> 4);
+            const int left = p.K - k * kTile8K;
+#pragma unroll
+            for (int j = 0; j < kTile8K / 32; ++j)
+              if (j * 32 < left) tc::mma8(sums + half * kTile8N, a + j * 2, b + j * 2, how, j > 0);
             tc::commit(empty + 8 * s);
             tc::commit(sums_full + 8 * half);
+            if (++s == stages) s = 0, phase ^= 1;
+            if (half ^= 1; half == 0) half_phase ^= 1;
           }
-          __syncwarp();
-          if (++s == stages) s = 0, phase ^= 1;
-          if (half ^= 1; half == 0) half_phase ^= 1;
         }
-      }
-      if (__any_sync(0xffffffffu, gone)) {
-        if (lane == 0) tc::commit(done);
-        for (uint32_t it = 0; it < tc::kSoon && !tc::bar_test(done, 0); ++it) __nanosleep(64);
+        if (gone) {
+          tc::commit(done);
+          for (uint32_t it = 0; it < tc::kSoon && !tc::bar_test(done, 0); ++it) __nanosleep(64);
+        }
       }
     }
   } else {
@@ -837,7 +841,7 @@ vc_status_t launch_product(DeviceState* st, int dev, const Sizes& z, const Opera
     vc_status_t rc = VC_SUCCESS;
     if (a.rows != 0 && a.width != 0 && b.rows != 0 && b.width != 0) {  // else no step loads anything
       rc = WEIGHT ? map_rows(&p.a[r], dtype, a, r, 64) : map_weights(&p.a[r], dtype, a, r, AMN ? 64 : 128);
-      if (rc == VC_SUCCESS) rc = map_rows(&p.b[r], dtype, b, r, WEIGHT ? 64 : 32);
+      if (rc == VC_SUCCESS) rc = map_rows(&p.b[r], dtype, b, r, WEIGHT ? 64 : kRowBox);
     }
     if (rc != VC_SUCCESS) return rc;
     p.out[r] = out[r];
