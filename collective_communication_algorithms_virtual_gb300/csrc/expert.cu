@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kSimpleThreads, 2) product_simple_kernel(const
 constexpr int kTileM = 128, kTileN = 256, kTileK = 64;
 constexpr int kTcThreads = 256, kMaxStages = 12;
 constexpr int kTileBytesA = kTileM * kTileK * 2;
+constexpr int kRoomBytes = 2 * 32 * kTileM * 2;
 constexpr uint32_t kColumns = 512;  // two accumulators
 constexpr size_t kTcSmem = 220 << 10;
 
@@ -174,9 +175,7 @@ struct ProductParams {
   int32_t capacity;
   int M, N, K;  // as SimpleParams
   int experts, each;
-  uint32_t type;  // of the operands (tc::instruction)
-  int out_dtype;
-  bool pairs;     // out's rows start on 4-byte boundaries
+  bool whole;     // out's rows are whole 16 bytes on 16-byte boundaries, of 16-bit elements
 };
 
 struct Tile {
@@ -215,36 +214,56 @@ __device__ __forceinline__ Tile tile_at(const P& p, const uint32_t* ends, uint32
 }
 
 // 32 accumulated columns of a warp (lane: m) to `columns` rows of out, lane 0's
-// first element at `at`.  PAIRS: neighbouring lanes trade halves, so that each
-// store is two elements of one row.
-template <int OUT, bool PAIRS>
+// first element at `at`.
+template <int OUT>
 __device__ __forceinline__ void store_columns(const uint32_t (&v)[32], char* at, int64_t pitch, int columns, bool there) {
-  const int lane = threadIdx.x & 31;
-  if constexpr (PAIRS) {
-    const bool odd = lane & 1;
-    char* to = at + (lane & ~1) * 2 + (odd ? pitch : 0);
+  char* to = at + (threadIdx.x & 31) * El<OUT>::kSize;
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      if (j >= columns) break;
-      const float mine = __uint_as_float(odd ? v[j + 1] : v[j]);
-      const float other = __uint_as_float(__shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1));
-      if (there && j + odd < columns)
-        *reinterpret_cast<uint32_t*>(to) = dev::pack2<OUT == VC_FLOAT16>(odd ? other : mine, odd ? mine : other);
-      to += 2 * pitch;
-    }
-  } else {
-    char* to = at + lane * El<OUT>::kSize;
+  for (int j = 0; j < 32; ++j) {
+    if (j >= columns) break;
+    if (there) El<OUT>::store(to, 0, __uint_as_float(v[j]));
+    to += pitch;
+  }
+}
+// The same of four warps' 128 m in 16-byte stores of out's rows, through
+// `room` (16 pairs of rows by 128 m; callers alternate two).  A warp by itself
+// would write 64 bytes of a row at a time, two bytes a lane: the weights'
+// gradients of 32 experts with 512 rows each, 2048 by 4096, 8 steps a tile, took
+// 352 us that way.
+template <bool F16>
+__device__ __forceinline__ void store_rows(const uint32_t (&v)[32], uint32_t room, char* at, int64_t pitch, int columns, int ms) {
+  const int thread = threadIdx.x & 127;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      if (j >= columns) break;
-      if (there) El<OUT>::store(to, 0, __uint_as_float(v[j]));
-      to += pitch;
+  for (int j = 0; j < 32; j += 2)
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(room + j * 256 + thread * 4), "r"(dev::pack2<F16>(__uint_as_float(v[j]), __uint_as_float(v[j + 1])))
+                 : "memory");
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+  const int m = thread % 16 * 8;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = (thread / 16 + i * 8) * 2;
+    uint32_t x[8];
+#pragma unroll
+    for (int h = 0; h < 8; h += 4)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(x[h]), "=r"(x[h + 1]), "=r"(x[h + 2]), "=r"(x[h + 3])
+                   : "r"(room + j * 256 + (m + h) * 4)
+                   : "memory");
+    if (m < ms) {
+      char* to = at + j * pitch + m * 2;
+      if (j < columns)
+        *reinterpret_cast<uint4*>(to) = make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
+                                                   __byte_perm(x[4], x[5], 0x5410), __byte_perm(x[6], x[7], 0x5410));
+      if (j + 1 < columns)
+        *reinterpret_cast<uint4*>(to + pitch) = make_uint4(__byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632),
+                                                           __byte_perm(x[4], x[5], 0x7632), __byte_perm(x[6], x[7], 0x7632));
     }
   }
 }
 
-// A: M runs along the rows of a's tiles (weights in by out; weights' gradients).
-template <bool AMN, bool WEIGHT, int R>
+// AMN: M runs along the rows of a's tiles (weights in by out; weights'
+// gradients).  OUT: out's type, of the operands or fp32.
+template <int DT, int OUT, bool AMN, bool WEIGHT, int R>
 __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_constant__ ProductParams<R> p) {
   extern __shared__ unsigned char dynamic[];
   __shared__ uint32_t ends[WEIGHT ? 1 : kMaxExperts];
@@ -278,8 +297,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
   // Above kTileN rows an expert with fewer may have the longer pieces.
   const int widest = WEIGHT ? tc::piece_of(p.N, kTileN, 16) : min(kTileN, (longest + 15) / 16 * 16);
   const uint32_t stage_bytes = kTileBytesA + (WEIGHT ? (widest / 2 + 63) / 64 * 8192 : (widest / 2 + kRowBox - 1) / kRowBox * 128 * kRowBox);
-  const uint32_t tiles = (tc::smem_addr(dynamic) + 1023) & ~1023u;
-  const int stages = min(kMaxStages, static_cast<int>((kTcSmem - 1024) / stage_bytes));
+  const uint32_t room = (tc::smem_addr(dynamic) + 1023) & ~1023u, tiles = room + kRoomBytes;  // of the stores; stages
+  const int stages = min(kMaxStages, static_cast<int>((kTcSmem - 1024 - kRoomBytes) / stage_bytes));
   const uint32_t sums = columns, pair = blockIdx.x / 2, pairs = gridDim.x / 2;
 
   if (warp == 0) {
@@ -354,7 +373,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
         if (!tc::bar_wait(sums_empty + 8 * half, half_phase ^ 1, &gone)) break;
         tc::after_sync();
         const uint32_t to = sums + half * kTileN;
-        const uint32_t how = tc::instruction(p.type, AMN, WEIGHT, 2 * x.half, 2 * kTileM);
+        const uint32_t how = tc::instruction(DT == VC_BFLOAT16, AMN, WEIGHT, 2 * x.half, 2 * kTileM);
         for (int k = 0; k < x.k; k += kTileK) {
           if (!tc::bar_wait(full + 8 * s, phase, &gone)) {
             ok = false;
@@ -401,38 +420,50 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
       if (lane == 0) tc::bar_arrive_there(full0 + 8 * s);
     }
   } else if (warp >= 4) {
-    int e = 0, half = 0;
+    int e = 0, half = 0, turn = 0;
     uint32_t half_phase = 0;
     const int part = warp & 3;  // the lanes of tensor memory that this warp reaches
+    constexpr int es = El<OUT>::kSize;
+    const int64_t pitch = static_cast<int64_t>(p.M) * es;
     for (uint32_t t = pair; t < total; t += pairs) {
       const Tile x = tile_at<WEIGHT>(p, ends, t, rank, e);
-      if (!tc::warp_wait(sums_full + 8 * half, half_phase, &gone, tc::kLate)) break;
+      const bool ok = tc::warp_wait(sums_full + 8 * half, half_phase, &gone, tc::kLate);
+      // the four warps meet below, and give up together
+      int all;
+      asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+                   : "=r"(all)
+                   : "r"(static_cast<int>(ok))
+                   : "memory");
+      if (!all) break;
       tc::after_sync();
-      const int es = p.out_dtype == VC_FLOAT32 ? 4 : 2, m = x.m0 + part * 32;
-      const int64_t pitch = static_cast<int64_t>(p.M) * es;
-      char* out = static_cast<char*>(p.out[x.d]) + x.row * pitch + static_cast<int64_t>(m) * es;
-      const bool there = m + lane < p.M;
-      for (int c = 0; c < x.n; c += 32) {
-        uint32_t v[32];
+      char* out = static_cast<char*>(p.out[x.d]) + x.row * pitch + static_cast<int64_t>(x.m0) * es;
+      const uint32_t from = sums + (part << 21) + half * kTileN;
+      const int ms = p.M - x.m0;
+      // Columns 32 at a time, the next ones on their way from tensor memory.
+      const auto take = [&](uint32_t(&now)[32], uint32_t(&next)[32], int c) {
+        const int columns = x.n - c;
         if (x.k > 0) {
-          tc::load_columns(sums + (part << 21) + half * kTileN + c, v);
-          tc::loaded(v);
+          tc::loaded(now);
+          if (columns > 32) tc::load_columns(from + c + 32, next);
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0;
+          for (int j = 0; j < 32; ++j) now[j] = 0;
         }
-        if (c + 32 >= x.n) {
+        if (columns <= 32) {
           tc::before_sync();
           __syncwarp();
           if (lane == 0) tc::bar_arrive_there(sums_empty0 + 8 * half);
         }
-        const int columns = min(32, x.n - c);
-        if (WEIGHT && p.out_dtype == VC_FLOAT32) store_columns<VC_FLOAT32, false>(v, out, pitch, columns, there);
-        else if (p.out_dtype == VC_BFLOAT16)
-          p.pairs ? store_columns<VC_BFLOAT16, true>(v, out, pitch, columns, there) : store_columns<VC_BFLOAT16, false>(v, out, pitch, columns, there);
+        if (OUT != VC_FLOAT32 && p.whole)
+          store_rows<OUT == VC_FLOAT16>(now, room + (turn ^= 1) * (32 * kTileM * 2), out + c * pitch, pitch, columns, ms);
         else
-          p.pairs ? store_columns<VC_FLOAT16, true>(v, out, pitch, columns, there) : store_columns<VC_FLOAT16, false>(v, out, pitch, columns, there);
-        out += 32 * pitch;
+          store_columns<OUT>(now, out + c * pitch + static_cast<int64_t>(part * 32) * es, pitch, columns, part * 32 + lane < ms);
+      };
+      uint32_t v[32], w[32];
+      if (x.k > 0) tc::load_columns(from, v);
+      for (int c = 0; c < x.n; c += 64) {
+        take(v, w, c);
+        if (c + 32 < x.n) take(w, v, c + 32);
       }
       if (half ^= 1; half == 0) half_phase ^= 1;
     }
@@ -829,14 +860,28 @@ vc_status_t map_weights(CUtensorMap* map, vc_dtype_t dtype, const Operand& o, in
   return tc::tensor_map(map, map_type(dtype), 3, o.p[r], dims, strides, 128 / o.es, box);
 }
 
+// Runs f with the 16-bit type, and how many ranks there is room for, as constants.
+template <class F>
+vc_status_t for_sizes(vc_dtype_t dtype, int nranks, F&& f) {
+  using Few = std::integral_constant<int, 8>;
+  using Many = std::integral_constant<int, VC_MAX_RANKS>;
+  if (dtype == VC_BFLOAT16) {
+    using T = std::integral_constant<int, VC_BFLOAT16>;
+    return nranks <= 8 ? f(T{}, Few{}) : f(T{}, Many{});
+  }
+  using T = std::integral_constant<int, VC_FLOAT16>;
+  return nranks <= 8 ? f(T{}, Few{}) : f(T{}, Many{});
+}
+
 // One launch of the tensor-core kernel.  a: weights or the right side of their
 // gradient; b: rows or the left side.
-template <bool AMN, bool WEIGHT, int R>
+template <int DT, int OUT, bool AMN, bool WEIGHT, int R>
 vc_status_t launch_product(DeviceState* st, int dev, const Sizes& z, const Operand& a, const Operand& b, const int32_t* const* offsets,
-                           void* const* out, int64_t M, int64_t N, int64_t K, vc_dtype_t dtype, vc_dtype_t out_dtype, int64_t tiles,
+                           void* const* out, int64_t M, int64_t N, int64_t K, int64_t tiles,
                            int64_t bytes, int step, cudaStream_t stream) {
+  constexpr vc_dtype_t dtype = static_cast<vc_dtype_t>(DT);
   ProductParams<R> p;
-  p.pairs = M % 2 == 0;
+  p.whole = M % 8 == 0;
   for (int r = 0; r < z.nranks; ++r) {
     vc_status_t rc = VC_SUCCESS;
     if (a.rows != 0 && a.width != 0 && b.rows != 0 && b.width != 0) {  // else no step loads anything
@@ -846,7 +891,7 @@ vc_status_t launch_product(DeviceState* st, int dev, const Sizes& z, const Opera
     if (rc != VC_SUCCESS) return rc;
     p.out[r] = out[r];
     p.offsets[r] = offsets[r];
-    p.pairs = p.pairs && reinterpret_cast<uintptr_t>(out[r]) % 4 == 0;
+    p.whole = p.whole && reinterpret_cast<uintptr_t>(out[r]) % 16 == 0;
   }
   p.capacity = static_cast<int32_t>(z.capacity);
   p.M = static_cast<int>(M);
@@ -854,9 +899,7 @@ vc_status_t launch_product(DeviceState* st, int dev, const Sizes& z, const Opera
   p.K = static_cast<int>(K);
   p.experts = z.nexperts;
   p.each = z.each;
-  p.type = dtype == VC_BFLOAT16 ? 1 : 0;
-  p.out_dtype = out_dtype;
-  return launch<product_kernel<AMN, WEIGHT, R>>(dev, Shape{2 * grid_of(st, tiles, 2), kTcThreads, kTcSmem, 2}, stream, p,
+  return launch<product_kernel<DT, OUT, AMN, WEIGHT, R>>(dev, Shape{2 * grid_of(st, tiles, 2), kTcThreads, kTcSmem, 2}, stream, p,
                                                 WEIGHT ? kExpertWeight : kExpertProduct, step, bytes);
 }
 
@@ -867,13 +910,12 @@ vc_status_t rows_product(DeviceState* st, int dev, const Sizes& z, const Operand
   const int64_t bytes = (z.nranks * z.capacity * (in + width) + z.nexperts * in * width) * dtype_size(dtype);
   if (dtype != VC_FLOAT32) {
     const int64_t tiles = row_tiles(z, kTileN) * ((width + 2 * kTileM - 1) / (2 * kTileM));
-    const auto go = [&](auto mn, auto ranks) {
-      return launch_product<mn(), false, ranks()>(st, dev, z, weight, rows, offsets, out, width, 0, in, dtype, dtype, tiles, bytes, step, stream);
-    };
-    const auto sized = [&](auto mn) {
-      return z.nranks <= 8 ? go(mn, std::integral_constant<int, 8>{}) : go(mn, std::integral_constant<int, VC_MAX_RANKS>{});
-    };
-    return transposed ? sized(std::false_type{}) : sized(std::true_type{});
+    return for_sizes(dtype, z.nranks, [&](auto type, auto ranks) {
+      const auto go = [&](auto mn) {
+        return launch_product<type(), type(), mn(), false, ranks()>(st, dev, z, weight, rows, offsets, out, width, 0, in, tiles, bytes, step, stream);
+      };
+      return transposed ? go(std::false_type{}) : go(std::true_type{});
+    });
   }
   SimpleParams p = {};
   for (int r = 0; r < z.nranks; ++r) {
@@ -904,10 +946,12 @@ vc_status_t weights_gradient(DeviceState* st, int dev, const Sizes& z, const Ope
   const int64_t bytes = z.nranks * z.capacity * (N + M) * dtype_size(dtype) + z.nexperts * N * M * dtype_size(out_dtype);
   if (dtype != VC_FLOAT32) {
     const int64_t tiles = z.nexperts * ((N + kTileN - 1) / kTileN) * ((M + 2 * kTileM - 1) / (2 * kTileM));
-    const auto go = [&](auto ranks) {
-      return launch_product<true, true, ranks()>(st, dev, z, right, left, offsets, dweight, M, N, 0, dtype, out_dtype, tiles, bytes, step, stream);
-    };
-    return z.nranks <= 8 ? go(std::integral_constant<int, 8>{}) : go(std::integral_constant<int, VC_MAX_RANKS>{});
+    return for_sizes(dtype, z.nranks, [&](auto type, auto ranks) {
+      const auto go = [&](auto to) {
+        return launch_product<type(), to(), true, true, ranks()>(st, dev, z, right, left, offsets, dweight, M, N, 0, tiles, bytes, step, stream);
+      };
+      return out_dtype == VC_FLOAT32 ? go(std::integral_constant<int, VC_FLOAT32>{}) : go(type);
+    });
   }
   SimpleParams p = {};
   for (int r = 0; r < z.nranks; ++r) {
