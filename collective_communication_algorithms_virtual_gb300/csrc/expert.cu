@@ -490,8 +490,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
 // these hold 128 sums a thread and take the registers that the first four warps
 // give up (launched with 168 each: 4 x 40 + 8 x 232 = 12 x 168).
 constexpr int kTile8N = 256, kTile8K = 128;
-constexpr int kTc8Threads = 384;
-constexpr int kTileBytesB8 = kTile8N * kTile8K;
+constexpr int kTc8Threads = 384, kTc8Warps = 8;
+constexpr int kRoom8Bytes = kTc8Warps * 32 * 128;
 
 template <int R>
 struct Product8Params {
@@ -526,6 +526,44 @@ __device__ __forceinline__ Tile8 tile8_at(const P& p, const uint32_t* ends, uint
   return x;
 }
 
+// A thread's 128 sums of one row to out in whole 16 bytes, 128 bytes of a row
+// at a time through the warp's `room`, so that a store is four rows' 128 bytes
+// (16 bytes a lane and row took 12% of a product of 8192 by 8192 by 8192).
+template <int OUT>
+__device__ __forceinline__ void store_sums(const float (&acc)[128], uint32_t room, char* out, int64_t pitch, int rows, int left) {
+  using E = El<OUT>;
+  constexpr int kEach = 128 / E::kSize;  // elements of 128 bytes
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 128; c += kEach) {
+    if (c >= left) break;
+    __syncwarp();  // the last ones have been read
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint4 x = E::narrow(acc + c + j * E::kVec);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(room + lane * 128 + ((j ^ lane) & 7) * 16), "r"(x.x), "r"(x.y), "r"(x.z),
+                   "r"(x.w)
+                   : "memory");
+    }
+    __syncwarp();
+    const int j = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + lane / 8;
+      uint4 x;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                   : "r"(room + r * 128 + ((j ^ r) & 7) * 16)
+                   : "memory");
+      if (r < rows && c + j * E::kVec < left) *reinterpret_cast<uint4*>(out + r * pitch + c * E::kSize + j * 16) = x;
+    }
+  }
+}
+
+// A tile is 128 rows by 256 outputs.  (Pairs of blocks with 256 rows, each
+// loading half of the weights, measured 321 us against 310 at the prefill of
+// 32768 rows, 4096 by 2048, and 103 against 74 with a few rows an expert: a
+// pair's products take as long for 32 rows as for 256.)
 template <int OUT, int R>
 __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_constant__ Product8Params<R> p) {
   extern __shared__ unsigned char dynamic[];
@@ -533,29 +571,30 @@ __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_c
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
   __shared__ uint32_t columns, gone;
   __shared__ int longest;
+  constexpr uint32_t kWeightBytes = kTile8N * kTile8K;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t full = tc::smem_addr(bars), empty = full + 8 * kMaxStages, sums_full = empty + 8 * kMaxStages,
                  sums_empty = sums_full + 16, done = sums_empty + 16;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) tc::bar_init(full + 8 * s, 1), tc::bar_init(empty + 8 * s, 1);
-    for (int s = 0; s < 2; ++s) tc::bar_init(sums_full + 8 * s, 1), tc::bar_init(sums_empty + 8 * s, 8);
+    for (int s = 0; s < 2; ++s) tc::bar_init(sums_full + 8 * s, 1), tc::bar_init(sums_empty + 8 * s, kTc8Warps);
     tc::bar_init(done, 1);
     gone = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tc::take_columns<false>(tc::smem_addr(&columns), kColumns);
-  tc::before_sync();
   stream_order();
   if (warp == 0)
     tc::list_tiles(p.offsets, p.experts, p.each, p.capacity, kTileM, (p.M + kTile8N - 1) / kTile8N, ends, &longest);
+  tc::before_sync();
   __syncthreads();
   tc::after_sync();
   const uint32_t total = ends[p.experts - 1];
-  const uint32_t row_bytes = (min(kTileM, longest) + 31) / 32 * 4096, stage_bytes = kTileBytesB8 + row_bytes;
-  const uint32_t tiles = (tc::smem_addr(dynamic) + 1023) & ~1023u;
+  const uint32_t row_bytes = (min(kTileM, longest) + 31) / 32 * 4096, stage_bytes = kWeightBytes + row_bytes;
+  const uint32_t room = (tc::smem_addr(dynamic) + 1023) & ~1023u, tiles = room + kRoom8Bytes;
   // The products read 128 rows whatever was loaded: past the last stage's there
   // is room for them.  What they make of the others is not looked at.
-  const int stages = min(kMaxStages, static_cast<int>((kTcSmem - 1024 - (kTileM * kTile8K - row_bytes)) / stage_bytes));
+  const int stages = min(kMaxStages, static_cast<int>((kTcSmem - 1024 - kRoom8Bytes - (kTileM * kTile8K - row_bytes)) / stage_bytes));
   const uint32_t sums = columns;
   const int blocks = (p.K + kTile8K - 1) / kTile8K;
 
@@ -569,15 +608,17 @@ __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_c
         for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
           const Tile8 x = tile8_at(p, ends, t, e);
           const int boxes = (x.n + 31) / 32;
+          const CUtensorMap *rows = p.rows + x.d, *weight = p.weight + x.d;
           for (int k = 0; k < blocks; ++k) {
             if (!tc::bar_wait(empty + 8 * s, phase ^ 1, &gone)) {
               ok = false;
               break;
             }
-            const uint32_t bar = full + 8 * s, to = tiles + s * stage_bytes;
-            tc::bar_expect(bar, kTileBytesB8 + boxes * 4096);
-            tc::load3d(to, p.weight + x.d, bar, k * kTile8K, x.m0, x.i);
-            for (int j = 0; j < boxes; ++j) tc::load2d(to + kTileBytesB8 + j * 4096, p.rows + x.d, bar, k * kTile8K, x.first + j * 32);
+            const uint32_t to = tiles + s * stage_bytes;
+            const uint32_t bar = full + 8 * s;
+            tc::bar_expect(bar, kWeightBytes + boxes * 4096);
+            tc::load3d(to, weight, bar, k * kTile8K, x.m0, x.i);
+            for (int j = 0; j < boxes; ++j) tc::load2d(to + kWeightBytes + j * 4096, rows, bar, k * kTile8K, x.first + j * 32);
             ++issued;
             if (++s == stages) s = 0, phase ^= 1;
           }
@@ -585,7 +626,8 @@ __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_c
         for (int j = 0; j < stages && issued > static_cast<uint32_t>(j); ++j) {  // as in product_kernel
           if (s-- == 0) s = stages - 1, phase ^= 1;
           if (ok) ok = tc::bar_wait(empty + 8 * s, phase, &gone);
-          else tc::bar_wait(full + 8 * s, phase, &gone);
+          if (!ok)
+            for (uint32_t it = 0; it < tc::kSoon && !tc::bar_test(full + 8 * s, phase); ++it) __nanosleep(64);
         }
       }
     } else if (warp == 1) {
@@ -593,7 +635,7 @@ __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_c
         int e = 0, s = 0, half = 0;
         uint32_t phase = 0, half_phase = 0;
         bool ok = true;
-        const uint64_t b0 = tc::desc_k(tiles), a0 = tc::desc_k(tiles + kTileBytesB8);
+        const uint64_t b0 = tc::desc_k(tiles), a0 = tc::desc_k(tiles + kWeightBytes);
         for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
           const Tile8 x = tile8_at(p, ends, t, e);
           const uint32_t how = tc::instruction(0, false, false, (min(kTile8N, p.M - x.m0) + 15) / 16 * 16, kTileM);
@@ -624,49 +666,62 @@ __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_c
     uint32_t half_phase = 0;
     bool ok = true;
     const int part = warp & 3, side = (warp - 4) / 4;  // lanes of tensor memory; which 128 of the 256 outputs
-    const int64_t down = (p.M + VC_FP8_BLOCK - 1) / VC_FP8_BLOCK;
+    const int64_t down = (p.M + VC_FP8_BLOCK - 1) / VC_FP8_BLOCK, pitch = static_cast<int64_t>(p.M) * El<OUT>::kSize;
     for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
       const Tile8 x = tile8_at(p, ends, t, e);
       const int m = x.m0 + side * 128, row = part * 32 + lane;
       const bool busy = m < p.M && part * 32 < x.n, there = row < x.n;
-      const float* rs = p.row_scale[x.d] + (static_cast<int64_t>(x.first) + (there ? row : 0)) * blocks;
+      const float* rs = p.row_scale[x.d] + (there ? (static_cast<int64_t>(x.first) + row) * blocks : 0);
       const float* ws = p.weight_scale[x.d] + (x.i * down + (m < p.M ? m / VC_FP8_BLOCK : 0)) * blocks;
       float acc[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) acc[j] = 0.f;
-      float by = blocks > 0 ? __ldg(rs) * __ldg(ws) : 0.f;
+      float sr = blocks > 0 && there ? __ldg(rs) : 0.f, sw = blocks > 0 ? __ldg(ws) : 0.f;
       for (int k = 0; k < blocks; ++k) {
-        const float next = k + 1 < blocks ? __ldg(rs + k + 1) * __ldg(ws + k + 1) : 0.f;
+        const float by = sr * sw;
+        if (k + 1 < blocks) {
+          sr = there ? __ldg(rs + k + 1) : 0.f;
+          sw = __ldg(ws + k + 1);
+        }
         ok = tc::warp_wait(sums_full + 8 * half, half_phase, &gone, tc::kLate);
         if (!ok) break;
         if (busy) {
           tc::after_sync();
+          const uint32_t from = sums + (part << 21) + half * kTile8N + side * 128;
+          uint32_t v[32], w[32];
+          tc::load_columns(from, v);
+          // 32 sums at a time, the next ones on their way from tensor memory
+          const auto add = [&](uint32_t(&now)[32], uint32_t(&after)[32], auto from_column) {
+            constexpr int c = decltype(from_column)::value;
+            tc::loaded(now);
+            if constexpr (c < 96) {
+              tc::load_columns(from + c + 32, after);
+            } else {
+              tc::before_sync();
+              __syncwarp();
+              if (lane == 0) tc::bar_arrive(sums_empty + 8 * half);
+            }
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
-            uint32_t v[32];
-            tc::load_columns(sums + (part << 21) + half * kTile8N + side * 128 + c, v);
-            tc::loaded(v);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(by, __uint_as_float(v[j]), acc[c + j]);
-          }
-          tc::before_sync();
+            for (int j = 0; j < 32; j += 2) tc::fma2(acc[c + j], acc[c + j + 1], by, now[j], now[j + 1]);
+          };
+          add(v, w, std::integral_constant<int, 0>{});
+          add(w, v, std::integral_constant<int, 32>{});
+          add(v, w, std::integral_constant<int, 64>{});
+          add(w, v, std::integral_constant<int, 96>{});
+        } else if (lane == 0) {
+          tc::bar_arrive(sums_empty + 8 * half);
         }
-        __syncwarp();
-        if (lane == 0) tc::bar_arrive(sums_empty + 8 * half);
-        by = next;
         if (half ^= 1; half == 0) half_phase ^= 1;
       }
-      if (!ok || !busy || !there) continue;
-      char* out = static_cast<char*>(p.out[x.d]) + ((static_cast<int64_t>(x.first) + row) * p.M + m) * El<OUT>::kSize;
+      if (!ok || !busy) continue;
+      char* out = static_cast<char*>(p.out[x.d]) + (static_cast<int64_t>(x.first) + part * 32) * pitch + static_cast<int64_t>(m) * El<OUT>::kSize;
       const int left = min(128, p.M - m);
       if (p.whole) {
-#pragma unroll
-        for (int j = 0; j < 128; j += El<OUT>::kVec)
-          if (j < left) *reinterpret_cast<uint4*>(out + j * El<OUT>::kSize) = El<OUT>::narrow(acc + j);
-      } else {
+        store_sums<OUT>(acc, room + (warp - 4) * (32 * 128), out, pitch, x.n - part * 32, left);
+      } else if (there) {
 #pragma unroll
         for (int j = 0; j < 128; ++j)
-          if (j < left) El<OUT>::store(out, j, acc[j]);
+          if (j < left) El<OUT>::store(out + lane * pitch, j, acc[j]);
       }
     }
   }

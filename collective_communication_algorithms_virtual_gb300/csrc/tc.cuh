@@ -198,6 +198,14 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
                : "memory");
 }
 
+// x += by * a, y += by * b, in one instruction, rounded as two.  Volatile, so that
+// it stays where it is written: between the start of a load and its wait.
+__device__ __forceinline__ void fma2(float& x, float& y, float by, uint32_t a, uint32_t b) {
+  asm volatile("{\n\t.reg .b64 s, v, t;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 v, {%3, %4};\n\tmov.b64 t, {%2, %2};\n\tfma.rn.f32x2 s, t, v, s;\n\tmov.b64 "
+      "{%0, %1}, s;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(by), "r"(a), "r"(b));
+}
 // ---------------------------------------------------------------------------
 // device: the tiles of ragged experts
 // ---------------------------------------------------------------------------
