@@ -15,6 +15,8 @@ VC_CHECK_TENSORS=0 in the environment skips them.
 from __future__ import annotations
 
 import ctypes
+import itertools
+import operator
 import os
 import struct
 from typing import Sequence
@@ -680,6 +682,7 @@ def vc_expert_product_backward(dout, rows, weight, offsets, drows=None, dweight=
 
 
 FP8_BLOCK = 128  # VC_FP8_BLOCK
+_dtype_of = operator.attrgetter("dtype")
 
 
 def _blocks(n: int) -> int:
@@ -745,40 +748,36 @@ def vc_clip_grad_norm(grads, norm, max_norm=None, out=None, across: bool = True,
     model), without over each rank's own.  ``max_norm`` None: the norm alone;
     else gradients above it are scaled to it, in place or into ``out[r]``."""
     torch = _torch()
-    N = len(grads)
-    mine = [t for ts in grads for t in ts]
-    T = len(mine) // N if N else 0
-    if any(len(ts) != T for ts in grads):
-        raise _invalid("the ranks must hold the same number of tensors")
-    like = norm[0] if norm.__class__ in _SEQUENCES else norm
+    N, T = len(grads), len(_first(grads, "grads"))
+    mine = list(itertools.chain.from_iterable(grads))
+    like = _first(norm, "norm") if norm.__class__ in _SEQUENCES else norm
     dev = like.get_device()
     if dev < 0:
         raise _invalid(f"tensors must be on a CUDA device, not {like.device}")
-    types = [t.dtype for t in mine[:T]]
-    sizes = [t.numel() for t in mine]
-    where = None
-    if max_norm is None:
-        if out is not None:
-            raise _invalid("out wants a max_norm")
-    else:
-        where = mine if out is None else [t for ts in out for t in ts]
-        if len(where) != len(mine) or (out is not None and any(len(ts) != T for ts in out)):
-            raise _invalid("out: want a tensor for each gradient")
+    if max_norm is None and out is not None:
+        raise _invalid("out wants a max_norm")
+    to = mine if out is None else list(itertools.chain.from_iterable(out))
+    if set(map(len, grads)) != {T} or (to is not mine and (len(out) != N or set(map(len, out)) != {T})):
+        raise _invalid("grads, out: want the same number of tensors on every rank")
+    Tensor = torch.Tensor
+    sizes = list(map(Tensor.numel, mine))
+    types = list(map(_dtype_of, mine[:T]))
     if CHECK_TENSORS:
-        for ts in (mine,) if where is None or where is mine else (mine, where):
-            for t, dt, n in zip(ts, types * N, sizes):
-                if t.dtype is not dt or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
-                    raise _invalid(f"gradients: want contiguous {n} of {dt} on cuda:{dev}, not {tuple(t.shape)} {t.dtype} on "
-                                   f"{t.device}" + ("" if t.is_contiguous() else " (not contiguous)"))
-    codes = {dt: _dtype_code(t) for dt, t in zip(types, mine)}
+        for ts in (mine, to)[:1 if to is mine else 2]:
+            if list(map(_dtype_of, ts)) != types * N or not set(map(Tensor.get_device, ts)) <= {dev} or \
+                    not all(map(Tensor.is_contiguous, ts)) or (ts is to and list(map(Tensor.numel, ts)) != sizes):
+                for t, dt, n in zip(ts, types * N, sizes):
+                    if t.dtype is not dt or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+                        raise _invalid(f"gradients: want contiguous {n} of {dt} on cuda:{dev}, not {tuple(t.shape)} {t.dtype} on "
+                                       f"{t.device}" + ("" if t.is_contiguous() else " (not contiguous)"))
+    code = {dt: _dtype_code(t) for dt, t in zip(types, mine)}
     M = N * T
-
-    def packed(ts):
-        return struct.pack(f"={M}Q", *[t.data_ptr() for t in ts])
+    ptrs = struct.pack(f"={M}Q", *map(Tensor.data_ptr, mine))
+    where = None if max_norm is None else ptrs if to is mine else struct.pack(f"={M}Q", *map(Tensor.data_ptr, to))
     check(lib().vc_clip_grad_norm(
-        packed(mine), None if where is None else packed(where), struct.pack(f"={M}Q", *sizes),
-        struct.pack(f"={T}i", *[codes[dt] for dt in types]), N, T, _ptrs(norm, "norm", (N,), 4, torch.float32, dev),
-        0.0 if max_norm is None else max_norm, bool(across), _stream_handle(stream, like)))
+        ptrs, where, struct.pack(f"={M}Q", *sizes), struct.pack(f"={T}i", *[code[dt] for dt in types]), N, T,
+        _ptrs(norm, "norm", (N,), 4, torch.float32, dev), 0.0 if max_norm is None else max_norm, bool(across),
+        _stream_handle(stream, like)))
 
 
 def vc_busbw_factor(coll, nranks: int) -> float:

@@ -3,6 +3,9 @@
 // Two passes over memory: squares are summed, then every gradient is scaled.
 // The second walks the chunks in the opposite order, so that it begins on what
 // the first left in L2.
+#include <iterator>
+#include <memory>
+
 #include "layer.cuh"
 
 namespace vc {
@@ -10,18 +13,19 @@ namespace layer {
 namespace {
 
 constexpr int kClipThreads = 256, kClipUnits = 8;
+// Blocks of a multiprocessor, by their registers.  24 layers' 2.4 GB, eight
+// ranks: the norm 400 us with 4 and 419 with 3 (what its loads need), clipping
+// 749 with 3 and 860 with 4 (which spills).
+constexpr int kNormBlocks = 4, kClipBlocks = 3;
 constexpr int64_t kChunkBytes = int64_t(kClipThreads) * kClipUnits * 16;  // of one tensor, at most, at a time
-constexpr int kTable = 768;  // tensors of one launch
 
 struct Tensor {
   const char* g;
   char* out;
   int64_t n;
 };
-struct ClipParams {
-  Tensor t[kTable];
-  uint32_t end[kTable];  // chunks of the rank's tensors so far in this launch
-  uint8_t dtype[kTable];
+// What both sizes of table have.
+struct ClipCall {
   uint16_t first[VC_MAX_RANKS + 1];  // of a rank's tensors
   double* part;          // [launch][rank][block]
   float* norm[VC_MAX_RANKS];
@@ -30,6 +34,15 @@ struct ClipParams {
   uint32_t launches, at;
   bool across;
 };
+// The tensors of one launch.  A call of few copies a small table.
+template <int N>
+struct ClipParams : ClipCall {
+  static constexpr int kTable = N;
+  Tensor t[N];
+  uint32_t end[N];  // chunks of the rank's tensors so far in this launch
+  uint8_t dtype[N];
+};
+constexpr int kFew = 96, kMany = 768;
 
 // A chunk: `n` elements at g and out.
 struct Chunk {
@@ -39,7 +52,8 @@ struct Chunk {
   int64_t n;
   int dtype;
 };
-__device__ __forceinline__ Chunk chunk_at(const ClipParams& p, int rank, uint32_t c) {
+template <class P>
+__device__ __forceinline__ Chunk chunk_at(const P& p, int rank, uint32_t c) {
   int lo = p.first[rank], hi = p.first[rank + 1] - 1;
   const int base = lo;
   while (lo < hi) {
@@ -55,6 +69,10 @@ __device__ __forceinline__ Chunk chunk_at(const ClipParams& p, int rank, uint32_
   x.out = x.t->out + at;
   x.n = min(kChunkBytes / es, x.t->n - at / es);
   return x;
+}
+template <class P>
+__device__ __forceinline__ uint32_t chunks_of(const P& p, int rank) {
+  return p.first[rank + 1] > p.first[rank] ? p.end[p.first[rank + 1] - 1] : 0;
 }
 
 template <class F>
@@ -77,43 +95,63 @@ __device__ __forceinline__ double block_sum(double x, double* part) {
   return all;
 }
 
-template <int DT, bool VEC>
-__device__ __forceinline__ float squares(const Chunk& x) {
+// A thread's units of a chunk, all loaded before `f` takes the first.  Off
+// 16-byte boundaries a unit is cut out of two loads: half as many at a time.
+// `between` runs once, while loads are on their way.
+template <int DT, bool VEC, class B, class F>
+__device__ __forceinline__ void units(const Chunk& x, B&& between, F&& f) {
   using E = El<DT>;
+  constexpr int kN = VEC ? kClipUnits : kClipUnits / 2;
   const int units = static_cast<int>((x.n + E::kVec - 1) / E::kVec);
   const Row<E::kSize, VEC> row(x.g, units, Bytes{x.t->g, x.t->g + x.t->n * E::kSize});
-  typename Row<E::kSize, VEC>::Raw raw[kClipUnits];
 #pragma unroll
-  for (int i = 0; i < kClipUnits; ++i) {
-    const int c = i * kClipThreads + threadIdx.x;
-    raw[i] = c < units ? row.load(c) : row.zero();
+  for (int i0 = 0; i0 < kClipUnits; i0 += kN) {
+    typename Row<E::kSize, VEC>::Raw raw[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int c = (i0 + i) * kClipThreads + threadIdx.x;
+      raw[i] = c < units ? row.load_plain(c) : row.zero();
+    }
+    if (i0 == 0) between();
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int c = (i0 + i) * kClipThreads + threadIdx.x;
+      if ((c & ~31) >= units) break;
+      float v[E::kVec] = {};
+      if (c < units) {
+        E::widen(row.finish(raw[i], c, x.n), v);
+        mask_unit<E::kSize, VEC>(c, x.n, v);
+      }
+      f(c, v);
+    }
   }
-  float sum[4] = {};
-#pragma unroll
-  for (int i = 0; i < kClipUnits; ++i) {
-    const int c = i * kClipThreads + threadIdx.x;
-    if (c >= units) break;
-    float f[E::kVec];
-    E::widen(row.finish(raw[i], c, x.n), f);
-    mask_unit<E::kSize, VEC>(c, x.n, f);
-#pragma unroll
-    for (int k = 0; k < E::kVec; ++k) sum[k % 4] = fmaf(f[k], f[k], sum[k % 4]);
-  }
-  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
-__global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const __grid_constant__ ClipParams p) {
+template <class P>
+__global__ void __launch_bounds__(kClipThreads, kNormBlocks) grad_norm_kernel(const __grid_constant__ P p) {
   __shared__ double part[kClipThreads / 32];
   stream_order();
   const int rank = blockIdx.y;
-  const uint32_t total = p.first[rank + 1] > p.first[rank] ? p.end[p.first[rank + 1] - 1] : 0;
+  const uint32_t total = chunks_of(p, rank);
   double sum = 0;
+  Chunk x, next{};
+  if (blockIdx.x < total) next = chunk_at(p, rank, blockIdx.x);
   for (uint32_t c = blockIdx.x; c < total; c += gridDim.x) {
-    const Chunk x = chunk_at(p, rank, c);
+    x = next;
     by_dtype(x.dtype, [&](auto code) {
       constexpr int DT = decltype(code)::value;
+      const auto go = [&](auto vec) {
+        float s[4] = {};
+        units<DT, decltype(vec)::value>(
+            x, [&] { if (c + gridDim.x < total) next = chunk_at(p, rank, c + gridDim.x); },
+            [&](int, const float* v) {
+#pragma unroll
+              for (int k = 0; k < El<DT>::kVec; ++k) s[k % 4] = fmaf(v[k], v[k], s[k % 4]);
+            });
+        sum += (s[0] + s[1]) + (s[2] + s[3]);
+      };
       const bool whole = reinterpret_cast<uintptr_t>(x.g) % 16 == 0 && x.n % El<DT>::kVec == 0;
-      sum += whole ? squares<DT, true>(x) : squares<DT, false>(x);
+      whole ? go(std::true_type{}) : go(std::false_type{});
     });
   }
   sum = block_sum(sum, part);
@@ -121,7 +159,7 @@ __global__ void __launch_bounds__(kClipThreads) grad_norm_kernel(const __grid_co
 }
 
 // The norm that rank `rank` goes by, from every block's part.
-__device__ __forceinline__ float norm_of(const ClipParams& p, int rank, int ranks, double* part) {
+__device__ __forceinline__ float norm_of(const ClipCall& p, int rank, int ranks, double* part) {
   double sum = 0;
   const int64_t all = static_cast<int64_t>(p.launches) * ranks * p.blocks;
   for (int64_t i = threadIdx.x; i < all; i += kClipThreads)
@@ -129,51 +167,45 @@ __device__ __forceinline__ float norm_of(const ClipParams& p, int rank, int rank
   return static_cast<float>(sqrt(block_sum(sum, part)));
 }
 
-template <int DT, bool VEC>
-__device__ __forceinline__ void scale_chunk(const Chunk& x, float by, unsigned char* room) {
-  using E = El<DT>;
-  const int units = static_cast<int>((x.n + E::kVec - 1) / E::kVec);
-  const Row<E::kSize, VEC> row(x.g, units, Bytes{x.t->g, x.t->g + x.t->n * E::kSize});
-  typename Row<E::kSize, VEC>::Raw raw[kClipUnits];
-#pragma unroll
-  for (int i = 0; i < kClipUnits; ++i) {
-    const int c = i * kClipThreads + threadIdx.x;
-    raw[i] = c < units ? row.load_plain(c) : row.zero();
-  }
-  if constexpr (!VEC) __syncthreads();  // in place: a unit is cut out of a neighbour's bytes too
-#pragma unroll
-  for (int i = 0; i < kClipUnits; ++i) {
-    const int c = i * kClipThreads + threadIdx.x, c0 = c & ~31;
-    if (c0 >= units) break;
-    float f[E::kVec];
-    E::widen(row.finish(raw[i], c, x.n), f);
-#pragma unroll
-    for (int k = 0; k < E::kVec; ++k) f[k] *= by;
-    Span<E::kSize, 16, VEC>(room, E::narrow(f)).template write<true>(x.out, c0, x.n);
-  }
-}
-
-__global__ void __launch_bounds__(kClipThreads) clip_kernel(const __grid_constant__ ClipParams p) {
+// In place too: a unit's bytes are written by its own warp alone, after it has
+// loaded them, and of what else its loads bring nothing is used.
+template <class P>
+__global__ void __launch_bounds__(kClipThreads, kClipBlocks) clip_kernel(const __grid_constant__ P p) {
   __shared__ double part[kClipThreads / 32];
-  __shared__ __align__(16) unsigned char room[kClipThreads / 32][Span<2, 16, false>::kRoom];
+  __shared__ __align__(16) unsigned char rooms[kClipThreads / 32][Span<2, 16, false>::kRoom];
   stream_order();
   const int rank = blockIdx.y;
+  unsigned char* room = rooms[threadIdx.x / 32];
   const float norm = norm_of(p, rank, gridDim.y, part);
   if (p.at == 0 && blockIdx.x == 0 && threadIdx.x == 0) *p.norm[rank] = norm;
   const float by = norm <= p.max_norm ? 1.f : __fdiv_rn(p.max_norm, norm);
-  const uint32_t total = p.first[rank + 1] > p.first[rank] ? p.end[p.first[rank + 1] - 1] : 0;
-  for (uint32_t i = blockIdx.x; i < total; i += gridDim.x) {
-    const Chunk x = chunk_at(p, rank, total - 1 - i);
-    if (by == 1.f && x.g == x.out) continue;
+  const uint32_t total = chunks_of(p, rank);
+  Chunk x, next{};
+  if (blockIdx.x < total) next = chunk_at(p, rank, total - 1 - blockIdx.x);
+  for (uint32_t c = blockIdx.x; c < total; c += gridDim.x) {
+    x = next;
+    const auto ahead = [&] { if (c + gridDim.x < total) next = chunk_at(p, rank, total - 1 - c - gridDim.x); };
+    if (by == 1.f && x.g == x.out) {
+      ahead();
+      continue;
+    }
     by_dtype(x.dtype, [&](auto code) {
       constexpr int DT = decltype(code)::value;
+      const auto go = [&](auto vec) {
+        constexpr bool VEC = decltype(vec)::value;
+        units<DT, VEC>(x, ahead, [&](int u, float* v) {
+#pragma unroll
+          for (int k = 0; k < El<DT>::kVec; ++k) v[k] *= by;
+          Span<El<DT>::kSize, 16, VEC>(room, El<DT>::narrow(v)).template write<true>(x.out, u & ~31, x.n);
+        });
+      };
       const bool whole = (reinterpret_cast<uintptr_t>(x.g) | reinterpret_cast<uintptr_t>(x.out)) % 16 == 0 && x.n % El<DT>::kVec == 0;
-      whole ? scale_chunk<DT, true>(x, by, room[threadIdx.x / 32]) : scale_chunk<DT, false>(x, by, room[threadIdx.x / 32]);
+      whole ? go(std::true_type{}) : go(std::false_type{});
     });
   }
 }
 
-__global__ void __launch_bounds__(kClipThreads) norm_kernel(const __grid_constant__ ClipParams p) {
+__global__ void __launch_bounds__(kClipThreads) norm_kernel(const __grid_constant__ ClipCall p) {
   __shared__ double part[kClipThreads / 32];
   stream_order();
   const float norm = norm_of(p, blockIdx.x, gridDim.x, part);
@@ -187,26 +219,116 @@ vc_status_t check_apart(const void* const* g, void* const* out, const size_t* co
     uintptr_t lo, hi;
     bool out;
   };
+  // As a rule a rank's tensors lie one behind another, or a few runs of them
+  // do: runs that do not interleave have no overlaps.
   std::vector<Range> ranges;
-  ranges.reserve(tensors * nranks * 2 + nranks);
-  const auto add = [&](const void* p, int64_t bytes, bool o) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    if (bytes) ranges.push_back(Range{lo, lo + static_cast<uintptr_t>(bytes), o});
+  const auto every = [&](auto&& add) {
+    for (int pass = 0; pass < (out ? 2 : 1); ++pass)
+      for (size_t i = 0; i < tensors * nranks; ++i) {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(pass ? out[i] : g[i]);
+        const uintptr_t bytes = counts[i] * static_cast<uintptr_t>(dtype_size(dtypes[i % tensors]));
+        if (bytes && (pass || !out || out[i] != g[i])) add(Range{lo, lo + bytes, pass != 0});
+      }
+    for (int r = 0; r < nranks; ++r) add(Range{reinterpret_cast<uintptr_t>(norm[r]), reinterpret_cast<uintptr_t>(norm[r]) + 4, true});
   };
-  for (size_t i = 0; i < tensors * nranks; ++i) {
-    const int64_t bytes = static_cast<int64_t>(counts[i]) * dtype_size(dtypes[i % tensors]);
-    if (!out || out[i] != g[i]) add(g[i], bytes, false);
-    if (out) add(out[i], bytes, true);
+  const auto apart = [&] {
+    std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    uintptr_t any = 0, outs = 0;
+    for (const Range& x : ranges) {
+      if (x.lo < outs || (x.out && x.lo < any)) return false;
+      any = std::max(any, x.hi);
+      if (x.out) outs = std::max(outs, x.hi);
+    }
+    return true;
+  };
+  every([&](const Range& x) {
+    if (!ranges.empty() && ranges.back().out == x.out && x.lo >= ranges.back().hi) ranges.back().hi = x.hi;
+    else ranges.push_back(x);
+  });
+  if (apart()) return VC_SUCCESS;
+  ranges.clear();
+  every([&](const Range& x) { ranges.push_back(x); });
+  return apart() ? VC_SUCCESS : fail(VC_ERR_INVALID_ARG, "an output buffer overlaps another buffer");
+}
+
+// The call's launches, with tables of P's size.
+template <class P>
+vc_status_t clip_with(const void* const* g, void* const* out, const size_t* counts, const vc_dtype_t* dtypes, int nranks, size_t tensors,
+                      float* const* norm, double max_norm, int across, int64_t bytes, cudaStream_t stream) {
+  DeviceState* st = nullptr;
+  int dev = 0;
+  vc_status_t rc = device_state(&st, &dev);
+  if (rc != VC_SUCCESS) return rc;
+  // the tensors that hold something, cut into tables by rank
+  std::vector<std::unique_ptr<P>> tables;
+  uint32_t most = 0;  // chunks of the rank that has most, in any table
+  int filled = P::kTable;
+  const auto open = [&] {
+    tables.emplace_back(new P);  // of the arrays, what is filled is looked at
+    std::fill(std::begin(tables.back()->first), std::end(tables.back()->first), uint16_t(0));
+    filled = 0;
+  };
+  for (int r = 0; r < nranks; ++r) {
+    uint32_t end = 0;
+    for (size_t i = 0; i < tensors; ++i) {
+      const size_t at = r * tensors + i;
+      if (counts[at] == 0) continue;
+      if (filled == P::kTable) {
+        if (!tables.empty())
+          for (int q = r + 1; q <= nranks; ++q) tables.back()->first[q] = static_cast<uint16_t>(filled);
+        open();
+        end = 0;
+      }
+      P& p = *tables.back();
+      const int64_t size = static_cast<int64_t>(counts[at]) * dtype_size(dtypes[i]);
+      p.t[filled] = Tensor{static_cast<const char*>(g[at]), out ? static_cast<char*>(out[at]) : nullptr, static_cast<int64_t>(counts[at])};
+      p.dtype[filled] = static_cast<uint8_t>(dtypes[i]);
+      end += static_cast<uint32_t>((size + kChunkBytes - 1) / kChunkBytes);
+      p.end[filled++] = end;
+      most = std::max(most, end);
+    }
+    if (!tables.empty()) tables.back()->first[r + 1] = static_cast<uint16_t>(filled);
   }
-  for (int r = 0; r < nranks; ++r) add(norm[r], 4, true);
-  std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
-  uintptr_t any = 0, outs = 0;
-  for (const Range& x : ranges) {
-    if (x.lo < outs || (x.out && x.lo < any)) return fail(VC_ERR_INVALID_ARG, "an output buffer overlaps another buffer");
-    any = std::max(any, x.hi);
-    if (x.out) outs = std::max(outs, x.hi);
+  if (tables.empty()) open();
+  const uint32_t launches = static_cast<uint32_t>(tables.size());
+  const auto blocks_of = [&](int resident) {
+    const int64_t fit = (int64_t(st->nsm) * resident + nranks - 1) / nranks;
+    return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(fit, most)));
+  };
+  const unsigned blocks = blocks_of(resident_blocks<grad_norm_kernel<P>>(dev, kClipThreads, 0));
+  const unsigned clip_blocks = blocks_of(resident_blocks<clip_kernel<P>>(dev, kClipThreads, 0));
+  cudaMemPool_t pool;
+  rc = scratch_pool(st, dev, &pool);
+  if (rc != VC_SUCCESS) return rc;
+  double* part = nullptr;
+  const size_t need = sizeof(double) * launches * nranks * blocks;
+  cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void**>(&part), need, pool, stream);
+  if (e == cudaErrorMemoryAllocation) {
+    cudaGetLastError();
+    return fail(VC_ERR_NOMEM, "scratch allocation of " + std::to_string(need) + " bytes failed");
   }
-  return VC_SUCCESS;
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMallocFromPoolAsync");
+  const unsigned n = static_cast<unsigned>(nranks);
+  int step = 0;
+  for (uint32_t i = 0; i < launches && rc == VC_SUCCESS; ++i) {
+    P& p = *tables[i];
+    std::copy(norm, norm + nranks, p.norm);
+    p.part = part;
+    p.blocks = blocks;
+    p.launches = launches;
+    p.at = i;
+    p.across = across != 0;
+    p.max_norm = static_cast<float>(max_norm);
+    rc = launch<grad_norm_kernel<P>>(dev, Shape{blocks, kClipThreads, 0, 1, n}, stream, p, kGradNorm, step++, i == 0 ? bytes : 0);
+  }
+  if (rc == VC_SUCCESS && !out)
+    rc = launch<norm_kernel, ClipCall>(dev, Shape{n, kClipThreads}, stream, *tables[0], kGradNorm, step++, static_cast<int64_t>(need));
+  // the last table first: its gradients are the ones left in L2
+  for (uint32_t i = launches; out && i-- > 0 && rc == VC_SUCCESS;)
+    rc = launch<clip_kernel<P>>(dev, Shape{clip_blocks, kClipThreads, 0, 1, n}, stream, *tables[i], kClip, step++, i == 0 ? 2 * bytes : 0);
+  e = cudaFreeAsync(part, stream);
+  if (e != cudaSuccess && rc == VC_SUCCESS) rc = cuda_fail(e, "cudaFreeAsync");
+  return rc;
 }
 
 vc_status_t clip(const void* const* g, void* const* out, const size_t* counts, const vc_dtype_t* dtypes, int nranks, size_t tensors,
@@ -238,85 +360,9 @@ vc_status_t clip(const void* const* g, void* const* out, const size_t* counts, c
   }
   rc = check_apart(g, out, counts, dtypes, tensors, nranks, norm);
   if (rc != VC_SUCCESS) return rc;
-  DeviceState* st = nullptr;
-  int dev = 0;
-  rc = device_state(&st, &dev);
-  if (rc != VC_SUCCESS) return rc;
-
-  // the tensors that hold something, cut into tables by rank
-  std::vector<ClipParams> tables;
-  std::vector<uint32_t> most;  // chunks of the rank that has most, of each table
-  int64_t chunks = 0;
-  int filled = kTable;
-  for (int r = 0; r < nranks; ++r) {
-    uint32_t end = 0;
-    for (size_t i = 0; i < tensors; ++i) {
-      const size_t at = r * tensors + i;
-      if (counts[at] == 0) continue;
-      if (filled == kTable) {
-        if (!tables.empty())
-          for (int q = r + 1; q <= nranks; ++q) tables.back().first[q] = static_cast<uint16_t>(filled);
-        tables.emplace_back();
-        most.push_back(0);
-        for (int q = 0; q <= nranks; ++q) tables.back().first[q] = 0;
-        filled = 0;
-        end = 0;
-      }
-      ClipParams& p = tables.back();
-      const int64_t bytes = static_cast<int64_t>(counts[at]) * dtype_size(dtypes[i]), n = (bytes + kChunkBytes - 1) / kChunkBytes;
-      p.t[filled] = Tensor{static_cast<const char*>(g[at]), out ? static_cast<char*>(out[at]) : nullptr, static_cast<int64_t>(counts[at])};
-      p.dtype[filled] = static_cast<uint8_t>(dtypes[i]);
-      end += static_cast<uint32_t>(n);
-      chunks += n;
-      p.end[filled++] = end;
-      most.back() = std::max(most.back(), end);
-    }
-    if (!tables.empty()) tables.back().first[r + 1] = static_cast<uint16_t>(filled);
-  }
-  if (tables.empty()) {
-    tables.emplace_back();
-    most.push_back(0);
-    for (int q = 0; q <= nranks; ++q) tables.back().first[q] = 0;
-  }
-  const uint32_t launches = static_cast<uint32_t>(tables.size());
-  const auto blocks_of = [&](int resident) {
-    const int64_t fit = (int64_t(st->nsm) * resident + nranks - 1) / nranks;
-    return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(fit, *std::max_element(most.begin(), most.end()))));
-  };
-  const unsigned blocks = blocks_of(resident_blocks<grad_norm_kernel>(dev, kClipThreads, 0));
-  const unsigned clip_blocks = blocks_of(resident_blocks<clip_kernel>(dev, kClipThreads, 0));
-  cudaMemPool_t pool;
-  rc = scratch_pool(st, dev, &pool);
-  if (rc != VC_SUCCESS) return rc;
-  double* part = nullptr;
-  const size_t need = sizeof(double) * launches * nranks * blocks;
-  cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void**>(&part), need, pool, stream);
-  if (e == cudaErrorMemoryAllocation) {
-    cudaGetLastError();
-    return fail(VC_ERR_NOMEM, "scratch allocation of " + std::to_string(need) + " bytes failed");
-  }
-  if (e != cudaSuccess) return cuda_fail(e, "cudaMallocFromPoolAsync");
-  const unsigned n = static_cast<unsigned>(nranks);
-  int step = 0;
-  for (uint32_t i = 0; i < launches; ++i) {
-    ClipParams& p = tables[i];
-    for (int r = 0; r < nranks; ++r) p.norm[r] = norm[r];
-    p.part = part;
-    p.blocks = blocks;
-    p.launches = launches;
-    p.at = i;
-    p.across = across != 0;
-    p.max_norm = static_cast<float>(max_norm);
-    if (rc == VC_SUCCESS)
-      rc = launch<grad_norm_kernel>(dev, Shape{blocks, kClipThreads, 0, 1, n}, stream, p, kGradNorm, step++, i == 0 ? bytes : 0);
-  }
-  if (rc == VC_SUCCESS && !out)
-    rc = launch<norm_kernel>(dev, Shape{n, kClipThreads}, stream, tables[0], kGradNorm, step++, static_cast<int64_t>(need));
-  for (uint32_t i = 0; out && i < launches && rc == VC_SUCCESS; ++i)
-    rc = launch<clip_kernel>(dev, Shape{clip_blocks, kClipThreads, 0, 1, n}, stream, tables[i], kClip, step++, i == 0 ? 2 * bytes : 0);
-  e = cudaFreeAsync(part, stream);
-  if (e != cudaSuccess && rc == VC_SUCCESS) rc = cuda_fail(e, "cudaFreeAsync");
-  return rc;
+  if (tensors * nranks <= kFew)
+    return clip_with<ClipParams<kFew>>(g, out, counts, dtypes, nranks, tensors, norm, max_norm, across, bytes, stream);
+  return clip_with<ClipParams<kMany>>(g, out, counts, dtypes, nranks, tensors, norm, max_norm, across, bytes, stream);
 }
 
 }  // namespace

@@ -49,14 +49,44 @@ struct Scale {
   }
 };
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// The largest magnitude of a 16-byte unit, as the type's own bits (the two
+// halves of a word each have one for 16-bit types: their order is their bits').
+template <int DT>
+__device__ __forceinline__ uint32_t largest_of(uint4 v) {
+  if constexpr (DT == VC_FLOAT32) {
+    constexpr uint32_t m = 0x7fffffffu;
+    return max(max(v.x & m, v.y & m), max(v.z & m, v.w & m));
+  } else {
+    constexpr uint32_t m = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+  }
+}
+template <int DT>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  if constexpr (DT == VC_FLOAT32) return max(a, b);
+  else return __vmaxu2(a, b);
+}
+// As fp32 bits.
+template <int DT>
+__device__ __forceinline__ uint32_t magnitude_of(uint32_t x) {
+  if constexpr (DT == VC_FLOAT32) return x;
+  else return __float_as_uint(dev::widen1<DT == VC_FLOAT16>(static_cast<uint16_t>(max(x & 0xffffu, x >> 16))));
+}
 
 // -- a scale for each row's 128 ---------------------------------------------------
 // A warp works four spans of 32 units (16 bytes) of one row, all loaded first;
 // 128 elements are 16 lanes (fp32: 32) of one span.
-constexpr int kSpans = 4;
+#ifndef SPANS
+#define SPANS 4
+#endif
+constexpr int kSpans = SPANS;
 
+#ifndef QB
+#define QB 4
+#define TB 2
+#endif
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads8) quantize_rows_kernel(const __grid_constant__ QuantizeParams p) {
+__global__ void __launch_bounds__(kThreads8, QB) quantize_rows_kernel(const __grid_constant__ QuantizeParams p) {
   using E = El<DT>;
   constexpr int kLanes = kBlock / E::kVec;
   __shared__ __align__(16) unsigned char room[kWarps8][Span<1, E::kVec, VEC>::kRoom];
@@ -66,10 +96,12 @@ __global__ void __launch_bounds__(kThreads8) quantize_rows_kernel(const __grid_c
   const char* x = static_cast<const char*>(p.x[d]);
   const Bytes ends{x, x + p.rows * p.width * E::kSize};
   const int units = static_cast<int>((p.width + E::kVec - 1) / E::kVec);
-  const int64_t total = rows * p.pieces;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps8 + warp; t < total; t += static_cast<int64_t>(gridDim.x) * kWarps8) {
-    const int64_t r = t / p.pieces;
-    const int c0 = static_cast<int>(t % p.pieces) * (kSpans * 32);
+  // rows and pieces of a rank: neither they nor the rows' warps pass 32 bits
+  const uint32_t warps = gridDim.x * kWarps8;
+  uint32_t r = (blockIdx.x * kWarps8 + warp) / p.pieces, piece = (blockIdx.x * kWarps8 + warp) % p.pieces;
+  const uint32_t step_r = warps / p.pieces, step_piece = warps % p.pieces;
+  while (r < rows) {
+    const int c0 = static_cast<int>(piece) * (kSpans * 32);
     const Row<E::kSize, VEC> row(x + r * p.width * E::kSize, units, ends);
     typename Row<E::kSize, VEC>::Raw raw[kSpans];
 #pragma unroll
@@ -77,28 +109,32 @@ __global__ void __launch_bounds__(kThreads8) quantize_rows_kernel(const __grid_c
       const int c = c0 + s * 32 + lane;
       raw[s] = c < units ? row.load(c) : row.zero();
     }
+    char* out = static_cast<char*>(p.out[d]) + r * p.width;
 #pragma unroll
     for (int s = 0; s < kSpans; ++s) {
       const int c = c0 + s * 32 + lane;
       if (c0 + s * 32 >= units) break;
       float f[E::kVec] = {};
-      if (c < units) {
+      uint32_t most = 0;
+      if constexpr (VEC) {
+        E::widen(raw[s], f);
+        most = largest_of<DT>(raw[s]);
+      } else if (c < units) {
         E::widen(row.finish(raw[s], c, p.width), f);
         mask_unit<E::kSize, VEC>(c, p.width, f);
+        most = largest_of<DT>(E::narrow(f));  // exact
       }
-      uint32_t most = 0;
 #pragma unroll
-      for (int i = 0; i < E::kVec; ++i) most = max(most, magnitude(f[i]));
-#pragma unroll
-      for (int k = kLanes / 2; k > 0; k >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, k));
-      const Scale by(most);
+      for (int k = kLanes / 2; k > 0; k >>= 1) most = larger<DT>(most, __shfl_xor_sync(0xffffffffu, most, k));
+      const Scale by(magnitude_of<DT>(most));
       if (lane % kLanes == 0 && c < units) p.scale[d][r * p.blocks + c / kLanes] = by.scale;
-      char* out = static_cast<char*>(p.out[d]) + r * p.width;
       if constexpr (E::kVec == 8)
         Span<1, 8, VEC>(room[warp], make_uint2(by.round4(f), by.round4(f + 4))).write(out, c0 + s * 32, p.width);
       else
         Span<1, 4, VEC>(room[warp], by.round4(f)).write(out, c0 + s * 32, p.width);
     }
+    r += step_r;
+    if ((piece += step_piece) >= p.pieces) piece -= p.pieces, ++r;
   }
 }
 
@@ -106,7 +142,7 @@ __global__ void __launch_bounds__(kThreads8) quantize_rows_kernel(const __grid_c
 // A block of threads holds a tile in registers.  VEC: a row's 128 elements are
 // 16 lanes (fp32: 32); otherwise a thread takes one column, element by element.
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads8) quantize_tiles_kernel(const __grid_constant__ QuantizeParams p) {
+__global__ void __launch_bounds__(kThreads8, TB) quantize_tiles_kernel(const __grid_constant__ QuantizeParams p) {
   using E = El<DT>;
   __shared__ uint32_t part[2][32];
   stream_order();
@@ -128,13 +164,8 @@ __global__ void __launch_bounds__(kThreads8) quantize_tiles_kernel(const __grid_
       for (int i = 0; i < kHeld; ++i)
         held[i] = r0 + i * kPass < rows && u < cols ? dev::ld16(x + i * kPass * p.width * E::kSize) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        float f[E::kVec];
-        E::widen(held[i], f);
-#pragma unroll
-        for (int k = 0; k < E::kVec; ++k) most = max(most, magnitude(f[k]));
-      }
-      const Scale by(block_max_bits(most, part[turn]));
+      for (int i = 0; i < kHeld; ++i) most = larger<DT>(most, largest_of<DT>(held[i]));
+      const Scale by(block_max_bits(magnitude_of<DT>(most), part[turn]));
       if (threadIdx.x == 0) p.scale[d][t] = by.scale;
       char* out = static_cast<char*>(p.out[d]) + (first + r0) * p.width + col0 + u;
 #pragma unroll
