@@ -33,21 +33,21 @@ struct QuantizeParams {
 // A block's scale, and what its elements are multiplied by.  `bits`: its
 // largest magnitude's (a NaN's are above infinity's).
 struct Scale {
-  float scale, by;
-  bool fine;  // neither NaN nor infinity in the block
+  float scale, by;  // by: NaN for a block with a NaN or an infinity
   __device__ __forceinline__ explicit Scale(uint32_t bits) {
     const float most = __uint_as_float(bits);
-    fine = bits < 0x7f800000u;
+    const bool fine = bits < 0x7f800000u;
     scale = !fine ? most : bits == 0 ? 0.f : fmaxf(__fdiv_rn(most, kMost8), kLeastScale);
-    by = fminf(__fdiv_rn(kMost8, most), 1.f / kLeastScale);
-  }
-  // Four elements, rounded once each to the nearest e4m3 number (ties to even).
-  __device__ __forceinline__ uint32_t round4(const float* f) const {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0] * by, f[1] * by), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2] * by, f[3] * by), __NV_SATFINITE, __NV_E4M3);
-    return fine ? lo | hi << 16 : 0u;
+    by = fine ? fminf(__fdiv_rn(kMost8, most), 1.f / kLeastScale) : __uint_as_float(0x7fffffffu);
   }
 };
+// Four elements, rounded once each to the nearest e4m3 number (ties to even);
+// zeros where `by` is NaN.
+__device__ __forceinline__ uint32_t round4(const float* f, float by) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0] * by, f[1] * by), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2] * by, f[3] * by), __NV_SATFINITE, __NV_E4M3);
+  return by == by ? lo | hi << 16 : 0u;
+}
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 // The largest magnitude of a 16-byte unit, as the type's own bits (the two
 // halves of a word each have one for 16-bit types: their order is their bits').
@@ -75,18 +75,13 @@ __device__ __forceinline__ uint32_t magnitude_of(uint32_t x) {
 
 // -- a scale for each row's 128 ---------------------------------------------------
 // A warp works four spans of 32 units (16 bytes) of one row, all loaded first;
-// 128 elements are 16 lanes (fp32: 32) of one span.
-#ifndef SPANS
-#define SPANS 4
-#endif
-constexpr int kSpans = SPANS;
+// 128 elements are 16 lanes (fp32: 32) of one span.  Of those lanes, lane i
+// divides for span i: with every lane dividing for its own span the kernel is
+// bound by its instructions (80 us for 268 MB of rows, where memory takes 60).
+constexpr int kSpans = 4;
 
-#ifndef QB
-#define QB 4
-#define TB 2
-#endif
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads8, QB) quantize_rows_kernel(const __grid_constant__ QuantizeParams p) {
+__global__ void __launch_bounds__(kThreads8, 4) quantize_rows_kernel(const __grid_constant__ QuantizeParams p) {
   using E = El<DT>;
   constexpr int kLanes = kBlock / E::kVec;
   __shared__ __align__(16) unsigned char room[kWarps8][Span<1, E::kVec, VEC>::kRoom];
@@ -109,29 +104,39 @@ __global__ void __launch_bounds__(kThreads8, QB) quantize_rows_kernel(const __gr
       const int c = c0 + s * 32 + lane;
       raw[s] = c < units ? row.load(c) : row.zero();
     }
-    char* out = static_cast<char*>(p.out[d]) + r * p.width;
+    uint4 unit[kSpans];
+    uint32_t mine = 0;
 #pragma unroll
     for (int s = 0; s < kSpans; ++s) {
       const int c = c0 + s * 32 + lane;
-      if (c0 + s * 32 >= units) break;
-      float f[E::kVec] = {};
-      uint32_t most = 0;
+      unit[s] = make_uint4(0, 0, 0, 0);
       if constexpr (VEC) {
-        E::widen(raw[s], f);
-        most = largest_of<DT>(raw[s]);
+        unit[s] = raw[s];
       } else if (c < units) {
+        float f[E::kVec];
         E::widen(row.finish(raw[s], c, p.width), f);
         mask_unit<E::kSize, VEC>(c, p.width, f);
-        most = largest_of<DT>(E::narrow(f));  // exact
+        unit[s] = E::narrow(f);  // exact
       }
+      uint32_t most = largest_of<DT>(unit[s]);
 #pragma unroll
       for (int k = kLanes / 2; k > 0; k >>= 1) most = larger<DT>(most, __shfl_xor_sync(0xffffffffu, most, k));
-      const Scale by(magnitude_of<DT>(most));
-      if (lane % kLanes == 0 && c < units) p.scale[d][r * p.blocks + c / kLanes] = by.scale;
+      if (lane % kSpans == s) mine = most;
+    }
+    const Scale own(magnitude_of<DT>(mine));
+    const int first = lane & ~(kLanes - 1), block = c0 / kLanes + (lane % kSpans) * (32 / kLanes) + first / kLanes;
+    if (lane - first < kSpans && block < p.blocks) p.scale[d][r * p.blocks + block] = own.scale;
+    char* out = static_cast<char*>(p.out[d]) + r * p.width;
+#pragma unroll
+    for (int s = 0; s < kSpans; ++s) {
+      if (c0 + s * 32 >= units) break;
+      const float by = __shfl_sync(0xffffffffu, own.by, first + s);
+      float f[E::kVec];
+      E::widen(unit[s], f);
       if constexpr (E::kVec == 8)
-        Span<1, 8, VEC>(room[warp], make_uint2(by.round4(f), by.round4(f + 4))).write(out, c0 + s * 32, p.width);
+        Span<1, 8, VEC>(room[warp], make_uint2(round4(f, by), round4(f + 4, by))).write(out, c0 + s * 32, p.width);
       else
-        Span<1, 4, VEC>(room[warp], by.round4(f)).write(out, c0 + s * 32, p.width);
+        Span<1, 4, VEC>(room[warp], round4(f, by)).write(out, c0 + s * 32, p.width);
     }
     r += step_r;
     if ((piece += step_piece) >= p.pieces) piece -= p.pieces, ++r;
@@ -142,7 +147,7 @@ __global__ void __launch_bounds__(kThreads8, QB) quantize_rows_kernel(const __gr
 // A block of threads holds a tile in registers.  VEC: a row's 128 elements are
 // 16 lanes (fp32: 32); otherwise a thread takes one column, element by element.
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads8, TB) quantize_tiles_kernel(const __grid_constant__ QuantizeParams p) {
+__global__ void __launch_bounds__(kThreads8, 2) quantize_tiles_kernel(const __grid_constant__ QuantizeParams p) {
   using E = El<DT>;
   __shared__ uint32_t part[2][32];
   stream_order();
@@ -173,8 +178,8 @@ __global__ void __launch_bounds__(kThreads8, TB) quantize_tiles_kernel(const __g
         if (r0 + i * kPass < rows && u < cols) {
           float f[E::kVec];
           E::widen(held[i], f);
-          if constexpr (E::kVec == 8) *reinterpret_cast<uint2*>(out + i * kPass * p.width) = make_uint2(by.round4(f), by.round4(f + 4));
-          else *reinterpret_cast<uint32_t*>(out + i * kPass * p.width) = by.round4(f);
+          if constexpr (E::kVec == 8) *reinterpret_cast<uint2*>(out + i * kPass * p.width) = make_uint2(round4(f, by.by), round4(f + 4, by.by));
+          else *reinterpret_cast<uint32_t*>(out + i * kPass * p.width) = round4(f, by.by);
         }
     } else {
       constexpr int kPass = kThreads8 / kBlock, kHeld = kBlock / kPass;
@@ -191,7 +196,7 @@ __global__ void __launch_bounds__(kThreads8, TB) quantize_tiles_kernel(const __g
       uint8_t* out = static_cast<uint8_t*>(p.out[d]) + at;
 #pragma unroll
       for (int i = 0; i < kHeld; i += 4) {
-        const uint32_t q = by.round4(f + i);
+        const uint32_t q = round4(f + i, by.by);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           if (r0 + (i + k) * kPass < rows && c < cols) out[(i + k) * kPass * p.width] = static_cast<uint8_t>(q >> (8 * k));
