@@ -488,10 +488,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
 // reads than products.
 //   warp 0 loads, warp 1 issues the products, warps 4 to 11 scale and store;
 // these hold 128 sums a thread and take the registers that the first four warps
-// give up (launched with 168 each: 4 x 40 + 8 x 232 = 12 x 168).
+// give up (launched with 168 each: 4 x 56 + 8 x 224 = 12 x 168).
 constexpr int kTile8N = 256, kTile8K = 128;
 constexpr int kTc8Threads = 384, kTc8Warps = 8;
-constexpr int kRoom8Bytes = kTc8Warps * 32 * 128;
+constexpr int kRoom8Bytes = kTc8Warps * 32 * 64;
 
 template <int R>
 struct Product8Params {
@@ -526,34 +526,35 @@ __device__ __forceinline__ Tile8 tile8_at(const P& p, const uint32_t* ends, uint
   return x;
 }
 
-// A thread's 128 sums of one row to out in whole 16 bytes, 128 bytes of a row
-// at a time through the warp's `room`, so that a store is four rows' 128 bytes
-// (16 bytes a lane and row took 12% of a product of 8192 by 8192 by 8192).
+// A thread's 128 sums of one row to out in whole 16 bytes, 64 bytes of a row at a
+// time through the warp's `room`, so that a store is eight rows' 64 bytes (16
+// bytes a lane and row took 12% of a product of 8192 by 8192 by 8192; a room of
+// 128 bytes a row would take the fourth stage's place).
 template <int OUT>
 __device__ __forceinline__ void store_sums(const float (&acc)[128], uint32_t room, char* out, int64_t pitch, int rows, int left) {
   using E = El<OUT>;
-  constexpr int kEach = 128 / E::kSize;  // elements of 128 bytes
+  constexpr int kEach = 64 / E::kSize;  // elements of 64 bytes
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int c = 0; c < 128; c += kEach) {
     if (c >= left) break;
     __syncwarp();  // the last ones have been read
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 4; ++j) {
       const uint4 x = E::narrow(acc + c + j * E::kVec);
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(room + lane * 128 + ((j ^ lane) & 7) * 16), "r"(x.x), "r"(x.y), "r"(x.z),
-                   "r"(x.w)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(room + lane * 64 + ((j ^ lane >> 1) & 3) * 16), "r"(x.x), "r"(x.y),
+                   "r"(x.z), "r"(x.w)
                    : "memory");
     }
     __syncwarp();
-    const int j = lane & 7;
+    const int j = lane & 3;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = i * 4 + lane / 8;
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + lane / 4;
       uint4 x;
       asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                   : "r"(room + r * 128 + ((j ^ r) & 7) * 16)
+                   : "r"(room + r * 64 + ((j ^ r >> 1) & 3) * 16)
                    : "memory");
       if (r < rows && c + j * E::kVec < left) *reinterpret_cast<uint4*>(out + r * pitch + c * E::kSize + j * 16) = x;
     }
@@ -688,26 +689,18 @@ __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_c
         if (busy) {
           tc::after_sync();
           const uint32_t from = sums + (part << 21) + half * kTile8N + side * 128;
-          uint32_t v[32], w[32];
-          tc::load_columns(from, v);
-          // 32 sums at a time, the next ones on their way from tensor memory
-          const auto add = [&](uint32_t(&now)[32], uint32_t(&after)[32], auto from_column) {
-            constexpr int c = decltype(from_column)::value;
-            tc::loaded(now);
-            if constexpr (c < 96) {
-              tc::load_columns(from + c + 32, after);
-            } else {
-              tc::before_sync();
-              __syncwarp();
-              if (lane == 0) tc::bar_arrive(sums_empty + 8 * half);
-            }
+          uint32_t v[2][16];  // 16 sums at a time, the next ones on their way: 32 do not fit with the 128
+          tc::load_columns(from, v[0]);
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) tc::fma2(acc[c + j], acc[c + j + 1], by, now[j], now[j + 1]);
-          };
-          add(v, w, std::integral_constant<int, 0>{});
-          add(w, v, std::integral_constant<int, 32>{});
-          add(v, w, std::integral_constant<int, 64>{});
-          add(w, v, std::integral_constant<int, 96>{});
+          for (int c = 0; c < 128; c += 16) {
+            tc::loaded(v[c / 16 & 1]);
+            if (c < 112) tc::load_columns(from + c + 16, v[~(c / 16) & 1]);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(__uint_as_float(v[c / 16 & 1][j]), by, acc[c + j]);
+          }
+          tc::before_sync();
+          __syncwarp();
+          if (lane == 0) tc::bar_arrive(sums_empty + 8 * half);
         } else if (lane == 0) {
           tc::bar_arrive(sums_empty + 8 * half);
         }
@@ -717,7 +710,7 @@ __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_c
       char* out = static_cast<char*>(p.out[x.d]) + (static_cast<int64_t>(x.first) + part * 32) * pitch + static_cast<int64_t>(m) * El<OUT>::kSize;
       const int left = min(128, p.M - m);
       if (p.whole) {
-        store_sums<OUT>(acc, room + (warp - 4) * (32 * 128), out, pitch, x.n - part * 32, left);
+        store_sums<OUT>(acc, room + (warp - 4) * (32 * 64), out, pitch, x.n - part * 32, left);
       } else if (there) {
 #pragma unroll
         for (int j = 0; j < 128; ++j)
@@ -736,26 +729,32 @@ __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_c
 // Tensor maps want them, so such rows are copied to scratch first, a row each
 // 16 bytes' multiple apart: the rows that the experts have, the weights of
 // experts that have rows.
-struct PadParams {
+struct PadRows {
   const void* from[VC_MAX_RANKS];
-  const int32_t* offsets[VC_MAX_RANKS];
   char* to;
-  int64_t rows;          // of each rank
-  int64_t width, pitch;  // elements, bytes
-  int64_t group;         // rows of each expert's weights; 0: the experts' rows
-  int32_t capacity;
-  int nranks, each;
+  int64_t rows;   // of each rank
+  int64_t group;  // rows of each expert's weights; 0: the experts' rows
+  int width;      // elements
+  int units;      // of 16 bytes that a row takes
 };
-constexpr int kPadThreads = 256;
+struct PadParams {
+  PadRows op[3];
+  const int32_t* offsets[VC_MAX_RANKS];
+  int32_t capacity;
+  int ranks, each;
+};
+constexpr int kPadThreads = 256, kPadAhead = 4;
 
+// Blocks' second dimension: operands by ranks.
 template <int ES>
 __global__ void __launch_bounds__(kPadThreads) pad_kernel(const __grid_constant__ PadParams p) {
   stream_order();
   const int lane = threadIdx.x & 31;
-  const int d = blockIdx.y;
-  const int64_t warps = gridDim.x * (kPadThreads / 32);
-  int64_t last = p.rows;
-  if (p.group == 0) {
+  const int d = blockIdx.y % p.ranks;
+  const PadRows& op = p.op[blockIdx.y / p.ranks];
+  const int64_t warps = gridDim.x * (kPadThreads / 32), pitch = static_cast<int64_t>(op.width) * ES;
+  int64_t last = op.rows;
+  if (op.group == 0) {
     int32_t most = 0;
     for (int i = lane; i < p.each; i += 32) {
       const Rows r = tc::rows_of(p.offsets[d], i, p.capacity);
@@ -763,14 +762,20 @@ __global__ void __launch_bounds__(kPadThreads) pad_kernel(const __grid_constant_
     }
     last = __reduce_max_sync(0xffffffffu, most);
   }
-  const char* from = static_cast<const char*>(p.from[d]);
-  const Bytes ends{from, from + p.rows * p.width * ES};
-  const int units = static_cast<int>(p.pitch / 16);
+  const char* from = static_cast<const char*>(op.from[d]);
+  const Bytes ends{from, from + op.rows * pitch};
   for (int64_t r = blockIdx.x * (kPadThreads / 32) + threadIdx.x / 32; r < last; r += warps) {
-    if (p.group != 0 && tc::rows_of(p.offsets[d], static_cast<int>(r / p.group), p.capacity).count == 0) continue;
-    const Row<ES, false> row(from + r * p.width * ES, units, ends);
-    uint4* to = reinterpret_cast<uint4*>(p.to + (d * p.rows + r) * p.pitch);
-    for (int c = lane; c < units; c += 32) to[c] = row.finish(row.load(c), c, p.width);
+    if (op.group != 0 && tc::rows_of(p.offsets[d], static_cast<int>(r / op.group), p.capacity).count == 0) continue;
+    const Row<ES, false> row(from + r * pitch, op.units, ends);
+    uint4* to = reinterpret_cast<uint4*>(op.to) + (d * op.rows + r) * op.units;
+    for (int c0 = lane; c0 < op.units; c0 += 32 * kPadAhead) {
+      typename Row<ES, false>::Raw raw[kPadAhead];
+#pragma unroll
+      for (int i = 0; i < kPadAhead; ++i) raw[i] = c0 + i * 32 < op.units ? row.load(c0 + i * 32) : row.zero();
+#pragma unroll
+      for (int i = 0; i < kPadAhead; ++i)
+        if (c0 + i * 32 < op.units) to[c0 + i * 32] = row.finish(raw[i], c0 + i * 32, op.width);
+    }
   }
 }
 
@@ -859,7 +864,7 @@ struct Operand {
   }
 };
 
-// Copies the operands that want it to scratch.
+// Copies the operands that want it to scratch, in one launch.
 vc_status_t pad(DeviceState* st, int dev, const Sizes& z, const int32_t* const* offsets, Operand* const* ops, int n, Scratch* scratch,
                 int* step, cudaStream_t stream) {
   int64_t need = 0;
@@ -872,33 +877,37 @@ vc_status_t pad(DeviceState* st, int dev, const Sizes& z, const int32_t* const* 
     }
   if (need == 0) return VC_SUCCESS;
   vc_status_t rc = scratch->take(need);
-  for (int i = 0; i < n && rc == VC_SUCCESS; ++i)
+  if (rc != VC_SUCCESS) return rc;
+  PadParams p = {};
+  int used = 0, es = 1;
+  int64_t most = 0, bytes = 0;
+  for (int i = 0; i < n; ++i)
     if (ops[i]->padded >= 0) {
       Operand& o = *ops[i];
-      PadParams p = {};
-      for (int r = 0; r < z.nranks; ++r) {
-        p.from[r] = o.p[r];
-        p.offsets[r] = offsets[r];
-      }
-      p.to = scratch->mem() + o.padded;
-      p.rows = o.rows;
-      p.width = o.width;
-      p.pitch = o.pitch;
-      p.group = o.group;
-      p.capacity = static_cast<int32_t>(z.capacity);
-      p.nranks = z.nranks;
-      p.each = z.each;
-      const auto go = [&](auto size) {
-        constexpr auto K = pad_kernel<size()>;
-        const int64_t fit = (int64_t(st->nsm) * resident_blocks<K>(dev, kPadThreads, 0) + z.nranks - 1) / z.nranks;
-        const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((o.rows + 7) / 8, fit));
-        return launch<K>(dev, Shape{blocks, kPadThreads, 0, 1, static_cast<unsigned>(z.nranks)}, stream, p, kPad, (*step)++,
-                         z.nranks * o.rows * (o.width * o.es + o.pitch));
-      };
-      rc = o.es == 2 ? go(std::integral_constant<int, 2>{}) : go(std::integral_constant<int, 1>{});
-      for (int r = 0; r < z.nranks; ++r) o.p[r] = p.to + r * o.rows * o.pitch;
+      PadRows& to = p.op[used++];
+      std::copy(o.p, o.p + z.nranks, to.from);
+      to.to = scratch->mem() + o.padded;
+      to.rows = o.rows;
+      to.group = o.group;
+      to.width = static_cast<int>(o.width);
+      to.units = static_cast<int>(o.pitch / 16);
+      es = o.es;
+      most = std::max(most, o.rows);
+      bytes += z.nranks * o.rows * (o.width * o.es + o.pitch);
+      for (int r = 0; r < z.nranks; ++r) o.p[r] = to.to + r * o.rows * o.pitch;
     }
-  return rc;
+  std::copy(offsets, offsets + z.nranks, p.offsets);
+  p.capacity = static_cast<int32_t>(z.capacity);
+  p.ranks = z.nranks;
+  p.each = z.each;
+  const auto go = [&](auto size) {
+    constexpr auto K = pad_kernel<size()>;
+    const unsigned parts = static_cast<unsigned>(used * z.nranks);
+    const int64_t fit = (int64_t(st->nsm) * resident_blocks<K>(dev, kPadThreads, 0) + parts - 1) / parts;
+    const unsigned blocks = static_cast<unsigned>(std::min<int64_t>((most + 7) / 8, fit));
+    return launch<K>(dev, Shape{blocks, kPadThreads, 0, 1, parts}, stream, p, kPad, (*step)++, bytes);
+  };
+  return es == 2 ? go(std::integral_constant<int, 2>{}) : go(std::integral_constant<int, 1>{});
 }
 
 CUtensorMapDataType map_type(vc_dtype_t d) {

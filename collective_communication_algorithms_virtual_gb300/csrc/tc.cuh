@@ -197,15 +197,22 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
                :
                : "memory");
 }
-
-// x += by * a, y += by * b, in one instruction, rounded as two.  Volatile, so that
-// it stays where it is written: between the start of a load and its wait.
-__device__ __forceinline__ void fma2(float& x, float& y, float by, uint32_t a, uint32_t b) {
-  asm volatile("{\n\t.reg .b64 s, v, t;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 v, {%3, %4};\n\tmov.b64 t, {%2, %2};\n\tfma.rn.f32x2 s, t, v, s;\n\tmov.b64 "
-      "{%0, %1}, s;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(by), "r"(a), "r"(b));
+// The same of 16 columns.
+__device__ __forceinline__ void load_columns(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
 }
+__device__ __forceinline__ void loaded(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // device: the tiles of ragged experts
 // ---------------------------------------------------------------------------
