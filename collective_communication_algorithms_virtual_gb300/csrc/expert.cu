@@ -282,15 +282,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
     gone = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  __syncwarp();
+  tc::cluster_sync();  // both blocks and their barriers are there
   if (warp == 1) tc::take_columns<true>(tc::smem_addr(&columns), kColumns);
   stream_order();
   const uint32_t across = (p.M + 2 * kTileM - 1) / (2 * kTileM);
   if constexpr (!WEIGHT) {
     if (warp == 0) tc::list_tiles(p.offsets, p.experts, p.each, p.capacity, kTileN, across, ends, &longest);
   }
+  // This block's list and columns; the products wait for the other block's loads,
+  // which come after its own barrier here.
   tc::before_sync();
-  __syncwarp();
-  tc::cluster_sync();  // both blocks' barriers are there, and this block's list
+  __syncthreads();
   tc::after_sync();
   const uint32_t total = WEIGHT ? p.experts * across * tc::pieces(p.N, kTileN) : ends[p.experts - 1];
   // Stages as small as the longest piece of n allows: few rows, many stages.
@@ -472,7 +475,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
   __syncwarp();
   tc::cluster_sync();  // neither block ends while the other may reach it
   tc::after_sync();
-  if (warp == 1) tc::free_columns<true>(sums, kColumns);
+  if (warp == 1) {
+    tc::take_no_more<true>();
+    tc::free_columns<true>(sums, kColumns);
+  }
+  __syncwarp();
+  tc::cluster_sync();
   if (gone && threadIdx.x == 0) atomicOr(&dev::g_device_error, 4u);
 }
 
@@ -488,7 +496,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
 // reads than products.
 //   warp 0 loads, warp 1 issues the products, warps 4 to 11 scale and store;
 // these hold 128 sums a thread and take the registers that the first four warps
-// give up (launched with 168 each: 4 x 56 + 8 x 224 = 12 x 168).
+// give up (launched with 168 each: 4 x 40 + 8 x 232 = 12 x 168).
 constexpr int kTile8N = 256, kTile8K = 128;
 constexpr int kTc8Threads = 384, kTc8Warps = 8;
 constexpr int kRoom8Bytes = kTc8Warps * 32 * 64;
@@ -721,7 +729,10 @@ __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_c
   tc::before_sync();
   __syncthreads();
   tc::after_sync();
-  if (warp == 1) tc::free_columns<false>(sums, kColumns);
+  if (warp == 1) {
+    tc::take_no_more<false>();
+    tc::free_columns<false>(sums, kColumns);
+  }
   if (gone && threadIdx.x == 0) atomicOr(&dev::g_device_error, 4u);
 }
 

@@ -160,16 +160,22 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
 }
 __device__ __forceinline__ void before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// One warp (of each block of a pair) takes and frees the accumulators' columns.
+// One warp (of each block of a pair) takes the accumulators' columns, and gives up
+// the right to take more and frees them.  A pair's blocks take theirs together:
+// the one that starts first must not ask before the other one is there (behind
+// a kernel that leaves its multiprocessors one by one they start far enough
+// apart that once in some ten thousand launches its request was never answered),
+// nor may either end or give up while the other one takes or frees.  So a pair
+// meets (cluster_sync) before it takes, before it gives up and frees, and after.
 template <bool PAIR>
 __device__ __forceinline__ void take_columns(uint32_t to, uint32_t n) {
-  if constexpr (PAIR) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(n) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-  } else {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(n) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
+  if constexpr (PAIR) asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(n) : "memory");
+  else asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(n) : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void take_no_more() {
+  if constexpr (PAIR) asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  else asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
 }
 template <bool PAIR>
 __device__ __forceinline__ void free_columns(uint32_t at, uint32_t n) {

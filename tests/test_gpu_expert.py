@@ -191,3 +191,22 @@ def test_same_bits_again_and_on_another_stream_and_replayed():
         graph.replay()
         same()
     assert vc.vc_device_errors() == 0
+
+
+def test_pairs_of_blocks_behind_a_kernel_that_leaves_one_by_one():
+    """Many passes enqueued ahead, weights copied to 16-byte boundaries before
+    each product: a pair's blocks start apart, and meet before they share tensor
+    memory."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    N, each, cap, win, width = 8, 5, 32, 1089, 2473
+    x, w = made(N, cap, win, dt="bf16", g=g), made(N, each, win, width, dt="bf16", g=g)
+    offs = [offsets_of(torch.randint(0, 3, (N, each), generator=torch.Generator().manual_seed(k)).numpy()) for k in range(3)]
+    outs = [torch.zeros(N, cap, width, dtype=DT["bf16"], device="cuda") for _ in range(3)]
+    for i in range(3):
+        vc.vc_expert_product(x, w, offs[i], outs[i])
+    want = [t.clone() for t in outs]
+    for _ in range(20):
+        for j in range(600):
+            vc.vc_expert_product(x, w, offs[j % 3], outs[j % 3])
+        assert vc.vc_device_errors() == 0
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
