@@ -7,11 +7,14 @@ rank's partial sums of the attention output (tensor parallelism); then
   1. vc_reduce_scatter_norm  partial sums + residual -> residual, norm
   2. vc_route                the router's logits -> experts and their weights
   3. vc_dispatch_plan, vc_dispatch   tokens to their experts' ranks
-  4. the experts' products (torch.matmul here)
+  4. the experts' products: torch.matmul in a loop that waits for the offsets,
+     or, with library=True, vc_expert_product, which reads them on the device
   5. vc_combine              the experts' answers, weighted, back to the tokens
 
-`serve` sends the tokens in 8 bits with a scale each; `train` keeps the data
-type and runs the whole chain backward.  The command compares both with plain
+`serve` sends the tokens in 8 bits with a scale each; `serve8` multiplies in
+8-bit floating point too, with a scale for each block of 128; `train` keeps the
+data type and runs the whole chain backward; `clip` scales the experts'
+gradients by their norm over all ranks.  The command compares them with plain
 torch on the same numbers:
 
   python examples/expert_parallel_layer.py [--ranks 4] [--rows 64] [--hidden 512] [--experts 16] [--topk 4]
@@ -34,7 +37,8 @@ HOW = dict(score="softmax", renormalize=True)
 class Layer:
     """Weights of one layer, and buffers sized for one batch shape."""
 
-    def __init__(self, N, rows, hidden, experts, topk, dtype=torch.bfloat16, seed=0):
+    def __init__(self, N, rows, hidden, experts, topk, dtype=torch.bfloat16, seed=0, library=False):
+        self.library = library
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.N, self.rows, self.H, self.E, self.k, self.dtype = N, rows, hidden, experts, topk, dtype
         self.cap = N * rows * min(topk, experts // N)  # room for every choice
@@ -62,6 +66,9 @@ class Layer:
     def experts(self, recv):
         """The experts' products on the rows each has received."""
         each, answer = self.E // self.N, torch.zeros(self.N, self.cap, self.H, **self.data)
+        if self.library:
+            vc.vc_expert_product(recv, self.up.view(self.N, each, self.H, self.H), self.offsets, answer)
+            return answer
         for d, ends in enumerate(self.offsets.tolist()):
             for i in range(each):
                 rows = slice(ends[i], ends[i + 1])
@@ -83,6 +90,33 @@ class Layer:
         vc.vc_combine(self.experts(recv), self.slots, self.out, weights=self.weights)
         return self.out
 
+    def serve8(self, partial, residual):
+        """As serve, the experts' products in 8-bit floating point."""
+        N, rows, H, each = self.N, self.rows, self.H, self.E // self.N
+        blocks, f8 = -(-H // vc.FP8_BLOCK), dict(dtype=torch.float8_e4m3fn, device="cuda")
+        up = self.up.view(N, each, H, H).transpose(2, 3).contiguous()  # a program keeps these two
+        up8, up_scale = torch.empty(N, each, H, H, **f8), torch.empty(N, each, blocks, blocks, **self.f32)
+        vc.vc_quantize_fp8(up, up8, up_scale, block_rows=vc.FP8_BLOCK)
+        y = torch.empty(N, rows, H, **self.data)
+        vc.vc_reduce_scatter_norm(partial, self.norm, y, residual=residual, residual_out=self.h)
+        self.route(y @ self.router)
+        y8, scale = torch.empty(N, rows, H, **f8), torch.empty(N, rows, blocks, **self.f32)
+        vc.vc_quantize_fp8(y, y8, scale)
+        recv8, recv_scale = torch.empty(N, self.cap, H, **f8), torch.empty(N, self.cap, blocks, **self.f32)
+        vc.vc_dispatch(y8, self.slots, recv8)
+        vc.vc_dispatch(scale, self.slots, recv_scale)  # a row's scales go where the row goes
+        answer = torch.empty(N, self.cap, H, **self.data)
+        vc.vc_expert_product_fp8(recv8, recv_scale, up8, up_scale, self.offsets, answer)
+        vc.vc_combine(answer, self.slots, self.out, weights=self.weights)
+        return self.out
+
+    def clip(self, grads, max_norm):
+        """Scales the experts' gradients, each rank holding its own experts', in
+        place where their norm over all ranks is above max_norm; the norm."""
+        each, norm = self.E // self.N, torch.empty(self.N, **self.f32)
+        vc.vc_clip_grad_norm([[grads["up"][r * each:(r + 1) * each]] for r in range(self.N)], norm, max_norm=max_norm)
+        return norm
+
     def train(self, partial, residual, dout):
         """Forward in the data type, then the gradients of
         sum(out * dout): a dict of them."""
@@ -99,7 +133,10 @@ class Layer:
         danswer, dweights = torch.zeros_like(answer), torch.empty_like(self.weights)
         vc.vc_combine_backward(dout, answer, self.slots, self.weights, drecv=danswer, dweights=dweights)
         drecv, dup = torch.zeros_like(recv), torch.zeros_like(self.up)
-        for d, ends in enumerate(self.offsets.tolist()):
+        if self.library:
+            experts = (N, each, H, H)
+            vc.vc_expert_product_backward(danswer, recv, self.up.view(experts), self.offsets, drows=drecv, dweight=dup.view(experts))
+        for d, ends in enumerate([] if self.library else self.offsets.tolist()):
             for i in range(each):
                 at, e = slice(ends[i], ends[i + 1]), d * each + i
                 drecv[d, at] = danswer[d, at] @ self.up[e].T
@@ -134,9 +171,9 @@ def distance(a, b):
     return float((a.double() - b.double()).norm() / b.double().norm())
 
 
-def compare(N=4, rows=64, hidden=512, experts=16, topk=4, dtype=torch.bfloat16):
+def compare(N=4, rows=64, hidden=512, experts=16, topk=4, dtype=torch.bfloat16, library=False):
     """Relative distances of the layer's output and gradients from plain torch."""
-    layer = Layer(N, rows, hidden, experts, topk, dtype)
+    layer = Layer(N, rows, hidden, experts, topk, dtype, library=library)
     g = torch.Generator(device="cuda").manual_seed(1)
     partial = (torch.randn(N, N * rows, hidden, generator=g, device="cuda") * N ** -0.5).to(dtype)
     residual = torch.randn(N, rows, hidden, generator=g, device="cuda").to(dtype)
@@ -152,6 +189,13 @@ def compare(N=4, rows=64, hidden=512, experts=16, topk=4, dtype=torch.bfloat16):
     (want * dout.double()).sum().backward()
     for k, v in grads.items():
         found["d" + k] = distance(v, leaves[k].grad)
+    if library:
+        out = layer.serve8(partial, residual)
+        found["serve8"] = distance(out, plain(leaves, leaves["partial"], leaves["residual"], layer.ids).detach())
+        whole = leaves["up"].grad
+        norm = layer.clip(grads, float(whole.norm()) / 2)
+        found["norm"] = float((norm.double() - whole.norm()).abs().max() / whole.norm())
+        found["clipped"] = distance(grads["up"], whole / 2)
     return found
 
 
@@ -160,5 +204,7 @@ if __name__ == "__main__":
     for name, value in (("ranks", 4), ("rows", 64), ("hidden", 512), ("experts", 16), ("topk", 4)):
         ap.add_argument("--" + name, type=int, default=value)
     a = ap.parse_args()
-    for k, v in compare(a.ranks, a.rows, a.hidden, a.experts, a.topk).items():
-        print(f"{k:10s} relative distance from plain torch {v:.2e}")
+    for library in (False, True):
+        print("products of the library" if library else "products in torch")
+        for k, v in compare(a.ranks, a.rows, a.hidden, a.experts, a.topk, library=library).items():
+            print(f"  {k:10s} relative distance from plain torch {v:.2e}")

@@ -397,7 +397,9 @@ vc_status_t vc_plan_exec_order(vc_coll_t coll, vc_algo_t algo, int nranks, size_
  *   A layer operator's launch has bit 9 set, its kernel's index in bits 0-3
  *   (0 norm, 1 norm backward, 2 the sum of its weight gradients, 3 route, 4
  *   route backward, 5 dispatch plan, 6 dispatch, 7 combine, 8 combine
- *   backward), coll -1, algo -1 and step the launch within the call.
+ *   backward, 9 expert product, 10 its weights' gradient, 11 its 8-bit form, 12
+ *   rounding to 8 bits, 13 gradients' norm, 14 clipping, 15 operands copied to
+ *   16-byte boundaries), coll -1, algo -1 and step the launch within the call.
  */
 typedef struct {
   int32_t coll;   /* vc_coll_t; -1: a layer operator */
@@ -559,7 +561,8 @@ vc_status_t vc_get_reuse_order(size_t* min_step_bytes);
  * then reads and clears the word: bit 1 set when a bulk-copy pipeline's wait
  * for a tile's load gave up (the launch then stopped issuing copies and
  * returned; its outputs are incomplete).  A large vc_dispatch moves its rows by
- * such a pipeline and reports here too.  Never set in correct operation;
+ * such a pipeline and reports here too.  Bit 2 set when a wait of an expert
+ * product gave up, likewise.  Never set in correct operation;
  * the waits are bounded so that a fault elsewhere cannot hang a launch.
  */
 vc_status_t vc_device_errors(vc_stream_t stream, uint32_t* flags);
@@ -808,7 +811,10 @@ vc_status_t vc_combine_backward(const void* const* dout, const void* const* recv
  *   max(0, min(offset, capacity)).  out[d]: capacity*out_width.
  *   nranks divides nexperts <= VC_ROUTE_MAX_EXPERTS; a width above
  *   VC_EXPERT_MAX_WIDTH is VC_ERR_UNSUPPORTED.
- * Sums are fp32.
+ * Sums are fp32.  bf16 and fp16 run on the tensor cores, whatever the widths;
+ * widths of whole 16 bytes and buffers on 16-byte boundaries run faster (other
+ * operands are first copied to scratch, a row each 16 bytes' multiple apart).
+ * A capacity above 2^31 - 2^16 is VC_ERR_INVALID_ARG.
  */
 vc_status_t vc_expert_product(const void* const* rows, const void* const* weight, const int32_t* const* offsets,
                               void* const* out, int nranks, int nexperts, size_t capacity, size_t in_width,
