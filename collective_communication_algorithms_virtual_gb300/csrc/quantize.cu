@@ -2,7 +2,9 @@
 // 128 elements, or of 128 rows by 128 (see vc.h).
 //
 // Memory bounds it: every element is read once, held in registers while its
-// block's largest magnitude is found, and written once.
+// block's largest magnitude is found, and written once.  On a GB300 (copy rate
+// 6.78 TB/s): 32768 rows of 4096 bf16, 66 us, 6.2 TB/s; 64 matrices of 2048 by
+// 4096 by tiles, 257 us, 6.3 TB/s; one to eight rows are a launch, 1.7 us.
 #include <cuda_fp8.h>
 
 #include "layer.cuh"

@@ -620,9 +620,10 @@ vc_status_t vc_reduce_scatter_noalloc(const void* const* send, void* const* recv
  * What a transformer layer does around its collectives, on the same virtual
  * ranks (no counterpart on the source pages, which stop at the collectives):
  * the norm that follows a tensor-parallel ReduceScatter, the choice of experts
- * for each token, and the exchange of tokens between the ranks that hold them
+ * for each token, the exchange of tokens between the ranks that hold them
  * and the ranks that hold the experts -- an AllToAll whose counts the choice
- * decides.  Each rank holds `rows` tokens.
+ * decides --, the experts' products on what was exchanged, and the clipping of
+ * the ranks' gradients.  Each rank holds `rows` tokens.
  *
  * The common rules above hold: host arrays with one device pointer per rank,
  * work only enqueued, errors returned, graph capture allowed, scratch from
