@@ -1225,8 +1225,20 @@ vc_status_t tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, con
   cuuint32_t box[3] = {box0, box1, 1}, one[3] = {1, 1, 1};
   for (int i = 0; i < rank; ++i) d[i] = dims[i];
   for (int i = 0; i + 1 < rank; ++i) s[i] = strides[i];
-  const CUresult r = encode(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(data), d, s, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const auto go = [&] {
+    return encode(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(data), d, s, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = go();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    // A thread's first call: unlike the runtime's calls the driver's does not
+    // make the device's context current.
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+    r = go();
+  }
   if (r != CUDA_SUCCESS) return fail(VC_ERR_CUDA, "cuTensorMapEncodeTiled: error " + std::to_string(static_cast<int>(r)));
   return VC_SUCCESS;
 }

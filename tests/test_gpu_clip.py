@@ -161,3 +161,15 @@ def test_another_stream_a_graph_and_the_same_bits():
         run()
         torch.cuda.synchronize()
         assert torch.equal(norm, want[0]) and all(torch.equal(a, b) for x, y in zip(out, want[1]) for a, b in zip(x, y))
+
+
+def test_a_tensor_beyond_32_bits_of_elements():
+    n = 2 ** 31 + 4099
+    t = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    t[-5:], t[:3], t[2 ** 31 - 1:2 ** 31 + 2] = 3.0, 4.0, 2.0
+    norm = torch.empty(1, device="cuda")
+    vc.vc_clip_grad_norm([[t]], norm, max_norm=1.0)
+    want = math.sqrt(5 * 9 + 3 * 16 + 3 * 4)
+    assert abs(float(norm[0]) - want) <= NORM * want
+    for at, v in ((n - 5, 3.0), (n - 1, 3.0), (0, 4.0), (2, 4.0), (2 ** 31 - 1, 2.0), (2 ** 31 + 1, 2.0), (2 ** 31 + 2, 0.0), (5, 0.0)):
+        assert abs(float(t[at]) - v / want) <= store_bound(v / want, "bf16") * 1.001, at

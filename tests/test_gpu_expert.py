@@ -163,6 +163,84 @@ def test_infinities_and_nan_stay_in_their_rows():
         assert torch.equal(out[0][keep], clean[0][keep])
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("win,width", [(72, 136), (71, 137)])
+def test_weights_of_experts_without_rows_do_not_matter(dt, win, width):
+    x, w, dy, off = inputs(dt, [[5, 0, 40], [0, 20, 0]], 50, win, width, False)
+    w[0][1], w[1][0], w[1][2] = float("nan"), float("inf"), float("nan")
+    out, dx = (torch.zeros(2, 50, n, dtype=DT[dt], device="cuda") for n in (width, win))
+    vc.vc_expert_product(x, w, off, out)
+    vc.vc_expert_product_backward(dy, None, w, off, drows=dx)
+    w[0][1], w[1][0], w[1][2] = 0, 0, 0
+    X, W, dY = (host(t) for t in (x, w, dy))
+    check(f64(out), *ref.product(X, W, off.cpu(), np.zeros(out.shape), False, dt), "out")
+    check(f64(dx), *ref.product(dY, W, off.cpu(), np.zeros(dx.shape), True, dt), "drows")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_beyond_32_bits_of_elements(dt):
+    """The rows stand behind the first 2^31 elements of their buffers."""
+    cap, win, width = 2 ** 20 + 300, 2048 + 8, 2048 + 16
+    first = cap - 200
+    assert first * win > 2 ** 31
+    x, dy = (torch.zeros(1, cap, n, dtype=DT[dt], device="cuda") for n in (win, width))
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x[0, first:].copy_(torch.randn(200, win, generator=g, device="cuda"))
+    dy[0, first:].copy_(torch.randn(200, width, generator=g, device="cuda"))
+    w = (torch.randn(1, 2, win, width, generator=g, device="cuda") * win ** -0.5).to(DT[dt])
+    off = torch.tensor([[first, first + 130, cap]], dtype=torch.int32, device="cuda")
+    out, dx = torch.full_like(dy, 7), torch.full_like(x, 7)
+    dw = torch.empty_like(w)
+    vc.vc_expert_product(x, w, off, out)
+    vc.vc_expert_product_backward(dy, x, w, off, drows=dx, dweight=dw)
+    tail = torch.tensor([[0, 130, 200]])
+    X, W, dY = (np.stack([f64(t)]) for t in (x[0, first:], w[0], dy[0, first:]))
+    check(f64(out[:, first:]), *ref.product(X, W, tail, np.zeros((1, 200, width)), False, dt), "out")
+    check(f64(dx[:, first:]), *ref.product(dY, W, tail, np.zeros((1, 200, win)), True, dt), "drows")
+    check(f64(dw), *ref.weight_grad(dY, X, tail, W.shape, False, dt), "dweight")
+    assert bool((out[0, :first] == 7).all()) and bool((dx[0, :first] == 7).all())
+
+
+def test_two_threads_on_two_streams():
+    """Calls of two host threads on streams of their own, 16-bit and 8-bit
+    products at once, give the bits of calls by themselves."""
+    import threading
+    x, w, dy, off = inputs("bf16", [[100, 300], [0, 77]], 400, 264, 384, False)
+    odd = inputs("f16", [[30, 9], [60, 1]], 100, 131, 77, True, seed=3)
+    f8 = [torch.randn(2, 400, 256, device="cuda").to(torch.float8_e4m3fn), torch.rand(2, 400, 2, device="cuda"),
+          torch.randn(2, 2, 384, 256, device="cuda").to(torch.float8_e4m3fn), torch.rand(2, 2, 3, 2, device="cuda"), off]
+
+    def buffers():
+        return [torch.zeros(2, 400, 384, dtype=DT["bf16"], device="cuda"), torch.zeros(2, 2, 264, 384, dtype=DT["bf16"], device="cuda"),
+                torch.zeros(2, 100, 77, dtype=DT["f16"], device="cuda"), torch.zeros(2, 400, 384, device="cuda")]
+
+    def go(b, stream=None):
+        vc.vc_expert_product(x, w, off, b[0], stream=stream)
+        vc.vc_expert_product_fp8(*f8, b[3], stream=stream)
+        vc.vc_expert_product_backward(dy, x, w, off, dweight=b[1], stream=stream)
+        vc.vc_expert_product(odd[0], odd[1], odd[3], b[2], transposed=True, stream=stream)
+    want = buffers()
+    go(want)
+    torch.cuda.synchronize()
+    got, failed = [buffers() for _ in range(2)], []
+
+    def many(b, stream):
+        try:
+            for _ in range(300):
+                go(b, stream)
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+    threads = [threading.Thread(target=many, args=(b, torch.cuda.Stream())) for b in got]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed and vc.vc_device_errors() == 0
+    for b in got:
+        assert all(torch.equal(a, c) for a, c in zip(b, want))
+
+
 def test_same_bits_again_and_on_another_stream_and_replayed():
     x, w, dy, off = inputs("bf16", [[100, 300], [0, 77]], 400, 256, 384, True)
     out, dx, dw = torch.zeros(2, 400, 384, dtype=DT["bf16"], device="cuda"), torch.zeros(2, 400, 256, dtype=DT["bf16"], device="cuda"), \

@@ -239,3 +239,24 @@ def test_dispatched_replayed_and_again():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_rows_beyond_32_bits_of_elements():
+    cap, win, width = 2 ** 20 + 100, 2048 + 128, 256
+    first = cap - 64
+    assert first * win > 2 ** 31
+    x = torch.zeros(1, cap, win, dtype=torch.bfloat16, device="cuda")
+    x[0, first:].copy_(torch.randn(64, win, device="cuda"))
+    x8, xs = torch.empty(1, cap, win, dtype=F8, device="cuda"), torch.empty(1, cap, blocks(win), device="cuda")
+    vc.vc_quantize_fp8(x, x8, xs)
+    check_quantized([x[0, first:]], [x8[0, first:]], [xs[0, first:]], 1)
+    assert bool((xs[0, :first] == 0).all())
+    w = torch.randn(1, 1, width, win, device="cuda")
+    w8, ws = torch.empty(1, 1, width, win, dtype=F8, device="cuda"), torch.empty(1, 1, blocks(width), blocks(win), device="cuda")
+    vc.vc_quantize_fp8(w, w8, ws, block_rows=128)
+    off = torch.tensor([[first, cap]], dtype=torch.int32, device="cuda")
+    out = torch.full((1, cap, width), 7.0, device="cuda")
+    vc.vc_expert_product_fp8(x8, xs, w8, ws, off, out)
+    X, W = values(x8[0, first:], xs[0, first:], 1), values(w8[0], ws[0], 128)[0]
+    bound = (win + 2 * blocks(win) + 2) * ref.ULP * (np.abs(X) @ np.abs(W).T) + store_bound(X @ W.T, "f32")
+    assert (np.abs(f64(out[0, first:]) - X @ W.T) <= bound).all() and bool((out[0, :first] == 7).all())
