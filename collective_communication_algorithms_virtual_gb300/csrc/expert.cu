@@ -46,9 +46,9 @@ struct SimpleParams {
   int experts, each;
 };
 
-// One operand's 16 by W tile of k by m (or n) to shared memory, in fp32.
+// One operand's 16 by W tile of k by m (or n) to shared memory.
 // Neighbouring threads take neighbouring elements in memory.
-template <int DT, int W>
+template <int W>
 struct SimpleTile {
   static constexpr int kEach = kSimpleK * W / kSimpleThreads;
   float v[kEach];
@@ -57,12 +57,12 @@ struct SimpleTile {
     *k = k_runs ? at % kSimpleK : at / W;
     *w = k_runs ? at / kSimpleK : at % W;
   }
-  __device__ __forceinline__ void load(const void* p, int64_t sw, int64_t sk, int ws, int ks) {
+  __device__ __forceinline__ void load(const float* p, int64_t sw, int64_t sk, int ws, int ks) {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       int k, w;
       place(i, sk == 1, &k, &w);
-      v[i] = w < ws && k < ks ? El<DT>::load(p, w * sw + k * sk) : 0.f;
+      v[i] = w < ws && k < ks ? __ldg(p + w * sw + k * sk) : 0.f;
     }
   }
   __device__ __forceinline__ void store(float (*to)[W + 4], bool k_runs) const {
@@ -75,7 +75,7 @@ struct SimpleTile {
   }
 };
 
-template <int DT, int OUT, bool WEIGHT>
+template <bool WEIGHT>
 __global__ void __launch_bounds__(kSimpleThreads, 2) product_simple_kernel(const __grid_constant__ SimpleParams p) {
   __shared__ uint32_t ends[kMaxExperts];
   __shared__ int longest;
@@ -103,20 +103,19 @@ __global__ void __launch_bounds__(kSimpleThreads, 2) product_simple_kernel(const
     const Rows r = tc::rows_of(p.offsets[d], i, p.capacity);
     const int n0 = static_cast<int>(at / across) * kSimpleN, m0 = static_cast<int>(at % across) * kSimpleM;
     const int ns = min(kSimpleN, (WEIGHT ? p.N : r.count) - n0), ms = min(kSimpleM, p.M - m0), K = WEIGHT ? r.count : p.K;
-    const int es = El<DT>::kSize;
-    const char* a = static_cast<const char*>(p.a[d]) + ((WEIGHT ? r.first * p.ak : i * p.ae) + m0 * p.am) * es;
-    const char* b = static_cast<const char*>(p.b[d]) + (r.first * (WEIGHT ? p.bk : p.bn) + n0 * p.bn) * es;
+    const float* a = static_cast<const float*>(p.a[d]) + (WEIGHT ? r.first * p.ak : i * p.ae) + m0 * p.am;
+    const float* b = static_cast<const float*>(p.b[d]) + r.first * (WEIGHT ? p.bk : p.bn) + n0 * p.bn;
     const bool ka = p.ak == 1, kb = p.bk == 1;
     float acc[4][8] = {};
-    SimpleTile<DT, kSimpleM> ta;
-    SimpleTile<DT, kSimpleN> tb;
+    SimpleTile<kSimpleM> ta;
+    SimpleTile<kSimpleN> tb;
     const int steps = (K + kSimpleK - 1) / kSimpleK;
     __syncthreads();  // the last tile's products have read shared memory
     for (int s = 0; s <= steps; ++s) {
       if (s < steps) {
         const int k0 = s * kSimpleK;
-        ta.load(a + static_cast<int64_t>(k0) * p.ak * es, p.am, p.ak, ms, K - k0);
-        tb.load(b + static_cast<int64_t>(k0) * p.bk * es, p.bn, p.bk, ns, K - k0);
+        ta.load(a + static_cast<int64_t>(k0) * p.ak, p.am, p.ak, ms, K - k0);
+        tb.load(b + static_cast<int64_t>(k0) * p.bk, p.bn, p.bk, ns, K - k0);
       }
       if (s > 0) {
         const int w = (s - 1) & 1;
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(kSimpleThreads, 2) product_simple_kernel(const
         __syncthreads();
       }
     }
-    void* out = p.out[d];
+    float* out = static_cast<float*>(p.out[d]);
     const int64_t row = WEIGHT ? static_cast<int64_t>(i) * p.N + n0 : static_cast<int64_t>(r.first) + n0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -147,7 +146,7 @@ __global__ void __launch_bounds__(kSimpleThreads, 2) product_simple_kernel(const
 #pragma unroll
       for (int l = 0; l < 8; ++l) {
         const int m = (l / 4) * 64 + tx * 4 + l % 4;
-        if (m < ms) El<OUT>::store(out, (row + n) * p.M + m0 + m, acc[j][l]);
+        if (m < ms) out[(row + n) * p.M + m0 + m] = acc[j][l];
       }
     }
   }
@@ -1021,7 +1020,7 @@ vc_status_t rows_product(DeviceState* st, int dev, const Sizes& z, const Operand
   p.experts = z.nexperts;
   p.each = z.each;
   const int64_t tiles = row_tiles(z, kSimpleN) * ((width + kSimpleM - 1) / kSimpleM);
-  constexpr auto K = product_simple_kernel<VC_FLOAT32, VC_FLOAT32, false>;
+  constexpr auto K = product_simple_kernel<false>;
   return launch<K>(dev, Shape{simple_blocks<K>(st, dev, tiles), kSimpleThreads}, stream, p, kExpertProduct, step, bytes);
 }
 
@@ -1055,7 +1054,7 @@ vc_status_t weights_gradient(DeviceState* st, int dev, const Sizes& z, const Ope
   p.experts = z.nexperts;
   p.each = z.each;
   const int64_t tiles = z.nexperts * ((N + kSimpleN - 1) / kSimpleN) * ((M + kSimpleM - 1) / kSimpleM);
-  constexpr auto K = product_simple_kernel<VC_FLOAT32, VC_FLOAT32, true>;
+  constexpr auto K = product_simple_kernel<true>;
   return launch<K>(dev, Shape{simple_blocks<K>(st, dev, tiles), kSimpleThreads}, stream, p, kExpertWeight, step, bytes);
 }
 
