@@ -16,9 +16,9 @@ namespace {
 
 constexpr int kClipThreads = 256, kClipUnits = 8;
 // Blocks of a multiprocessor, by their registers.  24 layers' 2.4 GB, eight
-// ranks: the norm 400 us with 4 and 419 with 3 (what its loads need), clipping
-// 749 with 3 and 860 with 4 (which spills).
-constexpr int kNormBlocks = 4, kClipBlocks = 3;
+// ranks: clipping 749 us with 3 and 860 with 4 (which spills); the norm has 4
+// (400 us, and 419 with 3).
+constexpr int kClipBlocks = 3;
 constexpr int64_t kChunkBytes = int64_t(kClipThreads) * kClipUnits * 16;  // of one tensor, at most, at a time
 
 struct Tensor {
@@ -129,8 +129,72 @@ __device__ __forceinline__ void units(const Chunk& x, B&& between, F&& f) {
   }
 }
 
+// The sum of a thread's squares in a chunk.  Up to 64 are added in fp32, whose
+// numbers end at 2^128 and lose bits below 2^-126: within [kLow, kHigh] what a
+// sum has lost is below 2^-34 of it.  Elsewhere they are added again, of the
+// elements times a power of two:
+//   below 2^-110 every element is below 2^-55, and the squares of 2^100 times
+//   them lie between 2^-98 (2^-149 is the smallest number) and 2^90;
+//   above 2^100 (or infinite, or NaN) one element is above 2^46; the squares of
+//   2^-76 times them lie below 2^104, and what is lost of those below 2^-126
+//   is nothing next to the largest, above 2^-60.
+// fp16's squares are within 2^-48 and 2^32.  The loaded units are kept for that,
+// which is why this has a loop of its own.
+constexpr float kLow = 0x1p-110f, kHigh = 0x1p100f;
+template <int DT, bool VEC, class B>
+__device__ __forceinline__ double squares(const Chunk& x, B&& between) {
+  using E = El<DT>;
+  constexpr int kN = VEC ? kClipUnits : kClipUnits / 2;  // as in units()
+  const int units = static_cast<int>((x.n + E::kVec - 1) / E::kVec);
+  const Row<E::kSize, VEC> row(x.g, units, Bytes{x.t->g, x.t->g + x.t->n * E::kSize});
+  double sum = 0;
+#pragma unroll
+  for (int i0 = 0; i0 < kClipUnits; i0 += kN) {
+    typename Row<E::kSize, VEC>::Raw raw[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int c = (i0 + i) * kClipThreads + threadIdx.x;
+      raw[i] = c < units ? row.load_plain(c) : row.zero();
+    }
+    if (i0 == 0) between();
+    const auto add = [&](float by) {
+      float s[4] = {};
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const int c = (i0 + i) * kClipThreads + threadIdx.x;
+        if ((c & ~31) >= units) break;
+        float v[E::kVec] = {};
+        if (c < units) {
+          E::widen(row.finish(raw[i], c, x.n), v);
+          mask_unit<E::kSize, VEC>(c, x.n, v);
+        }
+#pragma unroll
+        for (int k = 0; k < E::kVec; ++k) s[k % 4] = fmaf(v[k] * by, v[k] * by, s[k % 4]);
+      }
+      return (s[0] + s[1]) + (s[2] + s[3]);
+    };
+    const float all = add(1.f);
+    if (DT == VC_FLOAT16 || (all >= kLow && all <= kHigh)) {
+      sum += all;
+      continue;
+    }
+    if constexpr (VEC) {  // zeros are common: 2.4 GB of them take 405 us so, 609 added again
+      constexpr uint32_t kMagnitude = E::kSize == 4 ? 0x7fffffff : 0x7fff7fff;
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) any |= raw[i].x | raw[i].y | raw[i].z | raw[i].w;
+      if ((any & kMagnitude) == 0) continue;
+    }
+    sum += add(all < kLow ? 0x1p100f : 0x1p-76f) * (all < kLow ? 0x1p-200 : 0x1p152);
+  }
+  return sum;
+}
+
+// 56 registers: four blocks leave room for the clipping's first block as soon as
+// one of them ends.  With 62 the same two kernels took 1186 us instead of 1161
+// (2.4 GB of bf16), the norm alone as long (fp32: 351 for 341).
 template <class P>
-__global__ void __launch_bounds__(kClipThreads, kNormBlocks) grad_norm_kernel(const __grid_constant__ P p) {
+__global__ void __maxnreg__(56) grad_norm_kernel(const __grid_constant__ P p) {
   __shared__ double part[kClipThreads / 32];
   stream_order();
   const int rank = blockIdx.y;
@@ -143,14 +207,7 @@ __global__ void __launch_bounds__(kClipThreads, kNormBlocks) grad_norm_kernel(co
     by_dtype(x.dtype, [&](auto code) {
       constexpr int DT = decltype(code)::value;
       const auto go = [&](auto vec) {
-        float s[4] = {};
-        units<DT, decltype(vec)::value>(
-            x, [&] { if (c + gridDim.x < total) next = chunk_at(p, rank, c + gridDim.x); },
-            [&](int, const float* v) {
-#pragma unroll
-              for (int k = 0; k < El<DT>::kVec; ++k) s[k % 4] = fmaf(v[k], v[k], s[k % 4]);
-            });
-        sum += (s[0] + s[1]) + (s[2] + s[3]);
+        sum += squares<DT, decltype(vec)::value>(x, [&] { if (c + gridDim.x < total) next = chunk_at(p, rank, c + gridDim.x); });
       };
       const bool whole = reinterpret_cast<uintptr_t>(x.g) % 16 == 0 && x.n % El<DT>::kVec == 0;
       whole ? go(std::true_type{}) : go(std::false_type{});

@@ -891,9 +891,10 @@ vc_status_t vc_expert_product_fp8(const void* const* rows, const float* const* r
  *             ranks' with `across`: shards of one model)
  *   out = g where norm <= max_norm, else g * (max_norm / norm), both factors
  *         fp32, rounded once to the tensor's type.
- * Squares and the sums of 64 of them are fp32 (a gradient above 1.8e19 gives an
- * infinite norm), sums of those 64 bits.  An infinite norm scales by 0, a NaN one
- * by NaN.
+ * Squares and the sums of up to 64 of them are rounded to fp32's 24 bits,
+ * whatever their size (gradients of 1e-45 count like those of 1e38), sums of
+ * those are 64 bits.  A norm above the largest fp32 number is infinite.  An
+ * infinite norm scales by 0, a NaN one by NaN.
  *   out: NULL for the norm alone (max_norm is not looked at).  out[j] ==
  *   grads[j] is allowed; a tensor is then not touched where norm <= max_norm.
  *   max_norm: >= 0, infinity included, rounded to fp32; else
