@@ -38,6 +38,12 @@ __device__ __forceinline__ void bar_expect_there(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive_there(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// The same for what this block has written itself and the other one will read,
+// which the default scope (this block) does not cover; with a wait of CLUSTER at
+// the other end.
+__device__ __forceinline__ void bar_release_there(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ uint32_t rank_in_cluster() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -47,12 +53,21 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// CLUSTER: what other blocks of the cluster have written before their arrival is
+// there too.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok)
-               : "r"(bar), "r"(parity)
-               : "memory");
+  if constexpr (CLUSTER)
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
   return ok != 0;
 }
 // Polls with test_wait, which never blocks.  `gone` (shared memory) is set by
@@ -61,9 +76,10 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
 // accumulator end within microseconds: kSoon is some 0.3 s.  A whole product
 // may have 2^25 steps: kLate is some 20 s.
 constexpr uint32_t kSoon = 1u << 22, kLate = 1u << 28;
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gone, uint32_t limit = kSoon) {
   for (uint32_t it = 0; it < limit; ++it) {
-    if (bar_test(bar, parity)) return true;
+    if (bar_test<CLUSTER>(bar, parity)) return true;
     if (it >= 256) {
       if (*gone) return false;
       __nanosleep(64);
