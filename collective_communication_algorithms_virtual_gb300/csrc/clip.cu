@@ -29,11 +29,11 @@ struct Tensor {
 // What both sizes of table have.
 struct ClipCall {
   uint16_t first[VC_MAX_RANKS + 1];  // of a rank's tensors
-  double* part;          // [launch][rank][block]
+  double* part;          // [rank][block], of the launches so far
   float* norm[VC_MAX_RANKS];
   float max_norm;
-  uint32_t blocks;       // parts of a rank and launch
-  uint32_t launches, at;
+  uint32_t blocks;       // parts of a rank
+  uint32_t at;           // launch
   bool across;
 };
 // The tensors of one launch.  A call of few copies a small table.
@@ -200,6 +200,7 @@ __global__ void __maxnreg__(56) grad_norm_kernel(const __grid_constant__ P p) {
   const int rank = blockIdx.y;
   const uint32_t total = chunks_of(p, rank);
   double sum = 0;
+  if (p.at != 0 && threadIdx.x == 0) sum = __ldcg(p.part + static_cast<int64_t>(rank) * p.blocks + blockIdx.x);  // the last launch's
   Chunk x, next{};
   if (blockIdx.x < total) next = chunk_at(p, rank, blockIdx.x);
   for (uint32_t c = blockIdx.x; c < total; c += gridDim.x) {
@@ -214,15 +215,15 @@ __global__ void __maxnreg__(56) grad_norm_kernel(const __grid_constant__ P p) {
     });
   }
   sum = block_sum(sum, part);
-  if (threadIdx.x == 0) p.part[(static_cast<int64_t>(p.at) * gridDim.y + rank) * p.blocks + blockIdx.x] = sum;
+  if (threadIdx.x == 0) p.part[static_cast<int64_t>(rank) * p.blocks + blockIdx.x] = sum;
 }
 
-// The norm that rank `rank` goes by, from every block's part.
+// The norm that rank `rank` goes by, from every block's part, however many
+// launches there were: each block of each clipping launch adds them up.
 __device__ __forceinline__ float norm_of(const ClipCall& p, int rank, int ranks, double* part) {
   double sum = 0;
-  const int64_t all = static_cast<int64_t>(p.launches) * ranks * p.blocks;
-  for (int64_t i = threadIdx.x; i < all; i += kClipThreads)
-    if (p.across || static_cast<int>(i / p.blocks % ranks) == rank) sum += __ldcg(p.part + i);
+  const uint32_t first = p.across ? 0 : rank * p.blocks, last = p.across ? ranks * p.blocks : first + p.blocks;
+  for (uint32_t i = first + threadIdx.x; i < last; i += kClipThreads) sum += __ldcg(p.part + i);
   return static_cast<float>(sqrt(block_sum(sum, part)));
 }
 
@@ -360,7 +361,7 @@ vc_status_t clip_with(const void* const* g, void* const* out, const size_t* coun
   rc = scratch_pool(st, dev, &pool);
   if (rc != VC_SUCCESS) return rc;
   double* part = nullptr;
-  const size_t need = sizeof(double) * launches * nranks * blocks;
+  const size_t need = sizeof(double) * nranks * blocks;
   cudaError_t e = cudaMallocFromPoolAsync(reinterpret_cast<void**>(&part), need, pool, stream);
   if (e == cudaErrorMemoryAllocation) {
     cudaGetLastError();
@@ -374,7 +375,6 @@ vc_status_t clip_with(const void* const* g, void* const* out, const size_t* coun
     std::copy(norm, norm + nranks, p.norm);
     p.part = part;
     p.blocks = blocks;
-    p.launches = launches;
     p.at = i;
     p.across = across != 0;
     p.max_norm = static_cast<float>(max_norm);

@@ -81,3 +81,32 @@ def test_infinity_and_nan_among_small_numbers():
             norm = torch.empty(1, device="cuda")
             vc.vc_clip_grad_norm([[t]], norm)
             assert math.isnan(norm[0]) if math.isnan(bad) else norm[0] == math.inf
+
+
+@pytest.mark.parametrize("across", [True, False])
+@pytest.mark.parametrize("N,T", [(1, 5000), (64, 100), (3, 2500)])
+def test_many_tables(N, T, across):
+    """Tables of some hundred tensors each, one launch's blocks after another's
+    adding to the same parts."""
+    grads = gradients([1 + i % 41 + 3 * N for i in range(T)], ["bf16" if i % 5 else "f32" for i in range(T)], N)
+    clipped(grads, across)
+    first, again = (torch.empty(N, device="cuda") for _ in range(2))
+    for norm in (first, again):
+        vc.vc_clip_grad_norm(grads, norm, across=across)
+    assert torch.equal(first, again)
+
+
+def test_parts_do_not_grow_with_the_tables():
+    """What each block of each launch adds up for the norm: as many bytes for
+    eight tables of the largest tensors as for one."""
+    read = []
+    for T in (700, 6000):
+        grads = [[torch.ones(40, device="cuda")] * T for _ in range(2)]  # the norm alone: one tensor may stand for many
+        norm = torch.empty(2, device="cuda")
+        vc.vc_trace_enable(True)
+        vc.vc_clip_grad_norm(grads, norm)
+        records = vc.vc_trace_read()
+        vc.vc_trace_enable(False)
+        read.append(records[-1]["bytes"])
+        assert [r["step"] for r in records] == list(range(len(records))) and abs(float(norm[0]) - (80 * T) ** 0.5) < 1e-3
+    assert read[0] == read[1] > 0
