@@ -749,35 +749,57 @@ def vc_clip_grad_norm(grads, norm, max_norm=None, out=None, across: bool = True,
     else gradients above it are scaled to it, in place or into ``out[r]``."""
     torch = _torch()
     N, T = len(grads), len(_first(grads, "grads"))
-    mine = list(itertools.chain.from_iterable(grads))
     like = _first(norm, "norm") if norm.__class__ in _SEQUENCES else norm
     dev = like.get_device()
     if dev < 0:
         raise _invalid(f"tensors must be on a CUDA device, not {like.device}")
     if max_norm is None and out is not None:
         raise _invalid("out wants a max_norm")
+    ptrs, outs, sizes, codes = _lists().pack(grads, out, dev) or _gradients(grads, out, N, T, dev)
+    check(lib().vc_clip_grad_norm(
+        ptrs, None if max_norm is None else ptrs if out is None else outs, sizes, codes, N, T,
+        _ptrs(norm, "norm", (N,), 4, torch.float32, dev), 0.0 if max_norm is None else max_norm, bool(across),
+        _stream_handle(stream, like)))
+
+
+_lists_module = None
+
+
+def _lists():
+    """The compiled part of this binding (csrc/lists.cpp)."""
+    global _lists_module
+    if _lists_module is None:
+        version = str(_torch().__version__).split("+")[0]
+        try:
+            from . import _lists as module
+        except ImportError as e:
+            raise RuntimeError(f"_lists.so is not built; run __graft_entry__.build() ({e})") from None
+        if module.torch != version:
+            raise RuntimeError(f"_lists.so is built for PyTorch {module.torch}, not {version}; build again")
+        _lists_module = module
+    return _lists_module
+
+
+def _gradients(grads, out, N: int, T: int, dev: int) -> tuple:
+    """What _lists.pack returns, for lists that it left alone: sequences and
+    tensors that are not plain ones, or that the call refuses."""
+    Tensor = _torch().Tensor
+    mine = list(itertools.chain.from_iterable(grads))
     to = mine if out is None else list(itertools.chain.from_iterable(out))
     if set(map(len, grads)) != {T} or (to is not mine and (len(out) != N or set(map(len, out)) != {T})):
         raise _invalid("grads, out: want the same number of tensors on every rank")
-    Tensor = torch.Tensor
     sizes = list(map(Tensor.numel, mine))
     types = list(map(_dtype_of, mine[:T]))
     if CHECK_TENSORS:
         for ts in (mine, to)[:1 if to is mine else 2]:
-            if list(map(_dtype_of, ts)) != types * N or not set(map(Tensor.get_device, ts)) <= {dev} or \
-                    not all(map(Tensor.is_contiguous, ts)) or (ts is to and list(map(Tensor.numel, ts)) != sizes):
-                for t, dt, n in zip(ts, types * N, sizes):
-                    if t.dtype is not dt or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
-                        raise _invalid(f"gradients: want contiguous {n} of {dt} on cuda:{dev}, not {tuple(t.shape)} {t.dtype} on "
-                                       f"{t.device}" + ("" if t.is_contiguous() else " (not contiguous)"))
+            for t, dt, n in zip(ts, types * N, sizes):
+                if t.dtype is not dt or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+                    raise _invalid(f"gradients: want contiguous {n} of {dt} on cuda:{dev}, not {tuple(t.shape)} {t.dtype} on "
+                                   f"{t.device}" + ("" if t.is_contiguous() else " (not contiguous)"))
     code = {dt: _dtype_code(t) for dt, t in zip(types, mine)}
-    M = N * T
-    ptrs = struct.pack(f"={M}Q", *map(Tensor.data_ptr, mine))
-    where = None if max_norm is None else ptrs if to is mine else struct.pack(f"={M}Q", *map(Tensor.data_ptr, to))
-    check(lib().vc_clip_grad_norm(
-        ptrs, where, struct.pack(f"={M}Q", *sizes), struct.pack(f"={T}i", *[code[dt] for dt in types]), N, T,
-        _ptrs(norm, "norm", (N,), 4, torch.float32, dev), 0.0 if max_norm is None else max_norm, bool(across),
-        _stream_handle(stream, like)))
+    pack = struct.Struct(f"={N * T}Q").pack
+    return (pack(*map(Tensor.data_ptr, mine)), None if out is None else pack(*map(Tensor.data_ptr, to)), pack(*sizes),
+            struct.pack(f"={T}i", *[code[dt] for dt in types]))
 
 
 def vc_busbw_factor(coll, nranks: int) -> float:
