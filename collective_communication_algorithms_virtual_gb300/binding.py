@@ -668,7 +668,7 @@ def vc_expert_product_backward(dout, rows, weight, offsets, drows=None, dweight=
     each = _experts(offsets, N, "experts")
     every, n = (N, each, width, win) if transposed else (N, each, win, width), each * win * width
     wdt = dt
-    if dweight is not None and (dweight[0] if dweight.__class__ in _SEQUENCES else dweight).dtype is torch.float32:
+    if dweight is not None and (_first(dweight, "dweight") if dweight.__class__ in _SEQUENCES else dweight).dtype is torch.float32:
         wdt = torch.float32
     check(lib().vc_expert_product_backward(
         _ptrs(dout, "dout", row, cap * width * es, dt, dev),
@@ -748,7 +748,12 @@ def vc_clip_grad_norm(grads, norm, max_norm=None, out=None, across: bool = True,
     model), without over each rank's own.  ``max_norm`` None: the norm alone;
     else gradients above it are scaled to it, in place or into ``out[r]``."""
     torch = _torch()
-    N, T = len(grads), len(_first(grads, "grads"))
+    if grads.__class__ not in _SEQUENCES:
+        raise _invalid("grads: want a list of each rank's tensors")
+    try:
+        N, T = len(grads), len(_first(grads, "grads"))
+    except TypeError:
+        raise _invalid("grads: want a list of each rank's tensors") from None
     like = _first(norm, "norm") if norm.__class__ in _SEQUENCES else norm
     dev = like.get_device()
     if dev < 0:
@@ -784,10 +789,17 @@ def _gradients(grads, out, N: int, T: int, dev: int) -> tuple:
     """What _lists.pack returns, for lists that it left alone: sequences and
     tensors that are not plain ones, or that the call refuses."""
     Tensor = _torch().Tensor
-    mine = list(itertools.chain.from_iterable(grads))
-    to = mine if out is None else list(itertools.chain.from_iterable(out))
-    if set(map(len, grads)) != {T} or (to is not mine and (len(out) != N or set(map(len, out)) != {T})):
+    try:
+        mine = list(itertools.chain.from_iterable(grads))
+        to = mine if out is None else list(itertools.chain.from_iterable(out))
+        same = set(map(len, grads)) == {T} and (out is None or (len(out) == N and set(map(len, out)) == {T}))
+    except TypeError:
+        raise _invalid("grads, out: want a list of each rank's tensors") from None
+    if not same:
         raise _invalid("grads, out: want the same number of tensors on every rank")
+    for t in mine if out is None else mine + to:
+        if not isinstance(t, Tensor):
+            raise _invalid(f"grads, out: want tensors, not {type(t).__name__}")
     sizes = list(map(Tensor.numel, mine))
     types = list(map(_dtype_of, mine[:T]))
     if CHECK_TENSORS:
