@@ -148,6 +148,8 @@ def lib() -> ctypes.CDLL:
         L.vc_device_errors.restype = I
         L.vc_copy_selftest.argtypes = [V, ctypes.POINTER(ctypes.c_uint32)]
         L.vc_copy_selftest.restype = I
+        L.vc_product_selftest.argtypes = [V, ctypes.POINTER(ctypes.c_uint32)]
+        L.vc_product_selftest.restype = I
         L.vc_set_single_launch.argtypes = [Z]
         L.vc_set_single_launch.restype = I
         L.vc_get_single_launch.argtypes = [ctypes.POINTER(Z)]
@@ -937,6 +939,14 @@ def vc_copy_selftest(stream=None) -> int:
     v = ctypes.c_uint32(0)
     s = None if stream is None else (stream if isinstance(stream, int) else int(stream.cuda_stream))
     check(lib().vc_copy_selftest(s, ctypes.byref(v)))
+    return v.value
+
+
+def vc_product_selftest(stream=None) -> int:
+    """Error word left by a launch in which a wait as the expert products' runs out."""
+    v = ctypes.c_uint32(0)
+    s = None if stream is None else (stream if isinstance(stream, int) else int(stream.cuda_stream))
+    check(lib().vc_product_selftest(s, ctypes.byref(v)))
     return v.value
 
 

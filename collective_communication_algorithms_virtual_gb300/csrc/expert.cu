@@ -753,6 +753,34 @@ __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_c
   if (gone && threadIdx.x == 0) atomicOr(&dev::g_device_error, 4u);
 }
 
+// -- a drill of the products' waits ------------------------------------------------
+// As in the products, with nothing in flight: one thread waits for what never
+// comes and gives up, which ends the wait of a whole warp; a wait for what has
+// come goes on.  kDrill polls are less than a millisecond.
+constexpr uint32_t kDrill = 1u << 12;
+__global__ void __launch_bounds__(96) wait_drill_kernel() {
+  __shared__ __align__(8) uint64_t bars[3];
+  __shared__ uint32_t gone;
+  const uint32_t never = tc::smem_addr(bars), late = never + 8, there = late + 8;
+  const int warp = threadIdx.x / 32;
+  stream_order();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 3; ++i) tc::bar_init(never + 8 * i, 1);
+    gone = 0;
+    tc::bar_arrive(there);
+  }
+  __syncthreads();
+  bool as_it_should = true;
+  if (warp == 0) {
+    if (tc::elect()) as_it_should = !tc::bar_wait(never, 0, &gone, kDrill) && gone;
+  } else if (warp == 1) {
+    as_it_should = !tc::warp_wait(late, 0, &gone);
+  } else {
+    as_it_should = tc::warp_wait(there, 0, &gone) && tc::bar_wait<true>(there, 0, &gone);
+  }
+  if (__syncthreads_and(as_it_should) && gone && threadIdx.x == 0) atomicOr(&dev::g_device_error, 4u);
+}
+
 // -- operands off 16-byte boundaries --------------------------------------------
 // Tensor maps want them, so such rows are copied to scratch first, a row each
 // 16 bytes' multiple apart: the rows that the experts have, the weights of
@@ -1210,6 +1238,29 @@ cudaError_t take_product_errors(cudaStream_t stream, uint32_t* flags) {
   return e;
 }
 
+namespace {
+vc_status_t wait_drill(cudaStream_t stream, uint32_t* flags) {
+  if (!flags) return fail(VC_ERR_INVALID_ARG, "null output pointer");
+  *flags = 0;
+  DeviceState* st = nullptr;
+  int dev = 0;
+  vc_status_t rc = device_state(&st, &dev);
+  if (rc != VC_SUCCESS) return rc;
+  uint32_t before = 0;
+  cudaError_t e = take_product_errors(stream, &before);
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(96);
+    cfg.stream = stream;
+    e = cudaLaunchKernelEx(&cfg, wait_drill_kernel);
+  }
+  if (e == cudaSuccess) e = take_product_errors(stream, flags);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  return e == cudaSuccess ? VC_SUCCESS : cuda_fail(e, "the waits' drill");
+}
+}  // namespace
+
 namespace tc {
 vc_status_t tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* data, const uint64_t* dims,
                        const uint64_t* strides, uint32_t box0, uint32_t box1) {
@@ -1262,6 +1313,10 @@ VC_EXPORT vc_status_t vc_expert_product(const void* const* rows, const void* con
     return layer::product(rows, weight, offsets, out, nranks, nexperts, capacity, in_width, out_width, transposed, dtype,
                           reinterpret_cast<cudaStream_t>(stream));
   });
+}
+
+VC_EXPORT vc_status_t vc_product_selftest(vc_stream_t stream, uint32_t* flags) {
+  return entry([&] { return layer::wait_drill(reinterpret_cast<cudaStream_t>(stream), flags); });
 }
 
 VC_EXPORT vc_status_t vc_expert_product_backward(const void* const* dout, const void* const* rows,

@@ -575,6 +575,13 @@ vc_status_t vc_device_errors(vc_stream_t stream, uint32_t* flags);
  * 128 KB of device memory and waits for `stream`. */
 vc_status_t vc_copy_selftest(vc_stream_t stream, uint32_t* flags);
 
+/* The same for the expert products' waits, in a launch of one block with
+ * nothing in flight: one wait runs out (within a millisecond) and ends another,
+ * a third is for what is there.  *flags receives the expert products' part of
+ * the error word (bit 2 set where all three did so), which is cleared before and
+ * after.  Waits for `stream`. */
+vc_status_t vc_product_selftest(vc_stream_t stream, uint32_t* flags);
+
 /*
  * Ring ReduceScatter that allocates no device memory.
  *

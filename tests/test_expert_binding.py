@@ -48,3 +48,7 @@ def test_ranks_of_tuples_are_lists(recorded, monkeypatch, check):  # noqa: F811
     monkeypatch.setattr(vc.binding, "CHECK_TENSORS", check)
     vc.vc_clip_grad_norm(((on0(4), on0(2)),), on0(1), max_norm=1.0, out=((on0(4), on0(2)),))
     assert recorded[-1][1][4:6] == (1, 2)
+
+
+def test_the_drill_wants_somewhere_to_write():
+    assert vc.lib().vc_product_selftest(None, None) == INVALID

@@ -1,5 +1,7 @@
 """Edges of the experts' products that tests/test_gpu_expert.py does not reach,
 within the same bounds."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -37,4 +39,22 @@ def test_the_rows_behind_an_expert_are_nan(dt, wide):
     for _ in range(100):
         vc.vc_expert_product_backward(dy, x, w, off, dweight=dw)
         assert all(torch.equal(a[::2], b[::2]) for a, b in zip(first, dw))
+    assert vc.vc_device_errors() == 0
+
+
+def test_a_wait_that_runs_out_ends_the_others_and_is_reported():
+    """The way out of the products' waits, in a launch with nothing in flight.
+    The wait that is ended would run out by itself after some 0.3 s."""
+    assert vc.vc_device_errors() == 0
+    assert vc.vc_product_selftest() == 4  # the first launch loads the kernel
+    begin = time.perf_counter()
+    assert vc.vc_product_selftest() == 4
+    assert time.perf_counter() - begin < 0.1
+    side = torch.cuda.Stream()
+    assert vc.vc_product_selftest(side) == 4 and vc.vc_device_errors() == 0
+    x, w, _, off = inputs("bf16", [[40, 30]], 80, 72, 64, False)
+    out = torch.zeros(1, 80, 64, dtype=DT["bf16"], device="cuda")
+    vc.vc_expert_product(x, w, off, out)
+    X, W = host(x), host(w)
+    check(f64(out), *ref.product(X, W, off.cpu(), np.zeros(out.shape), False, "bf16"), "out")
     assert vc.vc_device_errors() == 0
