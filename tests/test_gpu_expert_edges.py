@@ -10,7 +10,8 @@ import collective_communication_algorithms_virtual_gb300 as vc
 
 from . import expert_ref as ref
 from .layer_ref import DT, f64
-from .test_gpu_expert import check, gpu, host, inputs, offsets_of  # noqa: F401
+from .test_gpu_expert import check, gpu, host, inputs  # noqa: F401
+from .test_gpu_fp8 import blocks, values
 
 pytestmark = pytest.mark.gpu
 
@@ -57,4 +58,63 @@ def test_a_wait_that_runs_out_ends_the_others_and_is_reported():
     vc.vc_expert_product(x, w, off, out)
     X, W = host(x), host(w)
     check(f64(out), *ref.product(X, W, off.cpu(), np.zeros(out.shape), False, "bf16"), "out")
+    assert vc.vc_device_errors() == 0
+
+
+OUTSIDE = [[[-5, 4, 400]], [[3, 2, 6]], [[0, 300, 300]], [[2 ** 31 - 1, -2 ** 31, 5]], [[60, -1, 70]], [[9, 9, 2]]]
+
+
+@pytest.mark.parametrize("ends", OUTSIDE)
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("win,width", [(64, 72), (61, 67)])
+def test_offsets_outside_the_buffer_all_outputs(dt, ends, win, width):
+    """Taken into [0, capacity]; an end before its beginning is an expert of no
+    rows, so that no row has two.  Widths off 16-byte boundaries are copied by
+    the same offsets."""
+    x, w, dy, _ = inputs(dt, [[4, 4]], 70, win, width, True)
+    off = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    out, dx = (torch.full((1, 70, n), 7.0, dtype=DT[dt], device="cuda") for n in (width, win))
+    dw = torch.full((1, 2, width, win), float("nan"), dtype=DT[dt], device="cuda")
+    vc.vc_expert_product(x, w, off, out, transposed=True)
+    vc.vc_expert_product_backward(dy, x, w, off, drows=dx, dweight=dw, transposed=True)
+    X, W, dY = (host(t) for t in (x, w, dy))
+    check(f64(out), *ref.product(X, W, off.cpu(), np.full(out.shape, 7.0), True, dt), "out")
+    check(f64(dx), *ref.product(dY, W, off.cpu(), np.full(dx.shape, 7.0), False, dt), "drows")
+    check(f64(dw), *ref.weight_grad(dY, X, off.cpu(), W.shape, True, dt), "dweight")
+
+
+def rounded(x, B):
+    """x (.., rows, width) in 8 bits by the library."""
+    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device="cuda")
+    s = torch.empty(*x.shape[:-2], -(-x.shape[-2] // B), blocks(x.shape[-1]), device="cuda")
+    vc.vc_quantize_fp8(x, q, s, block_rows=B)
+    return q, s
+
+
+@pytest.mark.parametrize("ends", OUTSIDE)
+@pytest.mark.parametrize("win,width", [(256, 144), (130, 67)])
+def test_8_bit_offsets_outside_the_buffer(ends, win, width):
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x8, xs = rounded(torch.randn(1, 70, win, generator=g, device="cuda"), 1)
+    w8, ws = rounded(torch.randn(1, 2, width, win, generator=g, device="cuda"), 128)
+    off, out = torch.tensor(ends, dtype=torch.int32, device="cuda"), torch.full((1, 70, width), 7.0, device="cuda")
+    vc.vc_expert_product_fp8(x8, xs, w8, ws, off, out)
+    X, W = values(x8, xs, 1), values(w8, ws, 128)
+    want, bound = ref.product(X, W, off.cpu(), np.full(out.shape, 7.0), True, "f32")
+    size, _ = ref.product(np.abs(X), np.abs(W), off.cpu(), np.zeros(out.shape), True, "f32")
+    # a block's scale is rounded once, its sums are added by one rounding each
+    check(f64(out), want, bound + (2 * blocks(win) + 1) * ref.ULP * size, "out")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+def test_8_bit_products_over_nothing(dt):
+    """in_width 0: the experts' rows are 0, the others stay."""
+    f8 = torch.float8_e4m3fn
+    x8, w8 = torch.empty(2, 200, 0, dtype=f8, device="cuda"), torch.empty(2, 2, 264, 0, dtype=f8, device="cuda")
+    xs, ws = torch.empty(2, 200, 0, device="cuda"), torch.empty(2, 2, 3, 0, device="cuda")
+    off = torch.tensor([[0, 3, 150], [7, 7, 8]], dtype=torch.int32, device="cuda")
+    out = torch.full((2, 200, 264), 7.0, dtype=DT[dt], device="cuda")
+    vc.vc_expert_product_fp8(x8, xs, w8, ws, off, out)
+    assert bool((out[0, :150] == 0).all()) and bool((out[0, 150:] == 7).all())
+    assert bool((out[1, 7] == 0).all()) and bool((out[1, :7] == 7).all()) and bool((out[1, 8:] == 7).all())
     assert vc.vc_device_errors() == 0
