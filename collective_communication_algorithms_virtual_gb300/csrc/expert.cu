@@ -10,7 +10,8 @@
 //                                    (400 us under the power limit, 1.37)
 //   8-bit, 128 rows                                        73 us, 6.4 TB/s
 //   8-bit, 32768 rows                                     291 us, 1.89 PFLOP/s
-//   32 experts of 2048 by 4096, 16384 rows, both gradients 392 us, 1.40 PFLOP/s
+//   32 experts of 2048 by 4096, 16384 rows, both gradients 406 us, 1.35 PFLOP/s
+//                          (the weights' part 228 us; to fp32 277)
 //   one expert, 8192 x 8192 x 8192: 615 us bf16 (1.79), 470 us 8-bit (2.34)
 #include "tc.cuh"
 
@@ -28,10 +29,10 @@ constexpr size_t kMaxCapacity = 0x7fff0000;  // a tile past the last row still h
 // ---------------------------------------------------------------------------
 // out(n, m) = sum over k of b(n, k) * a(m, k) in tiles of 64 n by 128 m, 16 of
 // k at a time; 256 threads with 4 n by 8 m each: 32 products for 48 bytes from
-// shared memory (4 ranks, 8192 rows, 16 experts of 4096 by 2048: 9.1 ms, 30
-// TFLOP/s).  (The tensor cores have no fp32
-// products; splitting each factor in three bf16 parts would take six of theirs
-// and three times the bytes.)
+// shared memory (16 experts of 4096 by 2048: 16384 rows in all 9.1 ms, 30
+// TFLOP/s; 8192 rows 4.8 ms, 29).  (The tensor cores have no fp32 products;
+// splitting each factor in three bf16 parts would take six of theirs and three
+// times the bytes.)
 //   rows' products: n is a row of the expert, m of its outputs, a its weights.
 //   weights' gradients: k is a row, n and m run over the weights.
 constexpr int kSimpleM = 128, kSimpleN = 64, kSimpleK = 16, kSimpleThreads = 256;
@@ -508,9 +509,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
 // block's products, summed in tensor memory).  Each block's sums go to one of
 // two accumulators in turn; eight warps take them from there, scaled, into
 // registers, while the products of the next block go to the other one.  The
-// rows stand on the m side here, so that a thread has one row's scale: with
-// rows on the n side every sum would want its own from shared memory, more
-// reads than products.
+// rows stand on the m side here, so that a thread has one row's scale, in a
+// register.  (With rows on the n side it would take its columns' scales from
+// shared memory, four to a read; that was not measured.)
 //   warp 0 loads, warp 1 issues the products, warps 4 to 11 scale and store;
 // these hold 128 sums a thread and take the registers that the first four warps
 // give up (launched with 168 each: 4 x 40 + 8 x 232 = 12 x 168).
@@ -589,7 +590,8 @@ __device__ __forceinline__ void store_sums(const float (&acc)[128], uint32_t roo
 // A tile is 128 rows by 256 outputs.  (Pairs of blocks with 256 rows, each
 // loading half of the weights, measured 321 us against 310 at the prefill of
 // 32768 rows, 4096 by 2048, and 103 against 74 with a few rows an expert: a
-// pair's products take as long for 32 rows as for 256.)
+// pair's products take as long for 32 rows as for 256.  That was before the sums
+// were taken 16 at a time, which brought the 310 to 291.)
 template <int OUT, int R>
 __global__ void __launch_bounds__(kTc8Threads, 1) product8_kernel(const __grid_constant__ Product8Params<R> p) {
   extern __shared__ unsigned char dynamic[];

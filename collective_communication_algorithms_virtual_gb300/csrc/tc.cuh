@@ -1,6 +1,6 @@
-// What the tensor-core kernels (expert.cu, expert8.cu) share: bounded waits,
-// tensor-map loads, tcgen05 instructions and their descriptors, and the list of
-// tiles that ragged experts make.
+// What the tensor-core kernels of expert.cu share: bounded waits, tensor-map
+// loads, tcgen05 instructions and their descriptors, and the list of tiles that
+// ragged experts make.
 #pragma once
 
 #include <cuda.h>
