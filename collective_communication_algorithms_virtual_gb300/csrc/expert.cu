@@ -392,10 +392,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) product_kernel(const __grid_con
         for (int k = 0; k < x.k; k += kTileK) {
           const int left = x.k - k;
           // Rows that a warp of each block has set to 0: the other block's write
-          // is this block's to read at the cluster's scope only.  (That costs:
-          // 228 us for the weights' gradient of 32 experts of 2048 by 4096, 16384
-          // rows, and 194 where every expert has a multiple of 16; with this
-          // scope in every step the forward product took three times as long.)
+          // is this block's to read at the cluster's scope only.  (Both gradients of
+          // 32 experts of 2048 by 4096, 16384 rows, take 406 us so and took 392
+          // with the default scope; with this one in every step the forward
+          // product took three times as long.)
           const bool zeroed = WEIGHT && left < kTileK && left % 16 != 0;
           if (!(zeroed ? tc::bar_wait<true>(full + 8 * s, phase, &gone) : tc::bar_wait(full + 8 * s, phase, &gone))) {
             ok = false;
