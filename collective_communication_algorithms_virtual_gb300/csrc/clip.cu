@@ -4,7 +4,7 @@
 // The second walks the chunks in the opposite order, so that it begins on what
 // the first left in L2.  Memory bounds both.  On a GB300 (copy rate 6.78 TB/s):
 // 2.4 GB of bf16 gradients in 1536 tensors, 390 us for the norm (6.2 TB/s) and
-// 762 us for the clipping (6.3 TB/s); 34 MB in 64 tensors 24 us together.
+// 740 us for the clipping (6.5 TB/s); 34 MB in 64 tensors 24 us together.
 #include <iterator>
 #include <memory>
 
@@ -16,9 +16,9 @@ namespace {
 
 constexpr int kClipThreads = 256, kClipUnits = 8;
 // Blocks of a multiprocessor, by their registers.  24 layers' 2.4 GB, eight
-// ranks: clipping 749 us with 3 and 860 with 4 (which spills); the norm has 4
-// (400 us, and 419 with 3).
-constexpr int kClipBlocks = 3;
+// ranks: the norm 400 us with 4 and 419 with 3 (what its loads need), clipping
+// 749 with 3 and 860 with 4 (which spills).
+constexpr int kNormBlocks = 4, kClipBlocks = 3;
 constexpr int64_t kChunkBytes = int64_t(kClipThreads) * kClipUnits * 16;  // of one tensor, at most, at a time
 
 struct Tensor {
@@ -45,6 +45,13 @@ struct ClipParams : ClipCall {
   uint8_t dtype[N];
 };
 constexpr int kFew = 96, kMany = 768;
+// Above this many bytes a clipping call's blocks do not come in before the launch
+// ahead has ended.  Behind a clipping launch that costs more than the launch's
+// latency that it hides: calls one after another, 8 ranks of 96 tensors, 131 us
+// with blocks that come in early and 118 without for 128 MB, 199 and 175 for 256
+// MB (8 tensors: 143 and 136), but 24.7 and 29.2 for 32 MB of 8 tensors.  The
+// norm alone is faster with them at every size (43 and 50 us for 128 MB).
+constexpr int64_t kLateBytes = 64 << 20;
 
 // A chunk: `n` elements at g and out.
 struct Chunk {
@@ -178,7 +185,7 @@ __device__ __forceinline__ double squares(const Chunk& x, B&& between) {
       sum += all;
       continue;
     }
-    if constexpr (VEC) {  // zeros are common: 2.4 GB of them take 405 us so, 609 added again
+    if constexpr (VEC) {  // zeros are common: 2.4 GB of them take 403 us so, 609 added again
       constexpr uint32_t kMagnitude = E::kSize == 4 ? 0x7fffffff : 0x7fff7fff;
       uint32_t any = 0;
 #pragma unroll
@@ -190,11 +197,8 @@ __device__ __forceinline__ double squares(const Chunk& x, B&& between) {
   return sum;
 }
 
-// 56 registers: four blocks leave room for the clipping's first block as soon as
-// one of them ends.  With 62 the same two kernels took 1186 us instead of 1161
-// (2.4 GB of bf16), the norm alone as long (fp32: 351 for 341).
 template <class P>
-__global__ void __maxnreg__(56) grad_norm_kernel(const __grid_constant__ P p) {
+__global__ void __launch_bounds__(kClipThreads, kNormBlocks) grad_norm_kernel(const __grid_constant__ P p) {
   __shared__ double part[kClipThreads / 32];
   stream_order();
   const int rank = blockIdx.y;
@@ -369,6 +373,7 @@ vc_status_t clip_with(const void* const* g, void* const* out, const size_t* coun
   }
   if (e != cudaSuccess) return cuda_fail(e, "cudaMallocFromPoolAsync");
   const unsigned n = static_cast<unsigned>(nranks);
+  const bool early = !out || bytes <= kLateBytes;
   int step = 0;
   for (uint32_t i = 0; i < launches && rc == VC_SUCCESS; ++i) {
     P& p = *tables[i];
@@ -378,13 +383,13 @@ vc_status_t clip_with(const void* const* g, void* const* out, const size_t* coun
     p.at = i;
     p.across = across != 0;
     p.max_norm = static_cast<float>(max_norm);
-    rc = launch<grad_norm_kernel<P>>(dev, Shape{blocks, kClipThreads, 0, 1, n}, stream, p, kGradNorm, step++, i == 0 ? bytes : 0);
+    rc = launch<grad_norm_kernel<P>>(dev, Shape{blocks, kClipThreads, 0, 1, n, early}, stream, p, kGradNorm, step++, i == 0 ? bytes : 0);
   }
   if (rc == VC_SUCCESS && !out)
     rc = launch<norm_kernel, ClipCall>(dev, Shape{n, kClipThreads}, stream, *tables[0], kGradNorm, step++, static_cast<int64_t>(need));
   // the last table first: its gradients are the ones left in L2
   for (uint32_t i = launches; out && i-- > 0 && rc == VC_SUCCESS;)
-    rc = launch<clip_kernel<P>>(dev, Shape{clip_blocks, kClipThreads, 0, 1, n}, stream, *tables[i], kClip, step++, i == 0 ? 2 * bytes : 0);
+    rc = launch<clip_kernel<P>>(dev, Shape{clip_blocks, kClipThreads, 0, 1, n, early}, stream, *tables[i], kClip, step++, i == 0 ? 2 * bytes : 0);
   e = cudaFreeAsync(part, stream);
   if (e != cudaSuccess && rc == VC_SUCCESS) rc = cuda_fail(e, "cudaFreeAsync");
   return rc;

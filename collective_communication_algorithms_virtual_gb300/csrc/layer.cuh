@@ -175,6 +175,7 @@ struct Shape {
   size_t smem = 0;
   unsigned cluster = 1;
   unsigned ranks = 1;  // the grid's second dimension, where blocks belong to ranks
+  bool early = true;   // its blocks may come in before the launch ahead has ended (stream_order)
 };
 
 // One launch of kernel K with its parameter block; `what`, `step` and `bytes`
@@ -191,7 +192,7 @@ vc_status_t launch(int dev, const Shape& s, cudaStream_t stream, const P& p, Ker
   cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
   cfg.numAttrs = 0;
-  if (pdl_enabled()) {
+  if (s.early && pdl_enabled()) {
     attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
   }
